@@ -31,6 +31,11 @@ STATUS_CU_SEQLENS = 1
 STATUS_CHECKPOINT_STARTS = 2
 STATUS_STATE_INDEX = 4
 STATUS_CHUNK_CAPACITY = 8
+STATUS_POOL_ROW = 16
+STATUS_POOL_DUPLICATE = 32
+STATUS_POOL_OVERLAP = 64
+RECURRENCE_CHUNK = 64
+POOL_MAX_ROWS = 262144
 
 # every symbol include/gdn_prefill.h declares
 EXPORTS = [
@@ -38,6 +43,9 @@ EXPORTS = [
     "gdn_prefill_workspace_size", "gdn_validate_host", "gdn_prefill",
     "gdn_prefill_timed", "gdn_build_chunk_indices", "gdn_decode",
     "gdn_validate_decode_host", "gdn_prefill_noalloc",
+    "gdn_recurrence_workspace_size", "gdn_validate_recurrence_host", "gdn_recurrence",
+    "gdn_recurrence_backward", "gdn_recurrence_decode", "gdn_validate_pool_host",
+    "gdn_pool_copy", "gdn_pool_reset", "gdn_pool_compact",
 ]
 
 _i64x4 = ctypes.c_int64 * 4
@@ -88,6 +96,67 @@ class Params(ctypes.Structure):
     ]
 
 
+class RecurrenceParams(ctypes.Structure):
+    _fields_ = [
+        ("total_tokens", ctypes.c_int64),
+        ("num_seqs", ctypes.c_int32),
+        ("num_heads", ctypes.c_int32),
+        ("head_size", ctypes.c_int32),
+        ("x_dtype", ctypes.c_int32),
+        ("g_dtype", ctypes.c_int32),
+        ("g_per_head", ctypes.c_int32),
+        ("x", ctypes.c_void_p),
+        ("g", ctypes.c_void_p),
+        ("x_stride", ctypes.c_int64),
+        ("g_stride", ctypes.c_int64),
+        ("cu_seqlens", ctypes.c_void_p),
+        ("cu_seqlens_type", ctypes.c_int32),
+        ("output", ctypes.c_void_p),
+        ("initial_state", ctypes.c_void_p),
+        ("initial_state_dtype", ctypes.c_int32),
+        ("initial_state_stride", ctypes.c_int64),
+        ("output_final_state", ctypes.c_int32),
+        ("output_state", ctypes.c_void_p),
+        ("output_state_dtype", ctypes.c_int32),
+        ("output_state_stride", ctypes.c_int64),
+        ("state_indices", ctypes.c_void_p),
+        ("state_indices_type", ctypes.c_int32),
+        ("pool_size", ctypes.c_int64),
+        ("chunk_states", ctypes.c_void_p),
+        ("doutput", ctypes.c_void_p),
+        ("doutput_stride", ctypes.c_int64),
+        ("dfinal_state", ctypes.c_void_p),
+        ("dx", ctypes.c_void_p),
+        ("dg", ctypes.c_void_p),
+        ("dinitial_state", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+        ("status", ctypes.c_void_p),
+    ]
+
+
+_i64x3 = ctypes.c_int64 * 3
+
+
+class PoolParams(ctypes.Structure):
+    _fields_ = [
+        ("extent", _i64x3),
+        ("src", ctypes.c_void_p),
+        ("src_dtype", ctypes.c_int32),
+        ("src_pool_rows", ctypes.c_int64),
+        ("src_strides", _i64x4),
+        ("dst", ctypes.c_void_p),
+        ("dst_dtype", ctypes.c_int32),
+        ("dst_pool_rows", ctypes.c_int64),
+        ("dst_strides", _i64x4),
+        ("src_rows", ctypes.c_void_p),
+        ("dst_rows", ctypes.c_void_p),
+        ("rows_type", ctypes.c_int32),
+        ("count", ctypes.c_int64),
+        ("status", ctypes.c_void_p),
+    ]
+
+
 _lib = None
 
 
@@ -129,6 +198,22 @@ def lib():
             ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_int64,
             ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
             ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]
+        rec, pool = ctypes.POINTER(RecurrenceParams), ctypes.POINTER(PoolParams)
+        L.gdn_recurrence_workspace_size.restype = ctypes.c_size_t
+        L.gdn_recurrence_workspace_size.argtypes = [rec, ctypes.c_int32]
+        L.gdn_validate_recurrence_host.restype = ctypes.c_int
+        L.gdn_validate_recurrence_host.argtypes = [rec, ctypes.c_int32]
+        for name in ("gdn_recurrence", "gdn_recurrence_backward", "gdn_recurrence_decode"):
+            getattr(L, name).restype = ctypes.c_int
+            getattr(L, name).argtypes = [rec, ctypes.c_void_p]
+        L.gdn_validate_pool_host.restype = ctypes.c_int
+        L.gdn_validate_pool_host.argtypes = [pool, ctypes.c_int32]
+        for name in ("gdn_pool_copy", "gdn_pool_reset"):
+            getattr(L, name).restype = ctypes.c_int
+            getattr(L, name).argtypes = [pool, ctypes.c_void_p]
+        L.gdn_pool_compact.restype = ctypes.c_int
+        L.gdn_pool_compact.argtypes = [pool, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                       ctypes.c_void_p]
         _lib = L
     return _lib
 

@@ -16,6 +16,7 @@
 
 #include "../../include/gdn_prefill.h"
 #include "gdn_internal.h"
+#include "gdn_recurrence.h"
 
 using namespace gdn;
 
@@ -171,9 +172,11 @@ bool io_aligned(const gdn_prefill_params *p) {
   return true;
 }
 
+}  // namespace
+
 // Checks that the current device is a gfx950 and reports its CU count
 // (cached per device).
-int check_device(int *num_cus = nullptr) {
+int gdn::check_device(int *num_cus) {
   static std::mutex mu;
   static int cached[64];
   static int cus[64];
@@ -195,8 +198,6 @@ int check_device(int *num_cus = nullptr) {
   if (num_cus) *num_cus = cus[dev];
   return cached[dev] == 1 ? GDN_OK : GDN_ERR_DEVICE;
 }
-
-}  // namespace
 
 extern "C" {
 
@@ -223,6 +224,9 @@ const char *gdn_status_string(int code) {
     case (int)GDN_STATUS_CHECKPOINT_STARTS: return "status: checkpoint_cu_starts differs from the prefix sum of floor(len / n)";
     case (int)GDN_STATUS_STATE_INDEX: return "status: a state index is outside [0, pool_size)";
     case (int)GDN_STATUS_CHUNK_CAPACITY: return "status: chunk table capacity exceeded";
+    case (int)GDN_STATUS_POOL_ROW: return "status: a pool row index is outside its pool";
+    case (int)GDN_STATUS_POOL_DUPLICATE: return "status: a destination row is named twice (the last entry won)";
+    case (int)GDN_STATUS_POOL_OVERLAP: return "status: a source row is another entry's destination (that entry was skipped)";
     default: return "unknown code";
   }
 }

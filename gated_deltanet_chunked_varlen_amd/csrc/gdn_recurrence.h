@@ -1,0 +1,92 @@
+// gdn_recurrence.h -- argument blocks and launchers of the gated linear
+// recurrence and of the state-pool row operators.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/gdn_prefill.h"
+
+namespace gdn {
+
+// GDN_OK if the current device is a gfx950; reports its CU count (gdn_host.hip).
+int check_device(int *num_cus = nullptr);
+
+// Tokens of one workgroup's tile in the recurrence scans.
+constexpr int kRecTile = 64;
+// Channels of one workgroup's tile: 64 lanes x 4.
+constexpr int kRecChannels = 256;
+
+struct RecArgs {
+  int64_t T;
+  int32_t N, H, D, C;  // C = H * D channels
+  int32_t x_dtype, g_dtype, g_per_head;
+  const void *x, *g;
+  int64_t x_stride, g_stride;  // elements per token
+  void *out;
+  const void *cu;
+  int32_t cu_type;
+  const int32_t *bos;  // sanitised sequence starts [N + 1]; NULL: N <= 63, from cu
+  const void *init;    // states: element type and row stride
+  int32_t init_dtype;
+  int64_t init_stride;
+  void *fin;
+  int32_t fin_dtype;
+  int64_t fin_stride;
+  const void *sidx;
+  int32_t sidx_type;
+  int64_t pool_rows;
+  float *chunk;  // [ceil(T / 64)][C] state before each tile, or NULL
+  // backward
+  const void *dy;
+  int64_t dy_stride;
+  const float *dfin;
+  void *dx, *dg;
+  float *dinit;
+  // tiles and their chain
+  int32_t ntiles, ncb;
+  uint32_t units;             // ntiles * ncb
+  uint32_t *ticket;           // next unit to take; NULL: one tile, unit = blockIdx.x
+  unsigned long long *words;  // [ntiles][C]
+  int32_t *status;
+  int32_t vec;  // every row of x, g, dy, out, dx, dg is a whole number of aligned 4-element groups
+  int32_t num_cus;
+};
+
+// Clears the chain's words and ticket, and for N > 63 forms bos and the status.
+hipError_t launch_rec_prepare(const RecArgs &a, int32_t *bos, hipStream_t s);
+hipError_t launch_rec_forward(const RecArgs &a, hipStream_t s);
+hipError_t launch_rec_backward(const RecArgs &a, hipStream_t s);
+hipError_t launch_rec_decode(const RecArgs &a, hipStream_t s);
+
+struct PoolArgs {
+  int64_t row;  // elements of a row
+  int64_t d2, d3;
+  const void *src;
+  int32_t src_dtype;
+  int64_t src_pool;
+  int64_t src_str[4];
+  void *dst;
+  int32_t dst_dtype;
+  int64_t dst_pool;
+  int64_t dst_str[4];
+  const void *src_rows, *dst_rows;
+  int32_t rows_type;
+  int64_t count;
+  int32_t *status;
+  int32_t same;  // src and dst are one view
+  // access: elements (or for equal types bytes) per thread and step, see k7_pool.hip
+  int32_t flat;   // both rows contiguous
+  int32_t align;  // largest power of two <= 16 that divides every row's address and length in bytes
+  // compact
+  void *new_rows;
+  int32_t *num_live;
+  int32_t *row_map;
+  int32_t num_cus;
+};
+
+hipError_t launch_pool_copy(const PoolArgs &a, hipStream_t s);
+hipError_t launch_pool_reset(const PoolArgs &a, hipStream_t s);
+hipError_t launch_pool_compact(const PoolArgs &a, hipStream_t s);
+
+}  // namespace gdn

@@ -1,0 +1,419 @@
+// k7_pool.hip -- rows of a state pool: copied (forked, moved, brought in from
+// another pool or type), zeroed, compacted.
+//
+// A row of a gated-delta pool is H x V x K elements (1 MB at 16 heads of 128 x
+// 128 fp32), one of a recurrence pool H x D (8 KB at 16 x 128), so the work is
+// cut into units of about kUnitBytes: a slice of one long row, or several
+// short rows.  Bounded by HBM (each byte moved once each way) for long rows
+// and by launch latency for a few short ones; every call is one kernel.
+//
+// Row lists live on the device, so who copies what is settled there: each
+// workgroup reads the whole list for its own entries (a few thousand 4-byte
+// words from L2) instead of waiting for a planning kernel.
+#include "gdn_common.h"
+#include "gdn_internal.h"
+#include "gdn_recurrence.h"
+
+namespace gdn {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int64_t kUnitBytes = 64 << 10;
+constexpr int kMaxGroup = 16;  // short rows per unit
+
+// Row numbers: the list entry, -1 for padding, -2 for entries outside the pool.
+__device__ __forceinline__ int list_row(const void *list, int type, int64_t i, int64_t pool) {
+  const int64_t r = load_index_any(list, type, i);
+  return r == -1 ? -1 : (r < 0 || r >= pool) ? -2 : (int)r;
+}
+
+// ------------------------------------------------------------ moving elements
+
+// Elements e0 .. e1 - 1 of a row (in the order d1, d2, d3), by the whole
+// workgroup.  src NULL: zeros.
+struct RowMover {
+  const PoolArgs &a;
+
+  __device__ __forceinline__ static int64_t offset(const int64_t *str, int64_t d2, int64_t d3,
+                                                   int64_t e) {
+    const int64_t k = e % d3, r = e / d3;
+    return (r / d2) * str[1] + (r % d2) * str[2] + k * str[3];
+  }
+
+  // contiguous rows of equal type: whole vectors, bit for bit
+  template <typename V>
+  __device__ __forceinline__ static void raw(const char *src, char *dst, int64_t b0, int64_t b1) {
+    constexpr int64_t W = sizeof(V);
+    const V zero{};
+    int64_t b = b0 + W * threadIdx.x;
+    constexpr int64_t step = W * kThreads;
+    for (; b + 7 * step < b1; b += 8 * step) {
+      V v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = src ? *(const V *)(src + b + i * step) : zero;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) *(V *)(dst + b + i * step) = v[i];
+    }
+    for (; b < b1; b += step) *(V *)(dst + b) = src ? *(const V *)(src + b) : zero;
+  }
+
+  template <typename S, typename D>
+  __device__ __forceinline__ void strided(const S *src, D *dst, int64_t e0, int64_t e1) const {
+    for (int64_t e = e0 + threadIdx.x; e < e1; e += kThreads)
+      dst[offset(a.dst_str, a.d2, a.d3, e)] =
+          src ? from_f32<D>(to_f32(src[offset(a.src_str, a.d2, a.d3, e)])) : from_f32<D>(0.f);
+  }
+  // equal types, strided: the bits
+  template <typename U>
+  __device__ __forceinline__ void strided_raw(const U *src, U *dst, int64_t e0, int64_t e1) const {
+    for (int64_t e = e0 + threadIdx.x; e < e1; e += kThreads)
+      dst[offset(a.dst_str, a.d2, a.d3, e)] =
+          src ? src[offset(a.src_str, a.d2, a.d3, e)] : (U)0;
+  }
+
+  // contiguous rows of two types: eight elements per thread and step where
+  // every row allows it
+  template <typename S, typename D>
+  __device__ __forceinline__ void convert(const S *src, D *dst, int64_t e0, int64_t e1) const {
+    if (!a.flat) return strided(src, dst, e0, e1);
+    int64_t e = e0;
+    if (a.align >= 16) {
+      const int64_t n8 = (e1 - e0) / 8;
+      for (int64_t i = threadIdx.x; i < n8; i += kThreads) {
+        S s[8];
+        D d[8];
+        __builtin_memcpy(s, __builtin_assume_aligned(src + e0 + 8 * i, sizeof(S) * 8 < 16 ? 8 : 16),
+                         sizeof(s));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[j] = from_f32<D>(to_f32(s[j]));
+        __builtin_memcpy(__builtin_assume_aligned(dst + e0 + 8 * i, sizeof(D) * 8 < 16 ? 8 : 16), d,
+                         sizeof(d));
+      }
+      e = e0 + 8 * n8;
+    }
+    for (e += threadIdx.x; e < e1; e += kThreads) dst[e] = from_f32<D>(to_f32(src[e]));
+  }
+
+  template <typename S>
+  __device__ __forceinline__ void from(const S *src, char *dst, int64_t e0, int64_t e1) const {
+    switch (a.dst_dtype) {
+      case GDN_F32: return convert(src, (float *)dst, e0, e1);
+      case GDN_BF16: return convert(src, (bf16 *)dst, e0, e1);
+      case GDN_F16: return convert(src, (f16 *)dst, e0, e1);
+      case GDN_FP8_E4M3: return convert(src, (fp8e4m3 *)dst, e0, e1);
+      default: return convert(src, (fp8e5m2 *)dst, e0, e1);
+    }
+  }
+
+  __device__ __forceinline__ static int size(int dtype) {
+    return dtype == GDN_F32 ? 4 : dtype == GDN_BF16 || dtype == GDN_F16 ? 2 : 1;
+  }
+
+  // s < 0: zeros
+  __device__ __forceinline__ void move(int s, int d, int64_t e0, int64_t e1) const {
+    const int ds = size(a.dst_dtype);
+    const char *src =
+        s < 0 ? nullptr : (const char *)a.src + (int64_t)s * a.src_str[0] * size(a.src_dtype);
+    char *dst = (char *)a.dst + (int64_t)d * a.dst_str[0] * ds;
+    if (!src || a.src_dtype == a.dst_dtype) {
+      if (!a.flat) {
+        if (ds == 4) strided_raw((const uint32_t *)src, (uint32_t *)dst, e0, e1);
+        else if (ds == 2) strided_raw((const uint16_t *)src, (uint16_t *)dst, e0, e1);
+        else strided_raw((const uint8_t *)src, (uint8_t *)dst, e0, e1);
+      } else if (a.align >= 16) {
+        raw<u32x4>(src, dst, e0 * ds, e1 * ds);
+      } else if (ds == 4) {
+        raw<uint32_t>(src, dst, e0 * ds, e1 * ds);
+      } else if (ds == 2) {
+        raw<uint16_t>(src, dst, e0 * ds, e1 * ds);
+      } else {
+        raw<uint8_t>(src, dst, e0 * ds, e1 * ds);
+      }
+      return;
+    }
+    switch (a.src_dtype) {
+      case GDN_F32: return from((const float *)src, dst, e0, e1);
+      case GDN_BF16: return from((const bf16 *)src, dst, e0, e1);
+      case GDN_F16: return from((const f16 *)src, dst, e0, e1);
+      case GDN_FP8_E4M3: return from((const fp8e4m3 *)src, dst, e0, e1);
+      default: return from((const fp8e5m2 *)src, dst, e0, e1);
+    }
+  }
+};
+
+// Units of a call: `group` entries by one slice of `slice` elements each.
+struct Units {
+  int group;
+  int64_t slice, slices, groups;
+  int64_t total;  // groups * slices
+};
+
+Units cut(const PoolArgs &a, int64_t entries) {
+  const int64_t big = a.src ? (a.src_dtype == GDN_F32 ? 4 : a.src_dtype <= GDN_F16 ? 2 : 1) : 0;
+  const int64_t ds = a.dst_dtype == GDN_F32 ? 4 : a.dst_dtype <= GDN_F16 ? 2 : 1;
+  const int64_t es = big > ds ? big : ds;
+  Units u;
+  // slices of whole 16-byte groups in any type: multiples of 16 elements
+  u.slice = kUnitBytes / es;
+  if (u.slice >= a.row) {
+    u.slice = a.row;
+    const int64_t fit = kUnitBytes / (a.row * es);
+    // no fewer units than two per compute unit for the sake of larger ones
+    const int64_t spread = entries / (2 * (int64_t)a.num_cus);
+    int64_t g = fit < spread ? fit : spread;
+    u.group = (int)(g < 1 ? 1 : g > kMaxGroup ? kMaxGroup : g);
+  } else {
+    u.group = 1;
+  }
+  u.slices = (a.row + u.slice - 1) / u.slice;
+  u.groups = (entries + u.group - 1) / u.group;
+  u.total = u.groups * u.slices;
+  return u;
+}
+
+unsigned unit_grid(const PoolArgs &a, const Units &u) {
+  const int64_t most = 16 * (int64_t)a.num_cus;
+  return (unsigned)(u.total < most ? u.total : most);
+}
+
+// ---------------------------------------------------------------- copy, reset
+
+// The status word of a list, by one workgroup of its own: out-of-range
+// entries, destinations named twice, sources that another entry overwrites.
+__device__ __forceinline__ void list_status(const PoolArgs &a, unsigned *map) {
+  __shared__ unsigned s_bits;
+  const int words = (int)((a.dst_pool + 31) / 32);
+  for (int i = threadIdx.x; i < words; i += kThreads) map[i] = 0u;
+  if (threadIdx.x == 0) s_bits = 0u;
+  __syncthreads();
+  unsigned bits = 0;
+  for (int64_t i = threadIdx.x; i < a.count; i += kThreads) {
+    const int d = list_row(a.dst_rows, a.rows_type, i, a.dst_pool);
+    const int s = a.src ? list_row(a.src_rows, a.rows_type, i, a.src_pool) : 0;
+    if (d == -2 || s == -2) bits |= GDN_STATUS_POOL_ROW;
+    // zeroing a row twice is no conflict
+    if (d >= 0 && s >= 0 && a.src && (atomicOr(&map[d >> 5], 1u << (d & 31)) >> (d & 31) & 1))
+      bits |= GDN_STATUS_POOL_DUPLICATE;
+  }
+  __syncthreads();
+  if (a.same) {
+    for (int64_t i = threadIdx.x; i < a.count; i += kThreads) {
+      const int d = list_row(a.dst_rows, a.rows_type, i, a.dst_pool);
+      const int s = list_row(a.src_rows, a.rows_type, i, a.src_pool);
+      if (d >= 0 && s >= 0 && s != d && s < a.dst_pool && (map[s >> 5] >> (s & 31) & 1))
+        bits |= GDN_STATUS_POOL_OVERLAP;
+    }
+  }
+  if (bits) atomicOr(&s_bits, bits);
+  __syncthreads();
+  if (threadIdx.x == 0) a.status[0] = (int32_t)s_bits;
+}
+
+// Which entries act: entry i is skipped if a later entry has its destination,
+// or (in one pool) if another entry's destination is its source.  Entries with
+// a row outside its pool take no part.
+template <bool ZERO>
+__global__ void __launch_bounds__(kThreads) pool_copy_kernel(PoolArgs a, Units u) {
+  extern __shared__ unsigned map[];
+  if (a.status && blockIdx.x == gridDim.x - 1) return list_status(a, map);
+  const int64_t workers = (int64_t)gridDim.x - (a.status ? 1 : 0);
+  __shared__ int s_src[kMaxGroup], s_dst[kMaxGroup], s_skip[kMaxGroup];
+  const RowMover m{a};
+  int64_t seen = -1;
+  for (int64_t unit = blockIdx.x; unit < u.total; unit += workers) {
+    const int64_t grp = unit / u.slices, e0 = (unit % u.slices) * u.slice;
+    const int64_t e1 = e0 + u.slice < a.row ? e0 + u.slice : a.row;
+    const int64_t i0 = grp * u.group;
+    const int n = (int)(a.count - i0 < u.group ? a.count - i0 : u.group);
+    if (grp != seen) {
+      seen = grp;
+      __syncthreads();
+      if ((int)threadIdx.x < n) {
+        const int d = list_row(a.dst_rows, a.rows_type, i0 + threadIdx.x, a.dst_pool);
+        const int s = ZERO ? 0 : list_row(a.src_rows, a.rows_type, i0 + threadIdx.x, a.src_pool);
+        s_src[threadIdx.x] = s;
+        s_dst[threadIdx.x] = d;
+        s_skip[threadIdx.x] = d < 0 || s < 0;
+      }
+      __syncthreads();
+      if (!ZERO) {
+        for (int64_t j = threadIdx.x; j < a.count; j += kThreads) {
+          const int d = list_row(a.dst_rows, a.rows_type, j, a.dst_pool);
+          const int s = list_row(a.src_rows, a.rows_type, j, a.src_pool);
+          if (d < 0 || s < 0) continue;
+          for (int p = 0; p < n; ++p) {
+            const bool later = j > i0 + p && d == s_dst[p];
+            const bool over = a.same && j != i0 + p && d == s_src[p] && s_src[p] != s_dst[p];
+            if (later || over) s_skip[p] = 1;
+          }
+        }
+        __syncthreads();
+      }
+    }
+    for (int p = 0; p < n; ++p)
+      if (!s_skip[p]) m.move(ZERO ? -1 : s_src[p], s_dst[p], e0, e1);
+  }
+}
+
+// -------------------------------------------------------------------- compact
+
+// Exclusive prefix sum over the workgroup of one value per thread; total in sh[0].
+__device__ __forceinline__ int block_prefix(int x, int *sh) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int inc = wave_prefix_sum_i(x);
+  __syncthreads();
+  if (lane == 63) sh[1 + wave] = inc;
+  __syncthreads();
+  int pre = 0, total = 0;
+  for (int w = 0; w < kThreads / 64; ++w) {
+    if (w < wave) pre += sh[1 + w];
+    total += sh[1 + w];
+  }
+  if (threadIdx.x == 0) sh[0] = total;
+  __syncthreads();
+  return pre + inc - x;
+}
+
+// Position of the k-th set bit of x (k < popcount).
+__device__ __forceinline__ int nth_bit(unsigned x, int k) {
+  for (; k > 0; --k) x &= x - 1;
+  return __ffs((int)x) - 1;
+}
+
+// Every workgroup forms the plan for itself in LDS: a bitmap of the live rows
+// and, per 32-row word, how many rows before it are live behind the new end
+// (movers) or free before it (holes).  The k-th mover and the k-th hole then
+// are two searches.  One launch, and nothing to hand over between workgroups.
+__global__ void __launch_bounds__(kThreads) pool_compact_kernel(PoolArgs a, Units u, int nwords) {
+  extern __shared__ unsigned map[];  // live bits
+  int *movers = (int *)(map + nwords), *holes = movers + nwords;
+  __shared__ int sh[1 + kThreads / 64];
+  __shared__ int s_src[kMaxGroup], s_dst[kMaxGroup];
+  __shared__ unsigned s_bits;
+  const int tid = threadIdx.x;
+  for (int i = tid; i < nwords; i += kThreads) map[i] = 0u;
+  if (tid == 0) s_bits = 0u;
+  __syncthreads();
+  for (int64_t i = tid; i < a.count; i += kThreads) {
+    const int r = list_row(a.dst_rows, a.rows_type, i, a.dst_pool);
+    if (r >= 0) atomicOr(&map[r >> 5], 1u << (r & 31));
+    else if (r == -2) atomicOr(&s_bits, GDN_STATUS_POOL_ROW);
+  }
+  __syncthreads();
+  // a thread owns `per` consecutive words
+  const int per = (nwords + kThreads - 1) / kThreads;
+  const int w0 = min(tid * per, nwords), w1 = min(w0 + per, nwords);
+  int n = 0;
+  for (int w = w0; w < w1; ++w) n += __popc(map[w]);
+  block_prefix(n, sh);
+  const int m = sh[0];
+  auto before = [&](int w) -> unsigned {  // the word's bits of rows before m
+    const int k = m - 32 * w;
+    return k >= 32 ? ~0u : k <= 0 ? 0u : (1u << k) - 1u;
+  };
+  int nm = 0, nh = 0;
+  for (int w = w0; w < w1; ++w) {
+    nm += __popc(map[w] & ~before(w));
+    nh += __popc(~map[w] & before(w));
+  }
+  int pm = block_prefix(nm, sh);
+  const int moves = sh[0];
+  int ph = block_prefix(nh, sh);
+  for (int w = w0; w < w1; ++w) {
+    movers[w] = pm;
+    holes[w] = ph;
+    pm += __popc(map[w] & ~before(w));
+    ph += __popc(~map[w] & before(w));
+  }
+  __syncthreads();
+  // last word whose count of earlier rows is <= k, and the row in it
+  auto word_of = [&](const int *pre, int k) {
+    int lo = 0, hi = nwords - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (pre[mid] <= k) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+  };
+  auto hole_row = [&](int k) {
+    const int w = word_of(holes, k);
+    return 32 * w + nth_bit(~map[w] & before(w), k - holes[w]);
+  };
+  auto mover_row = [&](int k) {
+    const int w = word_of(movers, k);
+    return 32 * w + nth_bit(map[w] & ~before(w), k - movers[w]);
+  };
+  auto place = [&](int r) {  // where live row r ends up
+    if (r < m) return r;
+    const int w = r >> 5;
+    return hole_row(movers[w] + __popc(map[w] & ~before(w) & ((1u << (r & 31)) - 1u)));
+  };
+
+  // renaming, spread over all workgroups
+  const int64_t gt = (int64_t)blockIdx.x * kThreads + tid, gn = (int64_t)gridDim.x * kThreads;
+  for (int64_t i = gt; i < a.count; i += gn) {
+    const int64_t raw = load_index_any(a.dst_rows, a.rows_type, i);
+    const int64_t r = raw >= 0 && raw < a.dst_pool ? (int64_t)place((int)raw) : raw;
+    if (a.rows_type == GDN_I64) ((int64_t *)a.new_rows)[i] = r;
+    else ((int32_t *)a.new_rows)[i] = (int32_t)r;
+  }
+  if (a.row_map)
+    for (int64_t r = gt; r < a.dst_pool; r += gn)
+      a.row_map[r] = map[r >> 5] >> (r & 31) & 1 ? place((int)r) : -1;
+  if (blockIdx.x == 0 && tid == 0) {
+    a.num_live[0] = m;
+    if (a.status) a.status[0] = (int32_t)s_bits;
+  }
+
+  const RowMover mv{a};
+  for (int64_t unit = blockIdx.x; unit < u.total; unit += gridDim.x) {
+    const int64_t grp = unit / u.slices, e0 = (unit % u.slices) * u.slice;
+    const int64_t e1 = e0 + u.slice < a.row ? e0 + u.slice : a.row;
+    const int64_t k0 = grp * u.group;
+    if (k0 >= moves) break;  // units of one group after another: none left
+    const int cnt = (int)(moves - k0 < u.group ? moves - k0 : u.group);
+    __syncthreads();
+    if (tid < cnt) {
+      s_src[tid] = mover_row((int)k0 + tid);
+      s_dst[tid] = hole_row((int)k0 + tid);
+    }
+    __syncthreads();
+    for (int p = 0; p < cnt; ++p) mv.move(s_src[p], s_dst[p], e0, e1);
+  }
+}
+
+}  // namespace
+
+static size_t status_map_bytes(const PoolArgs &a) {
+  return a.status ? (size_t)((a.dst_pool + 31) / 32) * 4 : 0;
+}
+
+template <bool ZERO>
+static hipError_t launch_list(const PoolArgs &a, hipStream_t s) {
+  const Units u = cut(a, a.count);
+  const unsigned grid = unit_grid(a, u) + (a.status ? 1u : 0u);
+  if (grid == 0) return hipSuccess;
+  pool_copy_kernel<ZERO><<<dim3(grid), dim3(kThreads), status_map_bytes(a), s>>>(a, u);
+  return hipGetLastError();
+}
+
+hipError_t launch_pool_copy(const PoolArgs &a, hipStream_t s) { return launch_list<false>(a, s); }
+hipError_t launch_pool_reset(const PoolArgs &a, hipStream_t s) { return launch_list<true>(a, s); }
+
+hipError_t launch_pool_compact(const PoolArgs &a, hipStream_t s) {
+  // a mover lies at or behind the new end and its hole before it
+  const int64_t entries = a.count < a.dst_pool / 2 ? a.count : a.dst_pool / 2;
+  const Units u = cut(a, entries);
+  const unsigned want = unit_grid(a, u);
+  const int nwords = (int)((a.dst_pool + 31) / 32);
+  const int lds = 12 * nwords;
+  static std::atomic<uint64_t> done{0};
+  const hipError_t e = set_dynamic_lds((const void *)pool_compact_kernel,
+                                       12 * (GDN_POOL_MAX_ROWS / 32), done);
+  if (e != hipSuccess) return e;
+  pool_compact_kernel<<<dim3(want ? want : 1u), dim3(kThreads), lds, s>>>(a, u, nwords);
+  return hipGetLastError();
+}
+
+}  // namespace gdn

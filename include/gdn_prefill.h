@@ -85,6 +85,9 @@ typedef enum { GDN_I32 = 0, GDN_I64 = 1 } gdn_itype;
 #define GDN_STATUS_CHECKPOINT_STARTS 2u /* checkpoint_cu_starts != prefix sum of floor(len/n) */
 #define GDN_STATUS_STATE_INDEX 4u       /* a state index outside [0, pool_size) */
 #define GDN_STATUS_CHUNK_CAPACITY 8u    /* more chunks than the sync-free bound (never expected) */
+#define GDN_STATUS_POOL_ROW 16u         /* a pool row index outside its pool (-1 is padding, not an error) */
+#define GDN_STATUS_POOL_DUPLICATE 32u   /* a destination row named twice (the last entry wins) */
+#define GDN_STATUS_POOL_OVERLAP 64u     /* a source row that another entry overwrites (that entry is skipped) */
 
 /*
  * Parameters of one prefill call (gitcode, section "API 全参数解析"; the
@@ -289,6 +292,158 @@ int gdn_build_chunk_indices(const void *cu_seqlens, int32_t cu_type,
                             int32_t *chunk_indices, int32_t *cu_chunks,
                             int32_t *seq_starts, int32_t *n_chunks,
                             int32_t *status, void *stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Gated linear recurrence: the diagonal sibling of the gated delta rule, over
+ * the same packed sequences and state pools.  For every sequence and every
+ * channel (h, d), with fp32 state,
+ *
+ *     h_t = g_t * h_{t-1} + x_t,      output_t = h_t
+ *
+ * from the given initial state (or zero).  g is the forget gate itself, in
+ * [0, 1] (a gate above 1 is computed, but the products of 64 consecutive
+ * gates must stay finite).
+ *
+ * Shapes: x, output, doutput, dx [T, H, D] in x_dtype (F32, BF16 or F16); g,
+ * dg [T, H, D], or [T, H] with g_per_head (one gate for the D channels of a
+ * head; D must then be 32, 64 or 128), in g_dtype: F32 or x_dtype.  H and D
+ * are any positive numbers.  A token's H * D (or H) values are contiguous;
+ * x, g and doutput have token strides in elements (0 = contiguous), every
+ * other tensor is contiguous.  States are [rows, H, D] in any state dtype
+ * with a row stride in elements (0 = contiguous); the 8-bit types saturate.
+ * cu_seqlens, num_seqs, state_indices, pool_size and status are those of
+ * gdn_prefill_params; output_state may be the same memory as initial_state.
+ * Rows of output outside every sequence are untouched.  An empty sequence's
+ * final state is its initial state.  A sequence whose state index is out of
+ * range starts from zero and writes no final state.
+ */
+#define GDN_RECURRENCE_CHUNK 64 /* tokens per row of chunk_states */
+
+typedef struct gdn_recurrence_params {
+  int64_t total_tokens;    /* T >= 0 */
+  int32_t num_seqs;        /* N >= 0; with cu_seqlens NULL, N must be 1 */
+  int32_t num_heads;       /* H >= 1 */
+  int32_t head_size;       /* D >= 1 */
+  int32_t x_dtype;         /* gdn_dtype: F32, BF16, F16 */
+  int32_t g_dtype;         /* F32 or x_dtype */
+  int32_t g_per_head;      /* 0: g [T, H, D]; 1: g [T, H] */
+  const void *x, *g;
+  int64_t x_stride, g_stride;
+  const void *cu_seqlens;  /* [N+1], NULL = one sequence [0, T] */
+  int32_t cu_seqlens_type;
+  void *output;
+  const void *initial_state;
+  int32_t initial_state_dtype;
+  int64_t initial_state_stride;
+  int32_t output_final_state;
+  void *output_state;
+  int32_t output_state_dtype;
+  int64_t output_state_stride;
+  const void *state_indices; /* [N] or NULL */
+  int32_t state_indices_type;
+  int64_t pool_size;
+  /* fp32 [ceil(T / 64), H, D] or NULL.  gdn_recurrence() writes the state
+   * before token 64 r into row r (rows whose first token starts a sequence or
+   * lies outside every sequence hold unspecified values);
+   * gdn_recurrence_backward() reads them, or forms them in its workspace at
+   * the cost of one more pass over x and g when NULL. */
+  float *chunk_states;
+  /* gradients, gdn_recurrence_backward() only */
+  const void *doutput;       /* [T, H, D] x_dtype */
+  int64_t doutput_stride;
+  const float *dfinal_state; /* [N, H, D] or NULL (zero) */
+  void *dx, *dg;
+  float *dinitial_state;     /* [N, H, D] or NULL (not formed) */
+  void *workspace;
+  size_t workspace_bytes;
+  int32_t *status;           /* optional device word */
+} gdn_recurrence_params;
+
+/* Bytes of workspace gdn_recurrence() (backward == 0) or
+ * gdn_recurrence_backward() (backward != 0) needs; only the shape fields and
+ * whether chunk_states is given are read.  Host only; 0 can be a valid
+ * answer: check the parameters with gdn_validate_recurrence_host(). */
+size_t gdn_recurrence_workspace_size(const gdn_recurrence_params *p, int32_t backward);
+
+/* The host-side checks of gdn_recurrence() (mode 0), its backward pass (1)
+ * and its decode step (2); no GPU needed. */
+int gdn_validate_recurrence_host(const gdn_recurrence_params *p, int32_t mode);
+
+/* The forward pass: at most two kernels on `stream`. */
+int gdn_recurrence(const gdn_recurrence_params *p, void *stream);
+
+/* The backward pass, from x, g, the initial state, doutput (d loss / d
+ * output) and dfinal_state (d loss / d final state):
+ *   dh_t = doutput_t + g_{t+1} dh_{t+1}   (last token: + dfinal_state)
+ *   dx_t = dh_t,  dg_t = dh_t h_{t-1}  (summed over D with g_per_head)
+ *   dinitial_state = g_first dh_first     (empty sequence: dfinal_state)
+ * The states are formed again in fp32 from x and g, so dg does not carry the
+ * rounding of output.  dx and dg rows outside every sequence are zero.
+ * state_indices must be NULL and output / output_state are ignored.  Results
+ * do not depend on the order in which workgroups run. */
+int gdn_recurrence_backward(const gdn_recurrence_params *p, void *stream);
+
+/* One decode step: token i of x, g, output [N, ...] is the new token of
+ * sequence i (total_tokens == num_seqs, cu_seqlens and chunk_states NULL).
+ * No workspace. */
+int gdn_recurrence_decode(const gdn_recurrence_params *p, void *stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Rows of a state pool.  A pool is [rows, d1, d2, d3] of any state dtype with
+ * four element strides (all zero = contiguous): the pools of gdn_prefill()
+ * ([rows, H, V, K]) and of gdn_recurrence() ([rows, 1, H, D]).  At most
+ * GDN_POOL_MAX_ROWS rows.  Row lists are device arrays (int32 or int64); an
+ * entry of -1 is padding.  Entries outside the pool are skipped and set
+ * GDN_STATUS_POOL_ROW.
+ */
+#define GDN_POOL_MAX_ROWS 262144
+
+typedef struct gdn_pool_params {
+  int64_t extent[3];        /* d1, d2, d3 >= 1 */
+  const void *src;          /* gdn_pool_copy(); NULL otherwise */
+  int32_t src_dtype;
+  int64_t src_pool_rows;
+  int64_t src_strides[4];
+  void *dst;
+  int32_t dst_dtype;
+  int64_t dst_pool_rows;
+  int64_t dst_strides[4];
+  const void *src_rows;     /* [count] */
+  const void *dst_rows;     /* [count] */
+  int32_t rows_type;        /* gdn_itype of both lists */
+  int64_t count;
+  int32_t *status;          /* optional device word */
+} gdn_pool_params;
+
+/* The host-side checks of gdn_pool_copy() (mode 0), gdn_pool_reset() (1) and
+ * gdn_pool_compact() (2). */
+int gdn_validate_pool_host(const gdn_pool_params *p, int32_t mode);
+
+/* dst[dst_rows[i]] = src[src_rows[i]] for every i: forking a row (one source,
+ * several destinations), moving rows, or bringing rows of another pool or a
+ * checkpoint buffer in, with conversion between state dtypes (to nearest; the
+ * 8-bit types saturate; equal types copy bit for bit).  src and dst may be
+ * the same view; other views may share no elements (GDN_ERR_STATE where the
+ * host can see that they do).  A destination named twice takes its last
+ * entry.  In one pool an entry whose source row is another entry's destination
+ * is skipped.  Both set their status bit. */
+int gdn_pool_copy(const gdn_pool_params *p, void *stream);
+
+/* dst[dst_rows[i]] = 0 (rows freed, or taken for a new sequence). */
+int gdn_pool_reset(const gdn_pool_params *p, void *stream);
+
+/* Moves the live rows of dst to its front.  dst_rows [count] names the live
+ * rows (a row may be named more than once).  With m distinct live rows, the
+ * k-th live row at or behind row m (ascending) is copied to the k-th row
+ * before m that is not live; new_rows [count] (same type, not overlapping
+ * dst_rows) receives dst_rows with the moved rows renamed, invalid entries
+ * as they are; num_live [1] (int32) receives m.  Rows at or behind m keep
+ * their bytes, so the call can be repeated.  row_map [dst_pool_rows] (int32,
+ * or NULL) receives each row's new place, -1 for rows that are not live. */
+int gdn_pool_compact(const gdn_pool_params *p, void *new_rows, int32_t *num_live,
+                     int32_t *row_map, void *stream);
 
 #ifdef __cplusplus
 }
