@@ -7,13 +7,15 @@ kernels, and without the built library or a gfx950 device the calls raise.
 """
 from __future__ import annotations
 
-import ctypes
+from ctypes import byref
 
 import torch
 
+from . import _launch
 from . import _native as nat
-from .api import (_QKV_DTYPES, _STATE_DTYPES, _check_dev, _index, _ptr, _raise,
-                  cached_workspace, state_tensor, workspace_tensor)
+from ._launch import Blocks, meta
+from .api import (_QKV_DTYPES, _STATE_DTYPES, _check_dev, _index, state_tensor,
+                  workspace_tensor)
 
 
 def _token_stride(name, t, inner):
@@ -71,7 +73,6 @@ def _base_params(x, g, cu_seqlens, decode, tensors):
     p.total_tokens, p.num_heads, p.head_size = T, H, D
     p.x_dtype, p.g_dtype = _QKV_DTYPES[x.dtype], _QKV_DTYPES[g.dtype]
     p.g_per_head = 1 if per_head else 0
-    p.x, p.g = _ptr(x), _ptr(g)
     p.x_stride = _token_stride("x", x, H * D)
     p.g_stride = _token_stride("g", g, H if per_head else H * D)
     if decode:
@@ -80,93 +81,130 @@ def _base_params(x, g, cu_seqlens, decode, tensors):
         p.cu_seqlens_type = _index("cu_seqlens", cu_seqlens)
         if cu_seqlens.numel() < 1:
             raise ValueError("cu_seqlens must hold at least one offset")
-        p.cu_seqlens = _ptr(cu_seqlens)
         p.num_seqs = cu_seqlens.numel() - 1
     else:
         p.num_seqs = 1
     return p
 
 
-def _status(p, status):
-    if status is not None:
-        if status.dtype != torch.int32 or status.numel() < 1:
-            raise ValueError("status must be an int32 tensor")
-        p.status = _ptr(status)
+def _status(status):
+    if status is not None and (status.dtype != torch.int32 or status.numel() < 1):
+        raise ValueError("status must be an int32 tensor")
 
 
 def _states(p, x, initial_state, output_final_state, output_state, state_indices):
-    """Initial, final and pool states of a forward or decode call; returns
-    (output_state, tensors to keep alive)."""
+    """Checks and fills in the initial, final and pool states of a forward or
+    decode call; returns (initial_state to read, rows of the final state)."""
     N, (_, H, D) = p.num_seqs, x.shape
     rows = N
     if state_indices is not None:
         p.state_indices_type = _index("state_indices", state_indices)
         if state_indices.numel() != N:
             raise ValueError("state_indices must hold %d rows" % N)
-        p.state_indices = _ptr(state_indices)
         pool = output_state if output_state is not None else initial_state
         if pool is None:
             raise ValueError("state_indices needs a state pool")
         p.pool_size = rows = pool.shape[0]
     if initial_state is not None:
         initial_state, stride = _rec_state("initial_state", initial_state, rows, H, D, False)
-        p.initial_state = _ptr(initial_state)
         p.initial_state_dtype = _STATE_DTYPES[initial_state.dtype]
         p.initial_state_stride = stride
     if output_final_state:
+        p.output_final_state = 1
         if output_state is None:
             if state_indices is not None:
                 raise ValueError("output_state (the pool) is required with state_indices")
-            output_state = torch.empty((N, H, D), dtype=torch.float32, device=x.device)
-        output_state, stride = _rec_state("output_state", output_state, rows, H, D, True)
-        p.output_final_state = 1
-        p.output_state = _ptr(output_state)
-        p.output_state_dtype = _STATE_DTYPES[output_state.dtype]
-        p.output_state_stride = stride
-    return output_state, initial_state
+            p.output_state_dtype, p.output_state_stride = nat.GDN_F32, H * D
+        else:
+            output_state, stride = _rec_state("output_state", output_state, rows, H, D, True)
+            p.output_state_dtype = _STATE_DTYPES[output_state.dtype]
+            p.output_state_stride = stride
+    return initial_state
 
 
-def _run(call, p, device, backward, workspace):
-    """Workspace and launch of a scan on the device's current stream."""
-    lib = nat.lib()
-    need = int(lib.gdn_recurrence_workspace_size(ctypes.byref(p), backward))
-    with torch.cuda.device(device):
-        stream = torch.cuda.current_stream(device).cuda_stream
-        if need > 0 or workspace is not None:
-            if workspace is not None:
-                workspace = workspace_tensor(workspace, device, need)
-            elif torch.cuda.is_current_stream_capturing():
-                # a graph keeps the address: memory of its own capture pool
-                workspace = torch.empty(need, dtype=torch.uint8, device=device)
-            else:
-                workspace = cached_workspace(device, stream, need)
-            p.workspace = ctypes.c_void_p(workspace.data_ptr())
-            p.workspace_bytes = workspace.numel()
-        rc = call(ctypes.byref(p), ctypes.c_void_p(stream))
-    if rc != 0:
-        _raise(rc)
+_forward_blocks = Blocks(nat.RecurrenceParams)
+_backward_blocks = Blocks(nat.RecurrenceParams)
+_decode_blocks = Blocks(nat.RecurrenceParams)
+
+
+def _memory(p, device, need, workspace):
+    """Puts the workspace of a scan into its parameter block; returns it."""
+    if workspace is not None:
+        workspace = workspace_tensor(workspace, device, need)
+    elif need > 0:
+        if torch.cuda.current_device() == device.index:
+            workspace = _launch.workspace(device, need)
+        else:
+            with torch.cuda.device(device):
+                workspace = _launch.workspace(device, need)
+    else:
+        return None
+    p.workspace, p.workspace_bytes = workspace.data_ptr(), workspace.numel()
+    return workspace
+
+
+def _new_like(x):
+    return torch.empty_like(x, memory_format=torch.contiguous_format)
 
 
 def _forward(x, g, initial_state, output_final_state, cu_seqlens, output, output_state,
-             state_indices, chunk_states, status, workspace):
-    p = _base_params(x, g, cu_seqlens, False, (
-        ("g", g), ("initial_state", initial_state), ("cu_seqlens", cu_seqlens),
-        ("output", output), ("output_state", output_state), ("state_indices", state_indices),
-        ("chunk_states", chunk_states), ("status", status)))
-    if output is None:
-        output = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+             state_indices, return_chunk_states, status, workspace):
+    """Returns (output, final state or None, chunk states or None)."""
+    try:
+        key = (x.shape, x.stride(), x.dtype, x.device, g.shape, g.stride(), g.dtype, g.device,
+               meta(initial_state), bool(output_final_state), meta(cu_seqlens), meta(output),
+               meta(output_state), meta(state_indices), meta(status), bool(return_chunk_states))
+        hit = _forward_blocks.get(key)
+    except AttributeError:
+        raise ValueError("x, g and the optional arguments must be tensors") from None
+    if hit is None:
+        p = _base_params(x, g, cu_seqlens, False, (
+            ("g", g), ("initial_state", initial_state), ("cu_seqlens", cu_seqlens),
+            ("output", output), ("output_state", output_state), ("state_indices", state_indices),
+            ("status", status)))
+        if output is not None:
+            _contiguous("output", output, x.shape, x.dtype)
+        _status(status)
+        used = _states(p, x, initial_state, output_final_state, output_state, state_indices)
+        need = _workspace_size(p, cu_seqlens, False)
+        if used is initial_state:
+            _forward_blocks.keep(key, p, need)
+        initial_state = used
     else:
-        _contiguous("output", output, x.shape, x.dtype)
-    p.output = _ptr(output)
-    output_state, keep = _states(p, x, initial_state, output_final_state, output_state,
-                                 state_indices)
-    if chunk_states is not None:
-        _contiguous("chunk_states", chunk_states, _chunk_shape(x), torch.float32)
-        p.chunk_states = _ptr(chunk_states)
-    _status(p, status)
-    _run(nat.lib().gdn_recurrence, p, x.device, 0, workspace)
-    del keep
-    return output, output_state
+        p, need = hit
+    if output is None:
+        output = _new_like(x)
+    p.x, p.g, p.output = x.data_ptr(), g.data_ptr(), output.data_ptr()
+    if cu_seqlens is not None:
+        p.cu_seqlens = cu_seqlens.data_ptr()
+    if initial_state is not None:
+        p.initial_state = initial_state.data_ptr()
+    if output_final_state:
+        if output_state is None:
+            output_state = torch.empty((p.num_seqs,) + x.shape[1:], dtype=torch.float32,
+                                       device=x.device)
+        p.output_state = output_state.data_ptr()
+    if state_indices is not None:
+        p.state_indices = state_indices.data_ptr()
+    kept = None
+    if return_chunk_states:
+        kept = torch.empty(_chunk_shape(x), dtype=torch.float32, device=x.device)
+        p.chunk_states = kept.data_ptr()
+    if status is not None:
+        p.status = status.data_ptr()
+    memory = _memory(p, x.device, need, workspace)
+    _launch.call(nat.lib().gdn_recurrence, x.device, byref(p))
+    del memory
+    return output, (output_state if output_final_state else None), kept
+
+
+def _workspace_size(p, cu_seqlens, backward):
+    """Workspace of a scan whose block has no addresses yet (the library looks
+    only at which of them are there)."""
+    p.cu_seqlens = None if cu_seqlens is None else cu_seqlens.data_ptr()
+    need = int(nat.lib().gdn_recurrence_workspace_size(byref(p), int(backward)))
+    p.cu_seqlens = None
+    return need
 
 
 def _chunk_shape(x):
@@ -179,9 +217,8 @@ class _Recurrence(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, g, initial_state, cu_seqlens, output_final_state):
-        kept = torch.empty(_chunk_shape(x), dtype=torch.float32, device=x.device)
-        out, final = _forward(x, g, initial_state, output_final_state, cu_seqlens, None, None,
-                              None, kept, None, None)
+        out, final, kept = _forward(x, g, initial_state, output_final_state, cu_seqlens, None,
+                                    None, None, True, None, None)
         ctx.save_for_backward(x, g, initial_state, cu_seqlens, kept)
         ctx.with_final = output_final_state
         return (out, final) if output_final_state else out
@@ -244,16 +281,11 @@ def gated_linear_recurrence(x, g, initial_state=None, output_final_state=False, 
                                "a graph; use torch.no_grad() and "
                                "gated_linear_recurrence_backward")
         return _Recurrence.apply(x, g, initial_state, cu_seqlens, bool(output_final_state))
-    kept = None
-    if return_chunk_states:
-        if not (isinstance(x, torch.Tensor) and x.dim() == 3):
-            raise ValueError("x must be [total_seq_len, heads, head_size]")
-        kept = torch.empty(_chunk_shape(x), dtype=torch.float32, device=x.device)
-    output, final = _forward(x, g, initial_state, output_final_state, cu_seqlens, output,
-                             output_state, state_indices, kept, status, workspace)
-    res = (output,) + ((final,) if output_final_state else ()) + (
-        (kept,) if return_chunk_states else ())
-    return res if len(res) > 1 else output
+    res = _forward(x, g, initial_state, output_final_state, cu_seqlens, output, output_state,
+                   state_indices, return_chunk_states, status, workspace)
+    if output_final_state:
+        return res if return_chunk_states else res[:2]
+    return (res[0], res[2]) if return_chunk_states else res[0]
 
 
 def gated_linear_recurrence_backward(doutput, x, g, initial_state=None, dfinal_state=None,
@@ -270,43 +302,70 @@ def gated_linear_recurrence_backward(doutput, x, g, initial_state=None, dfinal_s
     ``output_dinitial_state``: x's and g's shapes and dtypes, float32
     [N, H, D].  Rows of dx and dg outside every sequence are zero.  Results do
     not depend on the order in which the work runs."""
-    p = _base_params(x, g, cu_seqlens, False, (
-        ("g", g), ("doutput", doutput), ("initial_state", initial_state),
-        ("dfinal_state", dfinal_state), ("cu_seqlens", cu_seqlens),
-        ("chunk_states", chunk_states), ("dx", dx), ("dg", dg),
-        ("dinitial_state", dinitial_state), ("status", status)))
-    N, (_, H, D) = p.num_seqs, x.shape
-    if doutput.dtype != x.dtype or doutput.shape != x.shape:
-        raise ValueError("doutput must have x's shape and dtype")
-    p.doutput, p.doutput_stride = _ptr(doutput), _token_stride("doutput", doutput, H * D)
-    if initial_state is not None:
-        initial_state, stride = _rec_state("initial_state", initial_state, N, H, D, False)
-        p.initial_state = _ptr(initial_state)
-        p.initial_state_dtype = _STATE_DTYPES[initial_state.dtype]
-        p.initial_state_stride = stride
-    if dfinal_state is not None:
-        _contiguous("dfinal_state", dfinal_state, (N, H, D), torch.float32)
-        p.dfinal_state = _ptr(dfinal_state)
-    if chunk_states is not None:
-        _contiguous("chunk_states", chunk_states, _chunk_shape(x), torch.float32)
-        p.chunk_states = _ptr(chunk_states)
+    try:
+        key = (x.shape, x.stride(), x.dtype, x.device, g.shape, g.stride(), g.dtype, g.device,
+               doutput.shape, doutput.stride(), doutput.dtype, doutput.device,
+               meta(initial_state), meta(dfinal_state), meta(cu_seqlens), meta(chunk_states),
+               bool(output_dinitial_state), meta(dx), meta(dg), meta(dinitial_state),
+               meta(status))
+        hit = _backward_blocks.get(key)
+    except AttributeError:
+        raise ValueError("doutput, x, g and the optional arguments must be tensors") from None
+    if hit is None:
+        p = _base_params(x, g, cu_seqlens, False, (
+            ("g", g), ("doutput", doutput), ("initial_state", initial_state),
+            ("dfinal_state", dfinal_state), ("cu_seqlens", cu_seqlens),
+            ("chunk_states", chunk_states), ("dx", dx), ("dg", dg),
+            ("dinitial_state", dinitial_state), ("status", status)))
+        N, (_, H, D) = p.num_seqs, x.shape
+        if doutput.dtype != x.dtype or doutput.shape != x.shape:
+            raise ValueError("doutput must have x's shape and dtype")
+        p.doutput_stride = _token_stride("doutput", doutput, H * D)
+        used = initial_state
+        if initial_state is not None:
+            used, stride = _rec_state("initial_state", initial_state, N, H, D, False)
+            p.initial_state_dtype = _STATE_DTYPES[used.dtype]
+            p.initial_state_stride = stride
+        for name, t, shape, dtype in (
+                ("dfinal_state", dfinal_state, (N, H, D), torch.float32),
+                ("chunk_states", chunk_states, _chunk_shape(x), torch.float32),
+                ("dx", dx, x.shape, x.dtype), ("dg", dg, g.shape, g.dtype),
+                ("dinitial_state", dinitial_state, (N, H, D), torch.float32)):
+            if t is not None:
+                _contiguous(name, t, shape, dtype)
+        _status(status)
+        p.chunk_states = None if chunk_states is None else chunk_states.data_ptr()
+        need = _workspace_size(p, cu_seqlens, True)
+        p.chunk_states = None
+        if used is initial_state:
+            _backward_blocks.keep(key, p, need)
+        initial_state = used
+    else:
+        p, need = hit
     if dx is None:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    else:
-        _contiguous("dx", dx, x.shape, x.dtype)
+        dx = _new_like(x)
     if dg is None:
-        dg = torch.empty(g.shape, dtype=g.dtype, device=x.device)
-    else:
-        _contiguous("dg", dg, g.shape, g.dtype)
-    p.dx, p.dg = _ptr(dx), _ptr(dg)
+        dg = _new_like(g)
+    p.x, p.g, p.doutput = x.data_ptr(), g.data_ptr(), doutput.data_ptr()
+    p.dx, p.dg = dx.data_ptr(), dg.data_ptr()
+    if cu_seqlens is not None:
+        p.cu_seqlens = cu_seqlens.data_ptr()
+    if initial_state is not None:
+        p.initial_state = initial_state.data_ptr()
+    if dfinal_state is not None:
+        p.dfinal_state = dfinal_state.data_ptr()
+    if chunk_states is not None:
+        p.chunk_states = chunk_states.data_ptr()
     if output_dinitial_state:
         if dinitial_state is None:
-            dinitial_state = torch.empty((N, H, D), dtype=torch.float32, device=x.device)
-        else:
-            _contiguous("dinitial_state", dinitial_state, (N, H, D), torch.float32)
-        p.dinitial_state = _ptr(dinitial_state)
-    _status(p, status)
-    _run(nat.lib().gdn_recurrence_backward, p, x.device, 1, workspace)
+            dinitial_state = torch.empty((p.num_seqs,) + x.shape[1:], dtype=torch.float32,
+                                         device=x.device)
+        p.dinitial_state = dinitial_state.data_ptr()
+    if status is not None:
+        p.status = status.data_ptr()
+    memory = _memory(p, x.device, need, workspace)
+    _launch.call(nat.lib().gdn_recurrence_backward, x.device, byref(p))
+    del memory
     return (dx, dg, dinitial_state) if output_dinitial_state else (dx, dg)
 
 
@@ -315,23 +374,40 @@ def gated_linear_recurrence_decode(x, g, initial_state=None, output_final_state=
     """One decode step: token i of x, g [N, ...] is the new token of sequence
     i.  States and ``state_indices`` are those of ``gated_linear_recurrence``.
     Returns ``output`` [N, H, D], or ``(output, final_state)``."""
-    p = _base_params(x, g, None, True, (
-        ("g", g), ("initial_state", initial_state), ("output", output),
-        ("output_state", output_state), ("state_indices", state_indices), ("status", status)))
-    if output is None:
-        output = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    try:
+        key = (x.shape, x.stride(), x.dtype, x.device, g.shape, g.stride(), g.dtype, g.device,
+               meta(initial_state), bool(output_final_state), meta(output), meta(output_state),
+               meta(state_indices), meta(status))
+        hit = _decode_blocks.get(key)
+    except AttributeError:
+        raise ValueError("x, g and the optional arguments must be tensors") from None
+    if hit is None:
+        p = _base_params(x, g, None, True, (
+            ("g", g), ("initial_state", initial_state), ("output", output),
+            ("output_state", output_state), ("state_indices", state_indices),
+            ("status", status)))
+        if output is not None:
+            _contiguous("output", output, x.shape, x.dtype)
+        _status(status)
+        used = _states(p, x, initial_state, output_final_state, output_state, state_indices)
+        if used is initial_state:
+            _decode_blocks.keep(key, p)
+        initial_state = used
     else:
-        _contiguous("output", output, x.shape, x.dtype)
-    p.output = _ptr(output)
-    output_state, keep = _states(p, x, initial_state, output_final_state, output_state,
-                                 state_indices)
-    _status(p, status)
-    with torch.cuda.device(x.device):
-        stream = torch.cuda.current_stream(x.device).cuda_stream
-        rc = nat.lib().gdn_recurrence_decode(ctypes.byref(p), ctypes.c_void_p(stream))
-    del keep
-    if rc != 0:
-        _raise(rc)
+        p = hit[0]
+    if output is None:
+        output = _new_like(x)
+    p.x, p.g, p.output = x.data_ptr(), g.data_ptr(), output.data_ptr()
+    if initial_state is not None:
+        p.initial_state = initial_state.data_ptr()
     if output_final_state:
-        return output, output_state
-    return output
+        if output_state is None:
+            output_state = torch.empty((p.num_seqs,) + x.shape[1:], dtype=torch.float32,
+                                       device=x.device)
+        p.output_state = output_state.data_ptr()
+    if state_indices is not None:
+        p.state_indices = state_indices.data_ptr()
+    if status is not None:
+        p.status = status.data_ptr()
+    _launch.call(nat.lib().gdn_recurrence_decode, x.device, byref(p))
+    return (output, output_state) if output_final_state else output

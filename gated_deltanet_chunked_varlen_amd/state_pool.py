@@ -9,12 +9,14 @@ or int64 device tensors; an entry of -1 is padding.
 """
 from __future__ import annotations
 
-import ctypes
+from ctypes import byref
 
 import torch
 
+from . import _launch
 from . import _native as nat
-from .api import _STATE_DTYPES, _index, _ptr, _raise, state_tensor
+from ._launch import Blocks, meta
+from .api import _STATE_DTYPES, _index, state_tensor
 
 
 def _pool_fields(name, pool, written):
@@ -37,31 +39,35 @@ def _pool_fields(name, pool, written):
     return pool, _STATE_DTYPES[pool.dtype], pool.shape[0], nat._i64x4(*strides), extent
 
 
+def _tensors(*args):
+    return all(isinstance(t, torch.Tensor) for t in args)
+
+
 def _list(name, rows, device):
     if not isinstance(rows, torch.Tensor) or rows.device != device:
         raise ValueError("%s must be a tensor on %s" % (name, device))
     return _index(name, rows)
 
 
-def _params(pool, dst_rows, status):
-    pool, dtype, rows, strides, extent = _pool_fields("pool", pool, True)
+def _check_status(status, device):
+    if status is not None and (status.device != device or status.dtype != torch.int32
+                               or status.numel() < 1):
+        raise ValueError("status must be an int32 tensor on %s" % device)
+
+
+def _block(pool, kind, count):
+    """Parameter block of a call on ``pool``, without addresses."""
+    _, dtype, rows, strides, extent = _pool_fields("pool", pool, True)
     p = nat.PoolParams()
     p.extent = nat._i64x3(*extent)
-    p.dst, p.dst_dtype, p.dst_pool_rows, p.dst_strides = _ptr(pool), dtype, rows, strides
-    if status is not None:
-        if status.device != pool.device or status.dtype != torch.int32 or status.numel() < 1:
-            raise ValueError("status must be an int32 tensor on %s" % pool.device)
-        p.status = _ptr(status)
-    p.dst_rows, p.count = _ptr(dst_rows), dst_rows.numel()
+    p.dst_dtype, p.dst_pool_rows, p.dst_strides = dtype, rows, strides
+    p.rows_type, p.count = kind, count
     return p
 
 
-def _call(fn, p, device, *more):
-    with torch.cuda.device(device):
-        stream = torch.cuda.current_stream(device).cuda_stream
-        rc = fn(ctypes.byref(p), *more, ctypes.c_void_p(stream))
-    if rc != 0:
-        _raise(rc)
+_copy_blocks = Blocks(nat.PoolParams)
+_reset_blocks = Blocks(nat.PoolParams)
+_compact_blocks = Blocks(nat.PoolParams)
 
 
 def state_pool_copy(pool, src_rows, dst_rows, src_pool=None, status=None):
@@ -75,26 +81,39 @@ def state_pool_copy(pool, src_rows, dst_rows, src_pool=None, status=None):
     entries outside the pools are skipped.  ``status`` (optional int32 device
     tensor) receives the matching GDN_STATUS_POOL_* bits.  src_pool may be the
     same view as pool, or share no elements with it.  Returns pool."""
-    device = pool.device if isinstance(pool, torch.Tensor) else None
-    kind = _list("src_rows", src_rows, device)
-    if _list("dst_rows", dst_rows, device) != kind:
-        raise ValueError("src_rows and dst_rows must share a dtype")
-    if src_rows.numel() != dst_rows.numel():
-        raise ValueError("src_rows and dst_rows must have the same length")
-    p = _params(pool, dst_rows, status)
-    p.rows_type, p.src_rows = kind, _ptr(src_rows)
     src = pool if src_pool is None else src_pool
-    src, p.src_dtype, p.src_pool_rows, p.src_strides, extent = _pool_fields("src_pool", src, False)
-    if src.device != device:
-        raise ValueError("src_pool must be on %s" % device)
-    if tuple(extent) != tuple(p.extent):
-        raise ValueError("rows of pool and src_pool differ in shape")
-    p.src = _ptr(src)
-    if pool.shape[0] == 0 or src.shape[0] == 0:
-        if src_rows.numel() > 0:
+    key = (meta(pool), meta(src_rows), meta(dst_rows), meta(src_pool), meta(status)) \
+        if _tensors(pool, src_rows, dst_rows, src) else None
+    hit = _copy_blocks.get(key)
+    if hit is None:
+        device = pool.device if isinstance(pool, torch.Tensor) else None
+        kind = _list("src_rows", src_rows, device)
+        if _list("dst_rows", dst_rows, device) != kind:
+            raise ValueError("src_rows and dst_rows must share a dtype")
+        if src_rows.numel() != dst_rows.numel():
+            raise ValueError("src_rows and dst_rows must have the same length")
+        _check_status(status, device)
+        p = _block(pool, kind, dst_rows.numel())
+        read, p.src_dtype, p.src_pool_rows, p.src_strides, extent = _pool_fields(
+            "src_pool", src, False)
+        if src.device != device:
+            raise ValueError("src_pool must be on %s" % device)
+        if tuple(extent) != tuple(p.extent):
+            raise ValueError("rows of pool and src_pool differ in shape")
+        if src_rows.numel() > 0 and (pool.shape[0] == 0 or src.shape[0] == 0):
             raise ValueError("a pool without rows cannot be copied from or into")
+        if read is src:
+            _copy_blocks.keep(key, p)
+        src = read
+    else:
+        p = hit[0]
+    if pool.shape[0] == 0 or src.shape[0] == 0:
         return pool
-    _call(nat.lib().gdn_pool_copy, p, device)
+    p.src, p.dst = src.data_ptr(), pool.data_ptr()
+    p.src_rows, p.dst_rows = src_rows.data_ptr(), dst_rows.data_ptr()
+    if status is not None:
+        p.status = status.data_ptr()
+    _launch.call(nat.lib().gdn_pool_copy, pool.device, byref(p))
     return pool
 
 
@@ -102,11 +121,20 @@ def state_pool_reset(pool, rows, status=None):
     """pool[rows[i]] = 0 for every i, on the current stream: rows freed, or
     taken for sequences that start from zero.  Entries outside the pool are
     skipped and set GDN_STATUS_POOL_ROW in ``status``.  Returns pool."""
-    device = pool.device if isinstance(pool, torch.Tensor) else None
-    kind = _list("rows", rows, device)
-    p = _params(pool, rows, status)
-    p.rows_type = kind
-    _call(nat.lib().gdn_pool_reset, p, device)
+    key = (meta(pool), meta(rows), meta(status)) if _tensors(pool, rows) else None
+    hit = _reset_blocks.get(key)
+    if hit is None:
+        device = pool.device if isinstance(pool, torch.Tensor) else None
+        kind = _list("rows", rows, device)
+        _check_status(status, device)
+        p = _block(pool, kind, rows.numel())
+        _reset_blocks.keep(key, p)
+    else:
+        p = hit[0]
+    p.dst, p.dst_rows = pool.data_ptr(), rows.data_ptr()
+    if status is not None:
+        p.status = status.data_ptr()
+    _launch.call(nat.lib().gdn_pool_reset, pool.device, byref(p))
     return pool
 
 
@@ -127,26 +155,39 @@ def state_pool_compact(pools, state_indices, output_indices=None, row_map=None, 
     if not pools:
         raise ValueError("state_pool_compact needs a pool")
     device = pools[0].device if isinstance(pools[0], torch.Tensor) else None
-    kind = _list("state_indices", state_indices, device)
+    blocks = []
+    for pool in pools:
+        key = (meta(pool), meta(state_indices), meta(output_indices), meta(row_map),
+               meta(status), meta(pools[0])) if _tensors(pool, state_indices) else None
+        hit = _compact_blocks.get(key)
+        if hit is None:
+            kind = _list("state_indices", state_indices, device)
+            if output_indices is not None and (
+                    output_indices.device != device
+                    or output_indices.dtype != state_indices.dtype
+                    or output_indices.shape != state_indices.shape
+                    or not output_indices.is_contiguous()):
+                raise ValueError("output_indices must match state_indices")
+            if row_map is not None and (row_map.device != device or row_map.dtype != torch.int32
+                                        or tuple(row_map.shape) != (pools[0].shape[0],)
+                                        or not row_map.is_contiguous()):
+                raise ValueError("row_map must be contiguous int32 [%d] on %s"
+                                 % (pools[0].shape[0], device))
+            _check_status(status, device)
+            p = _block(pool, kind, state_indices.numel())
+            if pool.device != device or pool.shape[0] != pools[0].shape[0]:
+                raise ValueError("pools must share a device and a number of rows")
+            _compact_blocks.keep(key, p)
+        else:
+            p = hit[0]
+        blocks.append(p)
     if output_indices is None:
         output_indices = torch.empty_like(state_indices)
-    elif (output_indices.device != device or output_indices.dtype != state_indices.dtype
-          or output_indices.shape != state_indices.shape or not output_indices.is_contiguous()):
-        raise ValueError("output_indices must match state_indices")
-    if row_map is not None and (row_map.device != device or row_map.dtype != torch.int32
-                                or tuple(row_map.shape) != (pools[0].shape[0],)
-                                or not row_map.is_contiguous()):
-        raise ValueError("row_map must be contiguous int32 [%d] on %s"
-                         % (pools[0].shape[0], device))
-    calls = []
-    for pool in pools:
-        p = _params(pool, state_indices, status)
-        if pool.device != device or pool.shape[0] != pools[0].shape[0]:
-            raise ValueError("pools must share a device and a number of rows")
-        p.rows_type = kind
-        calls.append(p)
     num_live = torch.empty(1, dtype=torch.int32, device=device)
-    for p in calls:
-        _call(nat.lib().gdn_pool_compact, p, device, _ptr(output_indices), _ptr(num_live),
-              _ptr(row_map))
+    for pool, p in zip(pools, blocks):
+        p.dst, p.dst_rows = pool.data_ptr(), state_indices.data_ptr()
+        if status is not None:
+            p.status = status.data_ptr()
+        _launch.call(nat.lib().gdn_pool_compact, device, byref(p), output_indices.data_ptr(),
+                     num_live.data_ptr(), None if row_map is None else row_map.data_ptr())
     return output_indices, num_live
