@@ -15,6 +15,7 @@ using namespace gdn;
 namespace {
 
 constexpr size_t kAlign = 256;
+constexpr int64_t kMaxUnits = 1 << 22;  // tiles of 64 tokens x 256 channels
 constexpr int64_t kMaxTokens = INT32_MAX - 64;
 
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
@@ -44,7 +45,8 @@ int check_shape(const gdn_recurrence_params *p, int mode) {
   } else {
     if (!p->cu_seqlens && p->num_seqs != 1) return GDN_ERR_SHAPE;
     const int64_t ncb = (C + kRecChannels - 1) / kRecChannels;
-    if (tiles_of(p) * ncb > INT32_MAX) return GDN_ERR_SHAPE;
+    // one workgroup per unit; a grid holds fewer than 2^32 threads
+    if (tiles_of(p) * ncb > kMaxUnits) return GDN_ERR_SHAPE;
   }
   if (!float_type(p->x_dtype)) return GDN_ERR_DTYPE;
   if (p->g_dtype != GDN_F32 && p->g_dtype != p->x_dtype) return GDN_ERR_DTYPE;

@@ -27,11 +27,13 @@
 // tickets, which were taken by workgroups that are already running; the
 // smallest unfinished ticket waits for nothing, so every wait ends.
 //
-// Sequence bounds.  A token that starts a sequence folds its initial state
-// into x (x + g h0) and takes no h from the left; the carry is selected, not
-// multiplied by zero, so a NaN or infinity of one sequence never reaches the
-// next.  The backward scan runs the chain from the last tile to the first,
-// with the carry c_t = g_t dh_t.
+// Sequence bounds.  A wave walks its tokens segment by segment, a segment
+// being the wave's part of one sequence; where a sequence starts the carry is
+// replaced by its initial state, never multiplied by zero, so a NaN or
+// infinity of one sequence does not reach the next.  Sweep 1 needs the last
+// segment only (the first one, going backward): what lies before a start does
+// not leave the wave.  The backward scan runs the chain from the last tile to
+// the first, with the carry k_t = g_t dh_t.
 #include "gdn_common.h"
 #include "gdn_internal.h"
 #include "gdn_recurrence.h"
@@ -47,34 +49,32 @@ namespace {
 constexpr int kTok = 8;                     // tokens per wave
 constexpr int kWaves = kRecTile / kTok;     // waves per workgroup
 constexpr int kThreads = 64 * kWaves;
-constexpr int kWindow = 16;                 // tiles looked back over
+constexpr int kWindow = 8;                  // tiles looked back over
 constexpr unsigned kPending = 0xFFFFFFFFu, kLast = 0xFFFFFFFEu;
 
 typedef float f32x4v __attribute__((ext_vector_type(4)));
 
 // ------------------------------------------------------------ memory access
 
-// Four consecutive elements as fp32; `left` of them exist (VEC: all four, on
-// an address aligned to their size).
+template <typename T> using V4 = T __attribute__((ext_vector_type(4)));
+
+// Four consecutive elements, kept in their type until they are used (16-bit
+// types: two registers instead of four); `left` of them exist (VEC: all four,
+// on an address aligned to their size).
 template <typename T, bool VEC>
-__device__ __forceinline__ void load4(const T *p, int left, float (&o)[4]) {
-  if (VEC) {
-    typedef T vec __attribute__((ext_vector_type(4)));
-    const vec v = *reinterpret_cast<const vec *>(p);
+__device__ __forceinline__ V4<T> load4(const T *p, int left) {
+  if (VEC) return *reinterpret_cast<const V4<T> *>(p);
+  V4<T> v;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] = to_f32((T)v[e]);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] = e < left ? to_f32(p[e]) : 0.f;
-  }
+  for (int e = 0; e < 4; ++e) v[e] = e < left ? p[e] : (T)0.f;
+  return v;
 }
 
 template <typename T, bool VEC>
 __device__ __forceinline__ void store4(T *p, int left, const float (&o)[4]) {
   if (VEC) {
-    typedef T vec __attribute__((ext_vector_type(4)));
     const f32x4v f = {o[0], o[1], o[2], o[3]};
-    *reinterpret_cast<vec *>(p) = __builtin_convertvector(f, vec);
+    *reinterpret_cast<V4<T> *>(p) = __builtin_convertvector(f, V4<T>);
   } else {
 #pragma unroll
     for (int e = 0; e < 4; ++e)
@@ -168,8 +168,8 @@ __device__ __forceinline__ unsigned map_bits(float A) {
 // channel; avail >= 1 tiles lie in that direction, and the last of them always
 // publishes kLast by itself.
 __device__ __forceinline__ float look_back(const unsigned long long *words, int64_t C, int tile,
-                                           int c, int step, int avail) {
-  const unsigned long long *base = words + (int64_t)tile * C + c;
+                                           unsigned c, int step, int avail) {
+  words += (int64_t)(tile + step) * C;
   const int64_t d = (int64_t)step * C;
   for (;;) {
     unsigned long long w[kWindow];
@@ -180,7 +180,7 @@ __device__ __forceinline__ float look_back(const unsigned long long *words, int6
       if (found < 0 && open && j0 < avail) {
 #pragma unroll
         for (int j = j0; j < j0 + 4; ++j)
-          w[j] = j < avail ? __hip_atomic_load(base + (int64_t)(j + 1) * d, __ATOMIC_RELAXED,
+          w[j] = j < avail ? __hip_atomic_load(words + (int64_t)j * d + c, __ATOMIC_RELAXED,
                                                __HIP_MEMORY_SCOPE_AGENT)
                            : (unsigned long long)kPending << 32;
 #pragma unroll
@@ -287,48 +287,163 @@ __device__ __forceinline__ void for_empty_sequences(const RecArgs &a, F f) {
   }
 }
 
-// The unit this workgroup works on next: a ticket, or its block index.
-__device__ __forceinline__ unsigned next_unit(const RecArgs &a, unsigned &sh) {
+// The unit this workgroup works on: a ticket, or its block index.
+__device__ __forceinline__ unsigned take_unit(const RecArgs &a) {
   if (!a.ticket) return blockIdx.x;
-  __syncthreads();  // LDS of the unit before is free, and so is sh
+  __shared__ unsigned unit;
   if (threadIdx.x == 0)
-    sh = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    unit = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   __syncthreads();
-  return sh;
+  return __builtin_amdgcn_readfirstlane(unit);
 }
 
-// Gate of token row t for a lane's four channels (PH: their head's).
-template <typename Tg, bool PH, bool VEC>
-__device__ __forceinline__ void load_gate(const RecArgs &a, int64_t t, int c, int left, int head,
-                                          float (&g)[PH ? 1 : 4]) {
-  const Tg *p = (const Tg *)a.g + t * a.g_stride;
-  if constexpr (PH) g[0] = to_f32(p[head]);
-  else load4<Tg, VEC>(p + c, left, g);
-}
+// Gates of one token for a lane's four channels: four values, or their head's.
+template <typename Tg, bool PH, bool VEC> struct Gate {
+  V4<Tg> v;
+  __device__ __forceinline__ void load(const Tg *row, int c, int left, int) {
+    v = load4<Tg, VEC>(row + c, left);
+  }
+  __device__ __forceinline__ float operator[](int e) const { return to_f32((Tg)v[e]); }
+};
+template <typename Tg, bool VEC> struct Gate<Tg, true, VEC> {
+  Tg v;
+  __device__ __forceinline__ void load(const Tg *row, int, int, int head) { v = row[head]; }
+  __device__ __forceinline__ float operator[](int) const { return to_f32(v); }
+};
 
-// The marked tokens' values of v (wave-uniform `at`), for a lane's channels.
-__device__ __forceinline__ void pick(const float (&v)[kTok][4], int at, float (&o)[4]) {
+// The marks of a tile's tokens as wave-uniform bits, and of a wave's: tokens
+// that start and end a sequence, and those that belong to one, [lo, hi).
+struct Marks {
+  unsigned long long firsts, lasts;  // the tile's 64 tokens
+  unsigned first, last;              // this wave's
+  int lo, hi;
+  int id_first, id_last;  // lane i: sequence that starts / ends at the tile's token i
+  int base;               // the wave's first token within the tile
+
+  __device__ __forceinline__ void read(const TileGeo &G, int t0, int wave, int lane) {
+    id_first = G.start[lane];
+    id_last = G.end[lane];
+    firsts = __ballot(id_first >= 0);
+    lasts = __ballot(id_last >= 0);
+    base = wave * kTok;
+    first = wave_first(wave);
+    last = wave_last(wave);
+    lo = __builtin_amdgcn_readfirstlane(min(max(G.lo - t0 - base, 0), kTok));
+    hi = __builtin_amdgcn_readfirstlane(min(max(G.hi - t0 - base, 0), kTok));
+  }
+  __device__ __forceinline__ unsigned wave_first(int w) const {
+    return (unsigned)(firsts >> (w * kTok)) & ((1u << kTok) - 1);
+  }
+  __device__ __forceinline__ unsigned wave_last(int w) const {
+    return (unsigned)(lasts >> (w * kTok)) & ((1u << kTok) - 1);
+  }
+  // the wave's last token that starts a sequence
+  __device__ __forceinline__ int last_first() const { return 31 - __builtin_clz(first); }
+  // sequence that starts / ends at this wave's token s
+  __device__ __forceinline__ int seq_first(int s) const {
+    return __builtin_amdgcn_readlane(id_first, base + s);
+  }
+  __device__ __forceinline__ int seq_last(int s) const {
+    return __builtin_amdgcn_readlane(id_last, base + s);
+  }
+};
+
+// f(s) for the tokens s of [lo, hi), ascending or descending; the whole wave's
+// tokens take a loop without conditions.
+template <typename F>
+__device__ __forceinline__ void ascend(int lo, int hi, F f) {
+  if (lo == 0 && hi == kTok) {
 #pragma unroll
-  for (int s = 0; s < kTok; ++s)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] = s == at || s == 0 ? v[s][e] : o[e];
-}
-
-// x + g h0 at the tokens of `first`.
-template <bool PH>
-__device__ __forceinline__ void fold_initial(const RecArgs &a, unsigned first, int id, int c,
-                                             int left, const float (&g)[kTok][PH ? 1 : 4],
-                                             float (&x)[kTok][4]) {
-  for (unsigned m = first; m; m &= m - 1) {
-    const int at = __builtin_ctz(m);
-    float h0[4];
-    load_init(a, __builtin_amdgcn_readlane(id, at), c, left, h0);
+    for (int s = 0; s < kTok; ++s) f(s);
+  } else {
 #pragma unroll
     for (int s = 0; s < kTok; ++s)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        x[s][e] = s == at ? fmaf(g[s][PH ? 0 : e], h0[e], x[s][e]) : x[s][e];
+      if (s >= lo && s < hi) f(s);
   }
+}
+template <typename F>
+__device__ __forceinline__ void descend(int lo, int hi, F f) {
+  if (lo == 0 && hi == kTok) {
+#pragma unroll
+    for (int s = kTok - 1; s >= 0; --s) f(s);
+  } else {
+#pragma unroll
+    for (int s = kTok - 1; s >= 0; --s)
+      if (s >= lo && s < hi) f(s);
+  }
+}
+
+// Sweep 1 of the forward map: the wave's (A, B).  h0 receives the initial state
+// of the wave's last sequence start, which sweep 2 must not read again: in a
+// pool worked on in place, another wave may have written that sequence's final
+// state over it by then.
+template <typename Tx, typename GateT>
+__device__ __forceinline__ void forward_map(const RecArgs &a, const Marks &m,
+                                            const V4<Tx> (&x)[kTok], const GateT (&g)[kTok], int c,
+                                            int left, float (&A)[4], float (&B)[4],
+                                            float (&h0)[4]) {
+  int lo = m.lo;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) h0[e] = 0.f;
+  if (m.first) {
+    lo = m.last_first();
+    load_init(a, m.seq_first(lo), c, left, h0);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    A[e] = 1.f;
+    B[e] = h0[e];
+  }
+  ascend(lo, m.hi, [&](int s) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float gg = g[s][e];
+      B[e] = fmaf(gg, B[e], to_f32((Tx)x[s][e]));
+      A[e] *= gg;
+    }
+  });
+}
+
+// The state before token s, which starts a sequence.  Every start of the wave
+// but the last has its sequence end in this wave too, after this read.
+__device__ __forceinline__ void start_state(const RecArgs &a, const Marks &m, int s, int c,
+                                            int left, const float (&h0)[4], float (&h)[4]) {
+  if (s == m.last_first()) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e] = h0[e];
+  } else {
+    load_init(a, m.seq_first(s), c, left, h);
+  }
+}
+
+// f(lo, hi, started): the wave's segments in order, `started` where the first
+// token starts a sequence.
+template <typename F>
+__device__ __forceinline__ void segments_up(const Marks &m, F f) {
+  unsigned first = m.first;
+  int lo = m.lo;
+  bool started = false;
+  for (;;) {
+    const int hi = first ? __builtin_ctz(first) : m.hi;
+    if (hi > lo) f(lo, hi, started);
+    if (!first) break;
+    first &= first - 1;
+    lo = hi;
+    started = true;
+  }
+}
+// The same from the last to the first.
+template <typename F>
+__device__ __forceinline__ void segments_down(const Marks &m, F f) {
+  unsigned first = m.first;
+  int hi = m.hi;
+  while (first) {
+    const int lo = 31 - __builtin_clz(first);
+    if (hi > lo) f(lo, hi, true);
+    first &= ~(1u << lo);
+    hi = lo;
+  }
+  if (hi > m.lo) f(m.lo, hi, false);
 }
 
 // ------------------------------------------------------------------ forward
@@ -338,138 +453,95 @@ __device__ __forceinline__ void fold_initial(const RecArgs &a, unsigned first, i
 // and looking back.
 template <typename Tx, typename Tg, bool PH, bool VEC>
 __global__ void __launch_bounds__(kThreads) rec_forward_kernel(RecArgs a) {
-  constexpr int GV = PH ? 1 : 4;
   __shared__ TileGeo G;
   __shared__ float sA[kWaves][kRecChannels], sB[kWaves][kRecChannels];
-  __shared__ int s_reset[kWaves];
-  __shared__ unsigned s_unit;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  for (;;) {
-    const unsigned u = next_unit(a, s_unit);
-    if (u >= a.units) return;
-    const int tile = (int)(u / (unsigned)a.ncb), cb = (int)(u % (unsigned)a.ncb);
-    const int t0 = tile * kRecTile, tw = t0 + wave * kTok;
-    const int c = cb * kRecChannels + 4 * lane;
-    const int left = min(4, a.C - c);
-    const int head = PH ? min(c, a.C - 1) / a.D : 0;
+  // what is the same for a wave's lanes is kept in scalar registers
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const unsigned u = take_unit(a);
+  const int tile = (int)(u / (unsigned)a.ncb), cb = (int)(u % (unsigned)a.ncb);
+  const int T = (int)a.T;
+  const int t0 = tile * kRecTile, tw = t0 + wave * kTok;
+  const int c = cb * kRecChannels + 4 * lane;
+  const int left = min(4, a.C - c);
+  const int head = PH ? min(c, a.C - 1) / a.D : 0;
 
-    float x[kTok][4], g[kTok][GV];
+  V4<Tx> x[kTok];
+  Gate<Tg, PH, VEC> g[kTok];
+  if (left > 0) {
 #pragma unroll
     for (int s = 0; s < kTok; ++s) {
-      const int64_t t = tw + s;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[s][e] = 0.f;
-#pragma unroll
-      for (int e = 0; e < GV; ++e) g[s][e] = 1.f;
-      if (t < a.T && left > 0) {
-        load4<Tx, VEC>((const Tx *)a.x + t * a.x_stride + c, left, x[s]);
-        load_gate<Tg, PH, VEC>(a, t, c, left, head, g[s]);
-      }
-    }
-    tile_geometry(a, t0, u == 0, G);
-
-    // marks of this wave's tokens, as wave-uniform bits
-    const int my = wave * kTok + (lane & (kTok - 1));
-    const int id_s = G.start[my], id_e = G.end[my];
-    const unsigned first = (unsigned)__ballot(id_s >= 0) & ((1u << kTok) - 1);
-    const unsigned last = (unsigned)__ballot(id_e >= 0) & ((1u << kTok) - 1);
-    const int glo = G.lo, ghi = G.hi;
-
-    // tokens outside every sequence: the identity
-#pragma unroll
-    for (int s = 0; s < kTok; ++s) {
-      if (tw + s < glo || tw + s >= ghi) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[s][e] = 0.f;
-#pragma unroll
-        for (int e = 0; e < GV; ++e) g[s][e] = 1.f;
-      }
-    }
-    if (a.init) fold_initial<PH>(a, first, id_s, c, left, g, x);
-    {
-      float A[4] = {1.f, 1.f, 1.f, 1.f}, B[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int s = 0; s < kTok; ++s) {
-        const bool st = first >> s & 1;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float gg = g[s][PH ? 0 : e];
-          B[e] = st ? x[s][e] : fmaf(gg, B[e], x[s][e]);
-          A[e] *= gg;
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        sA[wave][4 * lane + e] = A[e];
-        sB[wave][4 * lane + e] = B[e];
-      }
-      if (lane == 0) s_reset[wave] = first != 0;
-    }
-    __syncthreads();
-
-    if (tid < kRecChannels) {
-      const int ch = cb * kRecChannels + tid;
-      if (ch < a.C) {
-        float A = 1.f, B = 0.f, h = 0.f;
-        bool reset = tile == 0;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-          const bool r = s_reset[w];
-          B = r ? sB[w][tid] : fmaf(sA[w][tid], B, sB[w][tid]);
-          A *= sA[w][tid];
-          reset |= r;
-        }
-        if (a.ticket) {
-          unsigned long long *w = a.words + (int64_t)tile * a.C + ch;
-          if (reset) publish(w, kLast, B);
-          else publish(w, map_bits(A), B);
-          if (tile > 0) {
-            h = look_back(a.words, a.C, tile, ch, -1, tile);
-            if (!reset) publish(w, kLast, fmaf(A, h, B));
-          }
-        }
-        if (a.chunk) a.chunk[(int64_t)tile * a.C + ch] = h;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-          const float b = sB[w][tid], aa = sA[w][tid];
-          sB[w][tid] = h;
-          h = s_reset[w] ? b : fmaf(aa, h, b);
-        }
-      }
-    }
-    __syncthreads();
-
-    if (left > 0) {
-      float h[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) h[e] = sB[wave][4 * lane + e];
-#pragma unroll
-      for (int s = 0; s < kTok; ++s) {
+      if (tw + s < T) {
         const int64_t t = tw + s;
-        const bool st = first >> s & 1;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          h[e] = st ? x[s][e] : fmaf(g[s][PH ? 0 : e], h[e], x[s][e]);
-        if (a.out && t >= glo && t < ghi) store4<Tx, VEC>((Tx *)a.out + t * a.C + c, left, h);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[s][e] = h[e];
+        x[s] = load4<Tx, VEC>((const Tx *)a.x + t * a.x_stride + c, left);
+        g[s].load((const Tg *)a.g + t * a.g_stride, c, left, head);
       }
-      if (a.fin) {
-        for (unsigned m = last; m; m &= m - 1) {
-          const int at = __builtin_ctz(m);
-          pick(x, at, h);
-          store_final(a, __builtin_amdgcn_readlane(id_e, at), c, left, h);
+    }
+  }
+  tile_geometry(a, t0, u == 0, G);
+  Marks m;
+  m.read(G, t0, wave, lane);
+  float h0[4];
+  {
+    float A[4], B[4];
+    forward_map<Tx>(a, m, x, g, c, left, A, B, h0);
+    *reinterpret_cast<f32x4v *>(&sA[wave][4 * lane]) = f32x4v{A[0], A[1], A[2], A[3]};
+    *reinterpret_cast<f32x4v *>(&sB[wave][4 * lane]) = f32x4v{B[0], B[1], B[2], B[3]};
+  }
+  __syncthreads();
+
+  if (tid < kRecChannels) {
+    const int ch = cb * kRecChannels + tid;
+    if (ch < a.C) {
+      float A = 1.f, B = 0.f, h = 0.f;
+      bool reset = tile == 0;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        const bool r = m.wave_first(w) != 0;
+        B = r ? sB[w][tid] : fmaf(sA[w][tid], B, sB[w][tid]);
+        A *= sA[w][tid];
+        reset |= r;
+      }
+      if (a.ticket) {
+        unsigned long long *w = a.words + (int64_t)tile * a.C + ch;
+        if (reset) publish(w, kLast, B);
+        else publish(w, map_bits(A), B);
+        if (tile > 0) {
+          h = look_back(a.words, a.C, tile, ch, -1, tile);
+          if (!reset) publish(w, kLast, fmaf(A, h, B));
         }
       }
+      if (a.chunk) a.chunk[(int64_t)tile * a.C + ch] = h;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        const float b = sB[w][tid], aa = sA[w][tid];
+        sB[w][tid] = h;
+        h = m.wave_first(w) ? b : fmaf(aa, h, b);
+      }
     }
-    if (tile == 0 && a.fin) {
-      for_empty_sequences(a, [&](int i) {
-        float h0[4];
-        load_init(a, i, c, left, h0);
-        if (left > 0) store_final(a, i, c, left, h0);
+  }
+  __syncthreads();
+
+  if (left > 0) {
+    float h[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e] = sB[wave][4 * lane + e];
+    segments_up(m, [&](int lo, int hi, bool started) {
+      if (started) start_state(a, m, lo, c, left, h0, h);
+      ascend(lo, hi, [&](int s) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[e] = fmaf(g[s][e], h[e], to_f32((Tx)x[s][e]));
+        if (a.out) store4<Tx, VEC>((Tx *)a.out + (int64_t)(tw + s) * a.C + c, left, h);
       });
-    }
-    if (!a.ticket) return;
+      if (a.fin && (m.last >> (hi - 1) & 1)) store_final(a, m.seq_last(hi - 1), c, left, h);
+    });
+  }
+  if (tile == 0 && a.fin) {
+    for_empty_sequences(a, [&](int i) {
+      float h0[4];
+      load_init(a, i, c, left, h0);
+      if (left > 0) store_final(a, i, c, left, h0);
+    });
   }
 }
 
@@ -480,207 +552,171 @@ __global__ void __launch_bounds__(kThreads) rec_forward_kernel(RecArgs a) {
 // comes through the chain from the tiles behind.  Bounded by HBM.
 template <typename Tx, typename Tg, bool PH, bool VEC>
 __global__ void __launch_bounds__(kThreads) rec_backward_kernel(RecArgs a) {
-  constexpr int GV = PH ? 1 : 4;
   __shared__ TileGeo G;
   __shared__ float sA[kWaves][kRecChannels], sF[kWaves][kRecChannels], sB[kWaves][kRecChannels];
-  __shared__ int s_first[kWaves], s_last[kWaves];
-  __shared__ unsigned s_unit;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  for (;;) {
-    const unsigned u = next_unit(a, s_unit);
-    if (u >= a.units) return;
-    const int tile = a.ntiles - 1 - (int)(u / (unsigned)a.ncb), cb = (int)(u % (unsigned)a.ncb);
-    const int t0 = tile * kRecTile, tw = t0 + wave * kTok;
-    const int c = cb * kRecChannels + 4 * lane;
-    const int left = min(4, a.C - c);
-    const int head = PH ? min(c, a.C - 1) / a.D : 0;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const unsigned u = take_unit(a);
+  const int tile = a.ntiles - 1 - (int)(u / (unsigned)a.ncb), cb = (int)(u % (unsigned)a.ncb);
+  const int T = (int)a.T;
+  const int t0 = tile * kRecTile, tw = t0 + wave * kTok;
+  const int c = cb * kRecChannels + 4 * lane;
+  const int left = min(4, a.C - c);
+  const int head = PH ? min(c, a.C - 1) / a.D : 0;
 
-    float x[kTok][4], g[kTok][GV], dy[kTok][4];
+  V4<Tx> x[kTok], dy[kTok];
+  Gate<Tg, PH, VEC> g[kTok];
+  if (left > 0) {
 #pragma unroll
+    for (int s = 0; s < kTok; ++s) {
+      if (tw + s < T) {
+        const int64_t t = tw + s;
+        x[s] = load4<Tx, VEC>((const Tx *)a.x + t * a.x_stride + c, left);
+        dy[s] = load4<Tx, VEC>((const Tx *)a.dy + t * a.dy_stride + c, left);
+        g[s].load((const Tg *)a.g + t * a.g_stride, c, left, head);
+      }
+    }
+  }
+  tile_geometry(a, t0, u == 0, G);
+  Marks m;
+  m.read(G, t0, wave, lane);
+  float h0[4];
+  auto load_dfinal = [&](int i, float (&k)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) k[e] = 0.f;
+    if (a.dfin) load_state(a.dfin, GDN_F32, (int64_t)i * a.C + c, left, k);
+  };
+  {
+    float A[4], F[4], B[4], P[4] = {1.f, 1.f, 1.f, 1.f};
+    forward_map<Tx>(a, m, x, g, c, left, A, F, h0);
+    // the map of the carry: over all tokens, or up to the first sequence end
+    int hi = m.hi;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) B[e] = 0.f;
+    if (m.last) {
+      hi = __builtin_ctz(m.last) + 1;
+      load_dfinal(m.seq_last(hi - 1), B);
+    }
+    descend(m.lo, hi, [&](int s) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float gg = g[s][e];
+        B[e] = gg * (to_f32((Tx)dy[s][e]) + B[e]);
+        P[e] *= gg;
+      }
+    });
+    *reinterpret_cast<f32x4v *>(&sA[wave][4 * lane]) = f32x4v{P[0], P[1], P[2], P[3]};
+    *reinterpret_cast<f32x4v *>(&sF[wave][4 * lane]) = f32x4v{F[0], F[1], F[2], F[3]};
+    *reinterpret_cast<f32x4v *>(&sB[wave][4 * lane]) = f32x4v{B[0], B[1], B[2], B[3]};
+  }
+  __syncthreads();
+
+  if (tid < kRecChannels) {
+    const int ch = cb * kRecChannels + tid;
+    if (ch < a.C) {
+      float A = 1.f, B = 0.f, k = 0.f;
+      bool reset = tile == a.ntiles - 1;
+#pragma unroll
+      for (int w = kWaves - 1; w >= 0; --w) {
+        const bool r = m.wave_last(w) != 0;
+        B = r ? sB[w][tid] : fmaf(sA[w][tid], B, sB[w][tid]);
+        A *= sA[w][tid];
+        reset |= r;
+      }
+      if (a.ticket) {
+        unsigned long long *w = a.words + (int64_t)tile * a.C + ch;
+        if (reset) publish(w, kLast, B);
+        else publish(w, map_bits(A), B);
+        if (tile < a.ntiles - 1) {
+          k = look_back(a.words, a.C, tile, ch, 1, a.ntiles - 1 - tile);
+          if (!reset) publish(w, kLast, fmaf(A, k, B));
+        }
+      }
+      float h = a.chunk ? a.chunk[(int64_t)tile * a.C + ch] : 0.f;
+#pragma unroll
+      for (int w = kWaves - 1; w >= 0; --w) {
+        const float b = sB[w][tid];
+        sB[w][tid] = k;
+        k = m.wave_last(w) ? b : fmaf(sA[w][tid], k, b);
+      }
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        const float f = sF[w][tid];
+        sF[w][tid] = h;
+        h = m.wave_first(w) ? f : fmaf(sA[w][tid], h, f);
+      }
+    }
+  }
+  __syncthreads();
+
+  // gradients of rows outside every sequence are zero
+  if (m.lo > 0 || m.hi < kTok) {
+    const float zero[4] = {0.f, 0.f, 0.f, 0.f};
     for (int s = 0; s < kTok; ++s) {
       const int64_t t = tw + s;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[s][e] = dy[s][e] = 0.f;
-#pragma unroll
-      for (int e = 0; e < GV; ++e) g[s][e] = 1.f;
-      if (t < a.T && left > 0) {
-        load4<Tx, VEC>((const Tx *)a.x + t * a.x_stride + c, left, x[s]);
-        load4<Tx, VEC>((const Tx *)a.dy + t * a.dy_stride + c, left, dy[s]);
-        load_gate<Tg, PH, VEC>(a, t, c, left, head, g[s]);
+      if ((s < m.lo || s >= m.hi) && t < a.T && left > 0) {
+        store4<Tx, VEC>((Tx *)a.dx + t * a.C + c, left, zero);
+        if constexpr (PH) {
+          if (c % a.D == 0) ((Tg *)a.dg)[t * a.H + head] = from_f32<Tg>(0.f);
+        } else {
+          store4<Tg, VEC>((Tg *)a.dg + t * a.C + c, left, zero);
+        }
       }
     }
-    tile_geometry(a, t0, u == 0, G);
-
-    const int my = wave * kTok + (lane & (kTok - 1));
-    const int id_s = G.start[my], id_e = G.end[my];
-    const unsigned first = (unsigned)__ballot(id_s >= 0) & ((1u << kTok) - 1);
-    const unsigned last = (unsigned)__ballot(id_e >= 0) & ((1u << kTok) - 1);
-    const int glo = G.lo, ghi = G.hi;
-#pragma unroll
-    for (int s = 0; s < kTok; ++s) {
-      if (tw + s < glo || tw + s >= ghi) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[s][e] = dy[s][e] = 0.f;
-#pragma unroll
-        for (int e = 0; e < GV; ++e) g[s][e] = 1.f;
-      }
-    }
-    if (a.init) fold_initial<PH>(a, first, id_s, c, left, g, x);
-    if (a.dfin) {
-      for (unsigned m = last; m; m &= m - 1) {
-        const int at = __builtin_ctz(m);
-        float d[4];
-        load_state(a.dfin, GDN_F32, (int64_t)__builtin_amdgcn_readlane(id_e, at) * a.C + c, left,
-                   d);
-#pragma unroll
-        for (int s = 0; s < kTok; ++s)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) dy[s][e] += s == at ? d[e] : 0.f;
-      }
-    }
+  }
+  if (left > 0) {
+    float before[kTok][4];  // the state before each token
     {
-      float A[4] = {1.f, 1.f, 1.f, 1.f}, F[4] = {0.f, 0.f, 0.f, 0.f}, B[4] = {0.f, 0.f, 0.f, 0.f};
+      float h[4];
 #pragma unroll
-      for (int s = 0; s < kTok; ++s) {
-        const bool st = first >> s & 1;
+      for (int e = 0; e < 4; ++e) h[e] = sF[wave][4 * lane + e];
+      segments_up(m, [&](int lo, int hi, bool started) {
+        if (started) start_state(a, m, lo, c, left, h0, h);
+        ascend(lo, hi, [&](int s) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float gg = g[s][PH ? 0 : e];
-          F[e] = st ? x[s][e] : fmaf(gg, F[e], x[s][e]);
-          A[e] *= gg;
-        }
-      }
-#pragma unroll
-      for (int s = kTok - 1; s >= 0; --s) {
-        const bool en = last >> s & 1;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) B[e] = g[s][PH ? 0 : e] * (en ? dy[s][e] : dy[s][e] + B[e]);
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        sA[wave][4 * lane + e] = A[e];
-        sF[wave][4 * lane + e] = F[e];
-        sB[wave][4 * lane + e] = B[e];
-      }
-      if (lane == 0) {
-        s_first[wave] = first != 0;
-        s_last[wave] = last != 0;
-      }
-    }
-    __syncthreads();
-
-    if (tid < kRecChannels) {
-      const int ch = cb * kRecChannels + tid;
-      if (ch < a.C) {
-        float A = 1.f, B = 0.f, k = 0.f;
-        bool reset = tile == a.ntiles - 1;
-#pragma unroll
-        for (int w = kWaves - 1; w >= 0; --w) {
-          const bool r = s_last[w];
-          B = r ? sB[w][tid] : fmaf(sA[w][tid], B, sB[w][tid]);
-          A *= sA[w][tid];
-          reset |= r;
-        }
-        if (a.ticket) {
-          unsigned long long *w = a.words + (int64_t)tile * a.C + ch;
-          if (reset) publish(w, kLast, B);
-          else publish(w, map_bits(A), B);
-          if (tile < a.ntiles - 1) {
-            k = look_back(a.words, a.C, tile, ch, 1, a.ntiles - 1 - tile);
-            if (!reset) publish(w, kLast, fmaf(A, k, B));
+          for (int e = 0; e < 4; ++e) {
+            before[s][e] = h[e];
+            h[e] = fmaf(g[s][e], h[e], to_f32((Tx)x[s][e]));
           }
-        }
-        float h = a.chunk ? a.chunk[(int64_t)tile * a.C + ch] : 0.f;
-#pragma unroll
-        for (int w = kWaves - 1; w >= 0; --w) {
-          const float b = sB[w][tid];
-          sB[w][tid] = k;
-          k = s_last[w] ? b : fmaf(sA[w][tid], k, b);
-        }
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-          const float f = sF[w][tid];
-          sF[w][tid] = h;
-          h = s_first[w] ? f : fmaf(sA[w][tid], h, f);
-        }
-      }
+        });
+      });
     }
-    __syncthreads();
-
-    if (left > 0) {
-      // x becomes the state before each token
-      float h[4], k[4];
+    float k[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        h[e] = sF[wave][4 * lane + e];
-        k[e] = sB[wave][4 * lane + e];
-      }
-#pragma unroll
-      for (int s = 0; s < kTok; ++s) {
-        const bool st = first >> s & 1;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float now = st ? x[s][e] : fmaf(g[s][PH ? 0 : e], h[e], x[s][e]);
-          x[s][e] = st ? 0.f : h[e];
-          h[e] = now;
-        }
-      }
-      if (a.init) {
-        for (unsigned m = first; m; m &= m - 1) {
-          const int at = __builtin_ctz(m);
-          float h0[4];
-          load_init(a, __builtin_amdgcn_readlane(id_s, at), c, left, h0);
-#pragma unroll
-          for (int s = 0; s < kTok; ++s)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[s][e] = s == at ? h0[e] : x[s][e];
-        }
-      }
-#pragma unroll
-      for (int s = kTok - 1; s >= 0; --s) {
+    for (int e = 0; e < 4; ++e) k[e] = sB[wave][4 * lane + e];
+    segments_down(m, [&](int lo, int hi, bool started) {
+      if (m.last >> (hi - 1) & 1) load_dfinal(m.seq_last(hi - 1), k);
+      descend(lo, hi, [&](int s) {
         const int64_t t = tw + s;
-        const bool en = last >> s & 1;
-        const bool inside = t >= glo && t < ghi;
         float dh[4], dg[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          dh[e] = en ? dy[s][e] : dy[s][e] + k[e];
-          dg[e] = inside ? dh[e] * x[s][e] : 0.f;
-          k[e] = g[s][PH ? 0 : e] * dh[e];
-          if (!inside) dh[e] = 0.f;
+          dh[e] = to_f32((Tx)dy[s][e]) + k[e];
+          dg[e] = dh[e] * before[s][e];
+          k[e] = g[s][e] * dh[e];
         }
         if constexpr (PH) {
           // a head's D / 4 lanes (8, 16 or 32) lie next to each other
           float sum = (dg[0] + dg[1]) + (dg[2] + dg[3]);
           for (int o = 1; o < a.D / 4; o <<= 1) sum += __shfl_xor(sum, o);
-          if (t < a.T && (c % a.D) == 0)
-            ((Tg *)a.dg)[t * a.H + head] = from_f32<Tg>(sum);
-        } else if (t < a.T) {
+          if (c % a.D == 0) ((Tg *)a.dg)[t * a.H + head] = from_f32<Tg>(sum);
+        } else {
           store4<Tg, VEC>((Tg *)a.dg + t * a.C + c, left, dg);
         }
-        if (t < a.T) store4<Tx, VEC>((Tx *)a.dx + t * a.C + c, left, dh);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) dy[s][e] = k[e];  // the carry out of this token
-      }
-      if (a.dinit) {
-        for (unsigned m = first; m; m &= m - 1) {
-          const int at = __builtin_ctz(m);
-          pick(dy, at, k);
-          store_state(a.dinit, GDN_F32, (int64_t)__builtin_amdgcn_readlane(id_s, at) * a.C + c,
-                      left, k);
-        }
-      }
-    }
-    if (tile == 0 && a.dinit) {
-      for_empty_sequences(a, [&](int i) {
-        if (left > 0) {
-          float d[4] = {0.f, 0.f, 0.f, 0.f};
-          if (a.dfin) load_state(a.dfin, GDN_F32, (int64_t)i * a.C + c, left, d);
-          store_state(a.dinit, GDN_F32, (int64_t)i * a.C + c, left, d);
-        }
+        store4<Tx, VEC>((Tx *)a.dx + t * a.C + c, left, dh);
       });
-    }
-    if (!a.ticket) return;
+      if (a.dinit && started)
+        store_state(a.dinit, GDN_F32, (int64_t)m.seq_first(lo) * a.C + c, left, k);
+    });
+  }
+  if (tile == 0 && a.dinit) {
+    for_empty_sequences(a, [&](int i) {
+      if (left > 0) {
+        float d[4];
+        load_dfinal(i, d);
+        store_state(a.dinit, GDN_F32, (int64_t)i * a.C + c, left, d);
+      }
+    });
   }
 }
 
@@ -706,12 +742,13 @@ __global__ void __launch_bounds__(256) rec_decode_kernel(RecArgs a) {
   if (id >= (int64_t)per * a.N) return;
   const int i = (int)(id / per), c = 4 * (int)(id % per);
   const int left = min(4, a.C - c);
-  float x[4], g[PH ? 1 : 4], h[4];
-  load4<Tx, VEC>((const Tx *)a.x + i * a.x_stride + c, left, x);
-  load_gate<Tg, PH, VEC>(a, i, c, left, PH ? c / a.D : 0, g);
+  const V4<Tx> x = load4<Tx, VEC>((const Tx *)a.x + i * a.x_stride + c, left);
+  Gate<Tg, PH, VEC> g;
+  g.load((const Tg *)a.g + i * a.g_stride, c, left, PH ? c / a.D : 0);
+  float h[4];
   load_init(a, i, c, left, h);
 #pragma unroll
-  for (int e = 0; e < 4; ++e) h[e] = fmaf(g[PH ? 0 : e], h[e], x[e]);
+  for (int e = 0; e < 4; ++e) h[e] = fmaf(g[e], h[e], to_f32((Tx)x[e]));
   store4<Tx, VEC>((Tx *)a.out + (int64_t)i * a.C + c, left, h);
   if (a.fin) store_final(a, i, c, left, h);
 }
@@ -786,22 +823,15 @@ hipError_t dispatch(const RecArgs &a, hipStream_t s) {
 #undef GDN_REC_GO
 }
 
-// Workgroups of a scan: one per unit up to 8 per compute unit, which then take
-// further tickets.
-unsigned scan_grid(const RecArgs &a) {
-  const uint32_t most = 8u * (uint32_t)a.num_cus;
-  return a.ticket && a.units > most ? most : a.units;
-}
-
 template <typename Tx, typename Tg, bool PH, bool VEC> struct Fwd {
   static hipError_t go(const RecArgs &a, hipStream_t s) {
-    rec_forward_kernel<Tx, Tg, PH, VEC><<<dim3(scan_grid(a)), dim3(kThreads), 0, s>>>(a);
+    rec_forward_kernel<Tx, Tg, PH, VEC><<<dim3(a.units), dim3(kThreads), 0, s>>>(a);
     return hipGetLastError();
   }
 };
 template <typename Tx, typename Tg, bool PH, bool VEC> struct Bwd {
   static hipError_t go(const RecArgs &a, hipStream_t s) {
-    rec_backward_kernel<Tx, Tg, PH, VEC><<<dim3(scan_grid(a)), dim3(kThreads), 0, s>>>(a);
+    rec_backward_kernel<Tx, Tg, PH, VEC><<<dim3(a.units), dim3(kThreads), 0, s>>>(a);
     return hipGetLastError();
   }
 };
