@@ -16,6 +16,13 @@ int check_device(int *num_cus = nullptr);
 constexpr int kRecTile = 64;
 // Channels of one workgroup's tile: 64 lanes x 4.
 constexpr int kRecChannels = 256;
+// Tiles of one group of the chain, and the distance of two ticket counters
+// (each in a cache line of its own).
+constexpr int kGroup = 8;
+constexpr int kTicketStep = 32;
+__host__ __device__ constexpr int64_t groups_of(int64_t tiles) {
+  return (tiles + kGroup - 1) / kGroup;
+}
 
 struct RecArgs {
   int64_t T;
@@ -46,8 +53,9 @@ struct RecArgs {
   // tiles and their chain
   int32_t ntiles, ncb;
   uint32_t units;             // ntiles * ncb
-  uint32_t *ticket;           // next unit to take; NULL: one tile, unit = blockIdx.x
-  unsigned long long *words;  // [ntiles][C]
+  uint32_t *ticket;           // [ncb][kTicketStep] next tile of a channel block; NULL: one tile
+  unsigned long long *words;  // [ntiles][C], then
+  unsigned long long *groups; // [ceil(ntiles / kGroup)][C]
   int32_t *status;
   int32_t vec;  // every row of x, g, dy, out, dx, dg is a whole number of aligned 4-element groups
   int32_t num_cus;

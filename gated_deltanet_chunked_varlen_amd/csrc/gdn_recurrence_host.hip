@@ -61,7 +61,7 @@ struct RecLayout {
   bool chain, starts, own_chunk;
 };
 
-// The chain's ticket and words (more than one tile), the sequence starts of a
+// The chain's tickets and words (more than one tile), the sequence starts of a
 // batch that does not fit a wave's lanes, and the backward pass's states where
 // the caller kept none.
 RecLayout plan(const gdn_recurrence_params *p, bool backward) {
@@ -73,8 +73,9 @@ RecLayout plan(const gdn_recurrence_params *p, bool backward) {
   L.starts = p->num_seqs > kDirectSeqs;
   L.own_chunk = backward && !p->chunk_states && tiles > 1;
   if (L.chain) {
-    L.ticket = take(sizeof(uint32_t));
-    L.words = take((size_t)tiles * C * sizeof(unsigned long long));
+    const int64_t ncb = (C + kRecChannels - 1) / kRecChannels;
+    L.ticket = take((size_t)ncb * kTicketStep * sizeof(uint32_t));
+    L.words = take((size_t)(tiles + groups_of(tiles)) * C * sizeof(unsigned long long));
   }
   if (L.starts) L.bos = take(sizeof(int32_t) * ((size_t)p->num_seqs + 1));
   if (L.own_chunk) L.chunk = take((size_t)tiles * C * sizeof(float));
@@ -181,6 +182,7 @@ int run_scan(const gdn_recurrence_params *p, bool backward, hipStream_t s) {
   if (L.chain) {
     a.ticket = (uint32_t *)(ws + L.ticket);
     a.words = (unsigned long long *)(ws + L.words);
+    a.groups = a.words + (int64_t)a.ntiles * a.C;
   }
   if (L.starts) a.bos = bos = (int32_t *)(ws + L.bos);
   a.chunk = L.own_chunk ? (float *)(ws + L.chunk) : p->chunk_states;
