@@ -357,9 +357,12 @@ __device__ __forceinline__ void for_empty_sequences(const RecArgs &a, F f) {
   }
 }
 
-// The channel block of this workgroup and its place in the block's chain.
+// The channel block of this workgroup and its place in the block's chain.  One
+// round of workgroups after another starts one block further: workgroups go
+// to the eight XCDs in turn, so without the shift a block of a multiple-of-8
+// set would stay on one XCD (65 536 tokens x 16 blocks: 486 us against 410).
 __device__ __forceinline__ int take_place(const RecArgs &a, int &cb) {
-  cb = (int)(blockIdx.x % (unsigned)a.ncb);
+  cb = (int)((blockIdx.x + blockIdx.x / (unsigned)a.ncb) % (unsigned)a.ncb);
   if (!a.ticket) return 0;
   __shared__ int place;
   if (threadIdx.x == 0)
@@ -610,6 +613,19 @@ __global__ void __launch_bounds__(kThreads) rec_forward_kernel(RecArgs a) {
   }
 }
 
+// Sum over a head's D / 4 lanes (8, 16 or 32 next to each other) by lane moves
+// within the vector unit: neighbours, pairs, quads and eights of a row of 16
+// hold equal sums in turn, and a second row takes the first one's.  The last
+// lane of the head has the sum.
+__device__ __forceinline__ float head_sum(float x, int D) {
+  x += dpp_or_zero<0xB1>(x);   // quad_perm [1, 0, 3, 2]
+  x += dpp_or_zero<0x4E>(x);   // quad_perm [2, 3, 0, 1]
+  x += dpp_or_zero<0x141>(x);  // row_half_mirror: the other quad of eight
+  if (D >= 64) x += dpp_or_zero<0x140>(x);         // row_mirror: the other eight
+  if (D >= 128) x += dpp_or_zero<0x142, 0xA>(x);   // row_bcast:15 into rows 1 and 3
+  return x;
+}
+
 // ----------------------------------------------------------------- backward
 
 // One pass over x, g and dy: the states before each token are formed again
@@ -709,6 +725,8 @@ __global__ void __launch_bounds__(kThreads, 4) rec_backward_kernel(RecArgs a) {
   }
   __syncthreads();
 
+  // the last of a head's lanes writes its gate's gradient
+  const bool writes_head = PH && (lane & (a.D / 4 - 1)) == a.D / 4 - 1;
   // gradients of rows outside every sequence are zero
   if (m.lo > 0 || m.hi < kTok) {
     const float zero[4] = {0.f, 0.f, 0.f, 0.f};
@@ -717,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 4) rec_backward_kernel(RecArgs a) {
       if ((s < m.lo || s >= m.hi) && t < a.T && left > 0) {
         store4<Tx, VEC>((Tx *)a.dx + t * a.C + c, left, zero);
         if constexpr (PH) {
-          if (c % a.D == 0) ((Tg *)a.dg)[t * a.H + head] = from_f32<Tg>(0.f);
+          if (writes_head) ((Tg *)a.dg)[t * a.H + head] = from_f32<Tg>(0.f);
         } else {
           store4<Tg, VEC>((Tg *)a.dg + t * a.C + c, left, zero);
         }
@@ -764,10 +782,8 @@ __global__ void __launch_bounds__(kThreads, 4) rec_backward_kernel(RecArgs a) {
             k[e] = g[s][e] * dh[e];
           }
           if constexpr (PH) {
-            // a head's D / 4 lanes (8, 16 or 32) lie next to each other
-            float sum = (dg[0] + dg[1]) + (dg[2] + dg[3]);
-            for (int o = 1; o < a.D / 4; o <<= 1) sum += __shfl_xor(sum, o);
-            if (c % a.D == 0) ((Tg *)a.dg)[t * a.H + head] = from_f32<Tg>(sum);
+            const float sum = head_sum((dg[0] + dg[1]) + (dg[2] + dg[3]), a.D);
+            if (writes_head) ((Tg *)a.dg)[t * a.H + head] = from_f32<Tg>(sum);
           } else {
             store4<Tg, VEC>((Tg *)a.dg + t * a.C + c, left, dg);
           }
