@@ -14,6 +14,8 @@
 #include "gdn_internal.h"
 #include "gdn_recurrence.h"
 
+#include <type_traits>
+
 namespace gdn {
 
 namespace {
@@ -21,6 +23,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int64_t kUnitBytes = 64 << 10;
 constexpr int kMaxGroup = 16;  // short rows per unit
+constexpr int kBatch = 4;      // loads in flight per thread
 
 // Row numbers: the list entry, -1 for padding, -2 for entries outside the pool.
 __device__ __forceinline__ int list_row(const void *list, int type, int64_t i, int64_t pool) {
@@ -30,117 +33,125 @@ __device__ __forceinline__ int list_row(const void *list, int type, int64_t i, i
 
 // ------------------------------------------------------------ moving elements
 
-// Elements e0 .. e1 - 1 of a row (in the order d1, d2, d3), by the whole
-// workgroup.  src NULL: zeros.
-struct RowMover {
-  const PoolArgs &a;
+__device__ __forceinline__ int64_t row_offset(const int64_t *str, int64_t d2, int64_t d3,
+                                              int64_t e) {
+  const int64_t k = e % d3, r = e / d3;
+  return (r / d2) * str[1] + (r % d2) * str[2] + k * str[3];
+}
 
-  __device__ __forceinline__ static int64_t offset(const int64_t *str, int64_t d2, int64_t d3,
-                                                   int64_t e) {
-    const int64_t k = e % d3, r = e / d3;
-    return (r / d2) * str[1] + (r % d2) * str[2] + k * str[3];
+__host__ __device__ constexpr int elem_size(int dtype) {
+  return dtype == GDN_F32 ? 4 : dtype == GDN_BF16 || dtype == GDN_F16 ? 2 : 1;
+}
+
+__device__ __forceinline__ const char *src_row(const PoolArgs &a, int r) {
+  return (const char *)a.src + (int64_t)r * a.src_str[0] * elem_size(a.src_dtype);
+}
+__device__ __forceinline__ char *dst_row(const PoolArgs &a, int r) {
+  return (char *)a.dst + (int64_t)r * a.dst_str[0] * elem_size(a.dst_dtype);
+}
+
+// Bytes b0 .. b1 - 1 of a contiguous row by the whole workgroup, in vectors V:
+// copied, or (ZERO) cleared.  kBatch loads per thread are on their way before
+// the first store; `go` is asked in between, so that whatever decides whether
+// the row is written runs beside them.
+template <typename V, bool ZERO, typename F>
+__device__ __forceinline__ void move_bytes(const char *src, char *dst, int64_t b0, int64_t b1,
+                                           F go) {
+  constexpr int64_t step = sizeof(V) * kThreads;
+  int64_t b = b0 + (int64_t)sizeof(V) * threadIdx.x;
+  if constexpr (ZERO) {
+    if (!go()) return;
+    for (; b < b1; b += step) *(V *)(dst + b) = V{};
+    return;
   }
-
-  // contiguous rows of equal type: whole vectors, bit for bit
-  template <typename V>
-  __device__ __forceinline__ static void raw(const char *src, char *dst, int64_t b0, int64_t b1) {
-    constexpr int64_t W = sizeof(V);
-    const V zero{};
-    int64_t b = b0 + W * threadIdx.x;
-    constexpr int64_t step = W * kThreads;
-    for (; b + 7 * step < b1; b += 8 * step) {
-      V v[8];
+  V v[kBatch];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = src ? *(const V *)(src + b + i * step) : zero;
+  for (int i = 0; i < kBatch; ++i)
+    if (b + i * step < b1) v[i] = *(const V *)(src + b + i * step);
+  if (!go()) return;
+  for (;;) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) *(V *)(dst + b + i * step) = v[i];
-    }
-    for (; b < b1; b += step) *(V *)(dst + b) = src ? *(const V *)(src + b) : zero;
+    for (int i = 0; i < kBatch; ++i)
+      if (b + i * step < b1) *(V *)(dst + b + i * step) = v[i];
+    b += kBatch * step;
+    if (b - (int64_t)sizeof(V) * threadIdx.x >= b1) return;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (b + i * step < b1) v[i] = *(const V *)(src + b + i * step);
   }
+}
 
-  template <typename S, typename D>
-  __device__ __forceinline__ void strided(const S *src, D *dst, int64_t e0, int64_t e1) const {
+template <typename U, bool ZERO>
+__device__ __forceinline__ void move_strided(const PoolArgs &a, const U *src, U *dst, int64_t e0,
+                                             int64_t e1) {
+  for (int64_t e = e0 + threadIdx.x; e < e1; e += kThreads)
+    dst[row_offset(a.dst_str, a.d2, a.d3, e)] =
+        ZERO ? (U)0 : src[row_offset(a.src_str, a.d2, a.d3, e)];
+}
+
+// Elements e0 .. e1 - 1 of row s (ZERO: zeros) into row d of the same type, bit
+// for bit.
+template <bool ZERO, typename F>
+__device__ __forceinline__ void move_equal(const PoolArgs &a, int s, int d, int64_t e0, int64_t e1,
+                                           F go) {
+  const int es = elem_size(a.dst_dtype);
+  const char *src = ZERO ? nullptr : src_row(a, s);
+  char *dst = dst_row(a, d);
+  if (a.flat) {
+    if (a.align >= 16) move_bytes<u32x4, ZERO>(src, dst, e0 * es, e1 * es, go);
+    else if (es == 4) move_bytes<uint32_t, ZERO>(src, dst, e0 * es, e1 * es, go);
+    else if (es == 2) move_bytes<uint16_t, ZERO>(src, dst, e0 * es, e1 * es, go);
+    else move_bytes<uint8_t, ZERO>(src, dst, e0 * es, e1 * es, go);
+  } else if (go()) {
+    if (es == 4) move_strided<uint32_t, ZERO>(a, (const uint32_t *)src, (uint32_t *)dst, e0, e1);
+    else if (es == 2)
+      move_strided<uint16_t, ZERO>(a, (const uint16_t *)src, (uint16_t *)dst, e0, e1);
+    else move_strided<uint8_t, ZERO>(a, (const uint8_t *)src, (uint8_t *)dst, e0, e1);
+  }
+}
+
+// The same between two types, 16 bytes of the wider one per thread and step
+// where every row allows it.
+template <typename S, typename D, typename F>
+__device__ __forceinline__ void move_convert(const PoolArgs &a, int s, int d, int64_t e0,
+                                             int64_t e1, F go) {
+  const S *src = (const S *)src_row(a, s);
+  D *dst = (D *)dst_row(a, d);
+  constexpr int W = 16 / (sizeof(S) > sizeof(D) ? sizeof(S) : sizeof(D));
+  struct alignas(sizeof(S) * W) SV { S e[W]; };
+  struct alignas(sizeof(D) * W) DV { D e[W]; };
+  if (!a.flat || a.align < 16) {
+    if (!go()) return;
     for (int64_t e = e0 + threadIdx.x; e < e1; e += kThreads)
-      dst[offset(a.dst_str, a.d2, a.d3, e)] =
-          src ? from_f32<D>(to_f32(src[offset(a.src_str, a.d2, a.d3, e)])) : from_f32<D>(0.f);
+      dst[row_offset(a.dst_str, a.d2, a.d3, e)] =
+          from_f32<D>(to_f32(src[row_offset(a.src_str, a.d2, a.d3, e)]));
+    return;
   }
-  // equal types, strided: the bits
-  template <typename U>
-  __device__ __forceinline__ void strided_raw(const U *src, U *dst, int64_t e0, int64_t e1) const {
-    for (int64_t e = e0 + threadIdx.x; e < e1; e += kThreads)
-      dst[offset(a.dst_str, a.d2, a.d3, e)] =
-          src ? src[offset(a.src_str, a.d2, a.d3, e)] : (U)0;
-  }
-
-  // contiguous rows of two types: eight elements per thread and step where
-  // every row allows it
-  template <typename S, typename D>
-  __device__ __forceinline__ void convert(const S *src, D *dst, int64_t e0, int64_t e1) const {
-    if (!a.flat) return strided(src, dst, e0, e1);
-    int64_t e = e0;
-    if (a.align >= 16) {
-      const int64_t n8 = (e1 - e0) / 8;
-      for (int64_t i = threadIdx.x; i < n8; i += kThreads) {
-        S s[8];
-        D d[8];
-        __builtin_memcpy(s, __builtin_assume_aligned(src + e0 + 8 * i, sizeof(S) * 8 < 16 ? 8 : 16),
-                         sizeof(s));
+  // rows are whole 16-byte groups in both types, so W divides e0 and e1
+  const SV *sv = reinterpret_cast<const SV *>(src);
+  DV *dv = reinterpret_cast<DV *>(dst);
+  int64_t i = e0 / W + threadIdx.x;
+  const int64_t end = e1 / W;
+  SV v[kBatch];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) d[j] = from_f32<D>(to_f32(s[j]));
-        __builtin_memcpy(__builtin_assume_aligned(dst + e0 + 8 * i, sizeof(D) * 8 < 16 ? 8 : 16), d,
-                         sizeof(d));
-      }
-      e = e0 + 8 * n8;
+  for (int j = 0; j < kBatch; ++j)
+    if (i + j * kThreads < end) v[j] = sv[i + j * kThreads];
+  if (!go()) return;
+  for (;;) {
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      DV o;
+#pragma unroll
+      for (int w = 0; w < W; ++w) o.e[w] = from_f32<D>(to_f32(v[j].e[w]));
+      if (i + j * kThreads < end) dv[i + j * kThreads] = o;
     }
-    for (e += threadIdx.x; e < e1; e += kThreads) dst[e] = from_f32<D>(to_f32(src[e]));
+    i += kBatch * kThreads;
+    if (i - (int64_t)threadIdx.x >= end) return;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j)
+      if (i + j * kThreads < end) v[j] = sv[i + j * kThreads];
   }
-
-  template <typename S>
-  __device__ __forceinline__ void from(const S *src, char *dst, int64_t e0, int64_t e1) const {
-    switch (a.dst_dtype) {
-      case GDN_F32: return convert(src, (float *)dst, e0, e1);
-      case GDN_BF16: return convert(src, (bf16 *)dst, e0, e1);
-      case GDN_F16: return convert(src, (f16 *)dst, e0, e1);
-      case GDN_FP8_E4M3: return convert(src, (fp8e4m3 *)dst, e0, e1);
-      default: return convert(src, (fp8e5m2 *)dst, e0, e1);
-    }
-  }
-
-  __device__ __forceinline__ static int size(int dtype) {
-    return dtype == GDN_F32 ? 4 : dtype == GDN_BF16 || dtype == GDN_F16 ? 2 : 1;
-  }
-
-  // s < 0: zeros
-  __device__ __forceinline__ void move(int s, int d, int64_t e0, int64_t e1) const {
-    const int ds = size(a.dst_dtype);
-    const char *src =
-        s < 0 ? nullptr : (const char *)a.src + (int64_t)s * a.src_str[0] * size(a.src_dtype);
-    char *dst = (char *)a.dst + (int64_t)d * a.dst_str[0] * ds;
-    if (!src || a.src_dtype == a.dst_dtype) {
-      if (!a.flat) {
-        if (ds == 4) strided_raw((const uint32_t *)src, (uint32_t *)dst, e0, e1);
-        else if (ds == 2) strided_raw((const uint16_t *)src, (uint16_t *)dst, e0, e1);
-        else strided_raw((const uint8_t *)src, (uint8_t *)dst, e0, e1);
-      } else if (a.align >= 16) {
-        raw<u32x4>(src, dst, e0 * ds, e1 * ds);
-      } else if (ds == 4) {
-        raw<uint32_t>(src, dst, e0 * ds, e1 * ds);
-      } else if (ds == 2) {
-        raw<uint16_t>(src, dst, e0 * ds, e1 * ds);
-      } else {
-        raw<uint8_t>(src, dst, e0 * ds, e1 * ds);
-      }
-      return;
-    }
-    switch (a.src_dtype) {
-      case GDN_F32: return from((const float *)src, dst, e0, e1);
-      case GDN_BF16: return from((const bf16 *)src, dst, e0, e1);
-      case GDN_F16: return from((const f16 *)src, dst, e0, e1);
-      case GDN_FP8_E4M3: return from((const fp8e4m3 *)src, dst, e0, e1);
-      default: return from((const fp8e5m2 *)src, dst, e0, e1);
-    }
-  }
-};
+}
 
 // Units of a call: `group` entries by one slice of `slice` elements each.
 struct Units {
@@ -210,51 +221,103 @@ __device__ __forceinline__ void list_status(const PoolArgs &a, unsigned *map) {
   if (threadIdx.x == 0) a.status[0] = (int32_t)s_bits;
 }
 
+// Entry j (destination dj) keeps entry i (source si, destination di) from
+// acting.
+__device__ __forceinline__ bool conflict(const PoolArgs &a, int64_t j, int dj, int64_t i, int si,
+                                         int di) {
+  return (j > i && dj == di) || (a.same && j != i && dj == si && si != di);
+}
+
+// Some entry of the list keeps entry i from acting; for the whole workgroup.
+__device__ __forceinline__ bool skipped(const PoolArgs &a, int64_t i, int si, int di) {
+  bool hit = false;
+  for (int64_t j = threadIdx.x; j < a.count; j += kThreads) {
+    const int d = list_row(a.dst_rows, a.rows_type, j, a.dst_pool);
+    const int s = list_row(a.src_rows, a.rows_type, j, a.src_pool);
+    if (d >= 0 && s >= 0) hit |= conflict(a, j, d, i, si, di);
+  }
+  return __syncthreads_or(hit) != 0;
+}
+
 // Which entries act: entry i is skipped if a later entry has its destination,
 // or (in one pool) if another entry's destination is its source.  Entries with
 // a row outside its pool take no part.
-template <bool ZERO>
-__global__ void __launch_bounds__(kThreads) pool_copy_kernel(PoolArgs a, Units u) {
+//
+// MOVE::row moves elements of a row; MOVE::kZero: there are no sources.
+template <typename MOVE>
+__global__ void __launch_bounds__(kThreads) pool_list_kernel(PoolArgs a, Units u) {
   extern __shared__ unsigned map[];
   if (a.status && blockIdx.x == gridDim.x - 1) return list_status(a, map);
   const int64_t workers = (int64_t)gridDim.x - (a.status ? 1 : 0);
+  constexpr bool kZero = MOVE::kZero;
+  if (u.group == 1) {
+    // long rows: one entry at a time, its rows read as scalars
+    int64_t seen = -1;
+    int src = -1, dst = -1;
+    for (int64_t unit = blockIdx.x; unit < u.total; unit += workers) {
+      const int64_t i = unit / u.slices, e0 = (unit % u.slices) * u.slice;
+      const int64_t e1 = e0 + u.slice < a.row ? e0 + u.slice : a.row;
+      const bool fresh = i != seen;
+      if (fresh) {
+        seen = i;
+        dst = list_row(a.dst_rows, a.rows_type, i, a.dst_pool);
+        src = kZero ? 0 : list_row(a.src_rows, a.rows_type, i, a.src_pool);
+      }
+      if (dst < 0 || src < 0) continue;
+      bool act = true;
+      MOVE::row(a, src, dst, e0, e1, [&]() {
+        if (!kZero && fresh) act = !skipped(a, i, src, dst);
+        return act;
+      });
+      if (!act) dst = -1;
+    }
+    return;
+  }
   __shared__ int s_src[kMaxGroup], s_dst[kMaxGroup], s_skip[kMaxGroup];
-  const RowMover m{a};
-  int64_t seen = -1;
   for (int64_t unit = blockIdx.x; unit < u.total; unit += workers) {
-    const int64_t grp = unit / u.slices, e0 = (unit % u.slices) * u.slice;
-    const int64_t e1 = e0 + u.slice < a.row ? e0 + u.slice : a.row;
-    const int64_t i0 = grp * u.group;
+    // short rows: a group of entries, each whole
+    const int64_t i0 = unit * u.group;
     const int n = (int)(a.count - i0 < u.group ? a.count - i0 : u.group);
-    if (grp != seen) {
-      seen = grp;
-      __syncthreads();
-      if ((int)threadIdx.x < n) {
-        const int d = list_row(a.dst_rows, a.rows_type, i0 + threadIdx.x, a.dst_pool);
-        const int s = ZERO ? 0 : list_row(a.src_rows, a.rows_type, i0 + threadIdx.x, a.src_pool);
-        s_src[threadIdx.x] = s;
-        s_dst[threadIdx.x] = d;
-        s_skip[threadIdx.x] = d < 0 || s < 0;
+    __syncthreads();
+    if ((int)threadIdx.x < n) {
+      const int d = list_row(a.dst_rows, a.rows_type, i0 + threadIdx.x, a.dst_pool);
+      const int s = kZero ? 0 : list_row(a.src_rows, a.rows_type, i0 + threadIdx.x, a.src_pool);
+      s_src[threadIdx.x] = s;
+      s_dst[threadIdx.x] = d;
+      s_skip[threadIdx.x] = d < 0 || s < 0;
+    }
+    __syncthreads();
+    if (!kZero) {
+      for (int64_t j = threadIdx.x; j < a.count; j += kThreads) {
+        const int d = list_row(a.dst_rows, a.rows_type, j, a.dst_pool);
+        const int s = list_row(a.src_rows, a.rows_type, j, a.src_pool);
+        if (d < 0 || s < 0) continue;
+        for (int p = 0; p < n; ++p)
+          if (conflict(a, j, d, i0 + p, s_src[p], s_dst[p])) s_skip[p] = 1;
       }
       __syncthreads();
-      if (!ZERO) {
-        for (int64_t j = threadIdx.x; j < a.count; j += kThreads) {
-          const int d = list_row(a.dst_rows, a.rows_type, j, a.dst_pool);
-          const int s = list_row(a.src_rows, a.rows_type, j, a.src_pool);
-          if (d < 0 || s < 0) continue;
-          for (int p = 0; p < n; ++p) {
-            const bool later = j > i0 + p && d == s_dst[p];
-            const bool over = a.same && j != i0 + p && d == s_src[p] && s_src[p] != s_dst[p];
-            if (later || over) s_skip[p] = 1;
-          }
-        }
-        __syncthreads();
-      }
     }
     for (int p = 0; p < n; ++p)
-      if (!s_skip[p]) m.move(ZERO ? -1 : s_src[p], s_dst[p], e0, e1);
+      if (!s_skip[p]) MOVE::row(a, s_src[p], s_dst[p], 0, a.row, []() { return true; });
   }
 }
+
+template <bool ZERO> struct MoveEqual {
+  static constexpr bool kZero = ZERO;
+  template <typename F>
+  __device__ __forceinline__ static void row(const PoolArgs &a, int s, int d, int64_t e0,
+                                             int64_t e1, F go) {
+    move_equal<ZERO>(a, s, d, e0, e1, go);
+  }
+};
+template <typename S, typename D> struct MoveConvert {
+  static constexpr bool kZero = false;
+  template <typename F>
+  __device__ __forceinline__ static void row(const PoolArgs &a, int s, int d, int64_t e0,
+                                             int64_t e1, F go) {
+    move_convert<S, D>(a, s, d, e0, e1, go);
+  }
+};
 
 // -------------------------------------------------------------------- compact
 
@@ -366,7 +429,6 @@ __global__ void __launch_bounds__(kThreads) pool_compact_kernel(PoolArgs a, Unit
     if (a.status) a.status[0] = (int32_t)s_bits;
   }
 
-  const RowMover mv{a};
   for (int64_t unit = blockIdx.x; unit < u.total; unit += gridDim.x) {
     const int64_t grp = unit / u.slices, e0 = (unit % u.slices) * u.slice;
     const int64_t e1 = e0 + u.slice < a.row ? e0 + u.slice : a.row;
@@ -379,7 +441,8 @@ __global__ void __launch_bounds__(kThreads) pool_compact_kernel(PoolArgs a, Unit
       s_dst[tid] = hole_row((int)k0 + tid);
     }
     __syncthreads();
-    for (int p = 0; p < cnt; ++p) mv.move(s_src[p], s_dst[p], e0, e1);
+    for (int p = 0; p < cnt; ++p)
+      move_equal<false>(a, s_src[p], s_dst[p], e0, e1, []() { return true; });
   }
 }
 
@@ -389,17 +452,44 @@ static size_t status_map_bytes(const PoolArgs &a) {
   return a.status ? (size_t)((a.dst_pool + 31) / 32) * 4 : 0;
 }
 
-template <bool ZERO>
+template <typename MOVE>
 static hipError_t launch_list(const PoolArgs &a, hipStream_t s) {
   const Units u = cut(a, a.count);
   const unsigned grid = unit_grid(a, u) + (a.status ? 1u : 0u);
   if (grid == 0) return hipSuccess;
-  pool_copy_kernel<ZERO><<<dim3(grid), dim3(kThreads), status_map_bytes(a), s>>>(a, u);
+  pool_list_kernel<MOVE><<<dim3(grid), dim3(kThreads), status_map_bytes(a), s>>>(a, u);
   return hipGetLastError();
 }
 
-hipError_t launch_pool_copy(const PoolArgs &a, hipStream_t s) { return launch_list<false>(a, s); }
-hipError_t launch_pool_reset(const PoolArgs &a, hipStream_t s) { return launch_list<true>(a, s); }
+template <typename S, typename D>
+static hipError_t launch_types(const PoolArgs &a, hipStream_t s) {
+  if constexpr (std::is_same<S, D>::value) return launch_list<MoveEqual<false>>(a, s);
+  else return launch_list<MoveConvert<S, D>>(a, s);
+}
+
+template <typename S>
+static hipError_t launch_from(const PoolArgs &a, hipStream_t s) {
+  switch (a.dst_dtype) {
+    case GDN_F32: return launch_types<S, float>(a, s);
+    case GDN_BF16: return launch_types<S, bf16>(a, s);
+    case GDN_F16: return launch_types<S, f16>(a, s);
+    case GDN_FP8_E4M3: return launch_types<S, fp8e4m3>(a, s);
+    default: return launch_types<S, fp8e5m2>(a, s);
+  }
+}
+
+hipError_t launch_pool_copy(const PoolArgs &a, hipStream_t s) {
+  switch (a.src_dtype) {
+    case GDN_F32: return launch_from<float>(a, s);
+    case GDN_BF16: return launch_from<bf16>(a, s);
+    case GDN_F16: return launch_from<f16>(a, s);
+    case GDN_FP8_E4M3: return launch_from<fp8e4m3>(a, s);
+    default: return launch_from<fp8e5m2>(a, s);
+  }
+}
+hipError_t launch_pool_reset(const PoolArgs &a, hipStream_t s) {
+  return launch_list<MoveEqual<true>>(a, s);
+}
 
 hipError_t launch_pool_compact(const PoolArgs &a, hipStream_t s) {
   // a mover lies at or behind the new end and its hole before it
