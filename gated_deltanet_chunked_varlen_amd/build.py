@@ -1,7 +1,8 @@
 """Build libgdn_prefill.so in-tree with hipcc for gfx950.
 
 Each source compiles to its own object in parallel, then one link step makes
-the shared library.
+the shared library.  _calls.so, the CPython module that marshals the
+recurrence's and the state pool's calls, is host code against torch's headers.
 
 Usage: python -m gated_deltanet_chunked_varlen_amd.build
 """
@@ -26,6 +27,30 @@ FLAGS = [
     # keep packed fp32 instructions out of device code
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
 ]
+
+
+CALLS = os.path.join(HERE, "_calls.so")
+CXX = os.environ.get("CXX", "g++")
+
+
+def build_calls(verbose: bool = False, out: str = CALLS) -> str:
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+    tmp = out + ".tmp%d" % os.getpid()
+    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI)]
+    cmd += ["-isystem" + p for p in include_paths() + [sysconfig.get_paths()["include"]]]
+    cmd += [os.path.join(CSRC, "torch_calls.cpp"), "-o", tmp]
+    cmd += ["-L" + p for p in library_paths()] + ["-ltorch_python", "-ltorch_cpu", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("%s failed on torch_calls.cpp:\n%s" % (CXX, r.stderr))
+    os.replace(tmp, out)
+    return out
 
 
 def _clean(stderr: str) -> str:
@@ -66,3 +91,4 @@ def build(verbose: bool = False, extra_flags=None, out: str = LIB) -> str:
 
 if __name__ == "__main__":
     print(build(verbose=True))
+    print(build_calls(verbose=True))
