@@ -55,8 +55,9 @@ def gated_linear_recurrence(x, g, initial_state=None, output_final_state=False, 
     States are [N or pool, H, D] in any state dtype, rows may be strided; with
     ``state_indices`` [N] sequence i starts from ``initial_state`` row
     state_indices[i] and leaves its final state in that row of
-    ``output_state``, which may be ``initial_state`` itself.  h is fp32
-    throughout.
+    ``output_state``, which may be ``initial_state`` itself; rows must then be
+    unique (sequences may share a start row where no final state is written).
+    h is fp32 throughout.  ``output`` may be x itself.
 
     Returns ``output`` [T, H, D] (rows outside every sequence are not
     written), then the final state with ``output_final_state``, then with

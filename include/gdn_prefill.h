@@ -313,7 +313,9 @@ int gdn_build_chunk_indices(const void *cu_seqlens, int32_t cu_type,
  * other tensor is contiguous.  States are [rows, H, D] in any state dtype
  * with a row stride in elements (0 = contiguous); the 8-bit types saturate.
  * cu_seqlens, num_seqs, state_indices, pool_size and status are those of
- * gdn_prefill_params; output_state may be the same memory as initial_state.
+ * gdn_prefill_params; output_state may be the same memory as initial_state,
+ * and state_indices must be unique where a final state is written.  output may
+ * be x itself (contiguous); no other two tensors of a call may overlap.
  * Rows of output outside every sequence are untouched.  An empty sequence's
  * final state is its initial state.  A sequence whose state index is out of
  * range starts from zero and writes no final state.

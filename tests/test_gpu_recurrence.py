@@ -275,6 +275,71 @@ def test_strided_tokens(dtype, gate, off, pad):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("off", [0, 1, 4])
+def test_strided_head_gates(off):
+    """Head gates as columns of a wider projection, x off a vector boundary."""
+    lens = [90, 45]
+    d = R.make(12, lens, 3, 64, F16, F32, True)
+    ref = _both(d, lens)
+    gw = torch.full((135, 11), float("nan"), device="cuda")
+    gw[:, off:off + 3] = d["g"]
+    xw = torch.full((135, 200), float("nan"), dtype=F16, device="cuda")
+    xw[:, off:off + 192] = d["x"].reshape(135, 192)
+    got = _both(dict(d, g=gw[:, off:off + 3], x=xw[:, off:off + 192].unflatten(1, (3, 64))), lens)
+    for a, b in zip(ref, got):
+        assert torch.equal(a, b)
+
+
+def test_thousands_of_sequences():
+    """More sequences than a workgroup has threads, most of them empty, several
+    ending in one tile, long runs of empty ones."""
+    rng = np.random.default_rng(1)
+    lens = rng.integers(0, 3, 3000)
+    lens[rng.random(3000) < 0.6] = 0
+    lens[1000:2200] = 0
+    lens[2300] = 150
+    lens = lens.tolist()
+    d = R.make(13, lens, 1, 40)
+    _both(d, lens)
+
+
+def test_output_in_place_of_x():
+    lens = [100, 300]
+    d = R.make(14, lens, 3, 32, BF16)
+    want = gated_linear_recurrence(d["x"], d["g"], initial_state=d["h0"], cu_seqlens=d["cu"])
+    x = d["x"].clone()
+    got = gated_linear_recurrence(x, d["g"], initial_state=d["h0"], cu_seqlens=d["cu"], output=x)
+    assert got is x and torch.equal(got, want)
+
+
+def test_sequences_that_share_a_start_row():
+    """Without a final state several sequences may start from one pool row."""
+    lens = [10, 70, 5]
+    d = R.make(15, lens, 2, 32)
+    pool = torch.randn((4, 2, 32), device="cuda")
+    idx = torch.tensor([2, 2, 0], dtype=torch.int32, device="cuda")
+    out = gated_linear_recurrence(d["x"], d["g"], initial_state=pool, cu_seqlens=d["cu"],
+                                  state_indices=idx)
+    h, err, _, _ = R.forward(R.f64(d["x"]), R.f64(d["g"]), lens, R.f64(pool)[[2, 2, 0]])
+    R.check("out", out, h, err, F32)
+
+
+def test_workspace_of_the_caller():
+    """A workspace that holds anything, reused by calls of other shapes."""
+    ws = torch.randint(0, 256, (1 << 22,), dtype=torch.uint8, device="cuda")
+    for lens, seed in (([700, 20], 16), ([5] * 100, 17), ([130], 18)):
+        d = R.make(seed, lens, 3, 32)
+        ref = _run_all(d)
+        out, fin, kept = gated_linear_recurrence(
+            d["x"], d["g"], initial_state=d["h0"], output_final_state=True, cu_seqlens=d["cu"],
+            return_chunk_states=True, workspace=ws)
+        got = (out, fin) + gated_linear_recurrence_backward(
+            d["dy"], d["x"], d["g"], initial_state=d["h0"], dfinal_state=d["dfinal"],
+            cu_seqlens=d["cu"], output_dinitial_state=True, workspace=ws)
+        for a, b in zip(ref, got):
+            assert torch.equal(a, b)
+
+
 def test_strided_pool_rows():
     """One layer's slice of a [rows, layers, H, D] pool."""
     lens = [30, 70]

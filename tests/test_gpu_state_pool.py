@@ -263,6 +263,45 @@ def test_compact_repeated_and_invalid_entries():
     assert new.tolist() == renamed and _same(pool, want)
 
 
+def test_pools_without_rows_and_empty_lists():
+    pool, none = torch.empty((0, 4), device="cuda"), _rows([])
+    st = _status()
+    assert state_pool_copy(pool, none, none) is pool
+    state_pool_reset(pool, _rows([-1]), status=st)
+    assert st.item() == 0
+    new, n = state_pool_compact(pool, _rows([-1, 3]), status=st)
+    assert n.item() == 0 and new.tolist() == [-1, 3] and st.item() == OUT
+    with pytest.raises(ValueError):
+        state_pool_copy(pool, _rows([0]), _rows([0]))
+    full = _pool(15, (3, 4), F32)
+    want = full.clone()
+    state_pool_copy(full, none, none, status=st)
+    assert st.item() == 0
+    new, n = state_pool_compact(full, none)
+    assert n.item() == 0 and new.numel() == 0 and _same(full, want)
+
+
+def test_rows_of_every_alignment():
+    """Rows of odd lengths at odd offsets: no access leaves its row."""
+    for dtype in (F32, BF16, E4M3):
+        for n in (1, 2, 3, 4, 8, 12, 15, 16, 17, 64, 100):
+            for off in (0, 1, 2, 4, 8):
+                base = _convert(torch.arange(5 * n + off + 3) % 7 + 1.0, dtype).cuda()
+                pool = base[off:off + 5 * n].view(5, n)
+                want = base.clone()
+                want[off + 3 * n:off + 4 * n] = base[off + n:off + 2 * n]
+                state_pool_copy(pool, _rows([1]), _rows([3]))
+                want[off:off + n] = torch.zeros(n, device="cuda").to(dtype)
+                state_pool_reset(pool, _rows([0]))
+                assert _same(base, want), (dtype, n, off)
+                wide = torch.full((4 * n + off + 2,), 9.0, device="cuda")
+                want = wide.clone()
+                want[off + 2 * n:off + 3 * n] = pool[3].float()
+                state_pool_copy(wide[off:off + 4 * n].view(4, n), _rows([3]), _rows([2]),
+                                src_pool=pool)
+                assert torch.equal(wide, want), (dtype, n, off)
+
+
 def test_compact_several_pools_alike():
     a, b = _pool(15, (20, 2, 32, 32), F32), _pool(16, (20, 3, 64), BF16)
     big = _pool(17, (20, 2, 8), F16)
