@@ -12,8 +12,12 @@ namespace gdn {
 // GDN_OK if the current device is a gfx950; reports its CU count (gdn_host.hip).
 int check_device(int *num_cus = nullptr);
 
-// Tokens of one workgroup's tile in the recurrence scans.
+// Tokens of one workgroup's tile in the backward scan, and in the forward scan
+// by its types (eight times k6_recurrence.hip's tokens per wave).
 constexpr int kRecTile = 64;
+constexpr int rec_forward_tile(int x_dtype, int g_dtype, int per_head) {
+  return x_dtype != GDN_F32 && (per_head || g_dtype != GDN_F32) ? 2 * kRecTile : kRecTile;
+}
 // Channels of one workgroup's tile: 64 lanes x 4.
 constexpr int kRecChannels = 256;
 // Tiles of one group of the chain, and the distance of two ticket counters
@@ -43,7 +47,7 @@ struct RecArgs {
   const void *sidx;
   int32_t sidx_type;
   int64_t pool_rows;
-  float *chunk;  // [ceil(T / 64)][C] state before each tile, or NULL
+  float *chunk;  // [ceil(T / 64)][C] state before every 64 tokens, or NULL
   // backward
   const void *dy;
   int64_t dy_stride;

@@ -29,8 +29,10 @@ bool aligned(const void *p, int64_t n) { return (uintptr_t)p % (uintptr_t)n == 0
 
 enum Mode { kForward = 0, kBackward = 1, kDecode = 2 };
 
-int64_t tiles_of(const gdn_recurrence_params *p) {
-  return std::max<int64_t>(1, (p->total_tokens + kRecTile - 1) / kRecTile);
+int64_t tiles_of(const gdn_recurrence_params *p, bool backward) {
+  const int64_t tile =
+      backward ? kRecTile : rec_forward_tile(p->x_dtype, p->g_dtype, p->g_per_head);
+  return std::max<int64_t>(1, (p->total_tokens + tile - 1) / tile);
 }
 
 int check_shape(const gdn_recurrence_params *p, int mode) {
@@ -46,7 +48,7 @@ int check_shape(const gdn_recurrence_params *p, int mode) {
     if (!p->cu_seqlens && p->num_seqs != 1) return GDN_ERR_SHAPE;
     const int64_t ncb = (C + kRecChannels - 1) / kRecChannels;
     // one workgroup per unit; a grid holds fewer than 2^32 threads
-    if (tiles_of(p) * ncb > kMaxUnits) return GDN_ERR_SHAPE;
+    if (tiles_of(p, true) * ncb > kMaxUnits) return GDN_ERR_SHAPE;
   }
   if (!float_type(p->x_dtype)) return GDN_ERR_DTYPE;
   if (p->g_dtype != GDN_F32 && p->g_dtype != p->x_dtype) return GDN_ERR_DTYPE;
@@ -66,7 +68,7 @@ struct RecLayout {
 // the caller kept none.
 RecLayout plan(const gdn_recurrence_params *p, bool backward) {
   RecLayout L{};
-  const int64_t C = (int64_t)p->num_heads * p->head_size, tiles = tiles_of(p);
+  const int64_t C = (int64_t)p->num_heads * p->head_size, tiles = tiles_of(p, backward);
   size_t off = 0;
   auto take = [&](size_t bytes) { size_t o = off; off = align_up(off + bytes); return o; };
   L.chain = tiles > 1;
@@ -78,6 +80,7 @@ RecLayout plan(const gdn_recurrence_params *p, bool backward) {
     L.words = take((size_t)(tiles + groups_of(tiles)) * C * sizeof(unsigned long long));
   }
   if (L.starts) L.bos = take(sizeof(int32_t) * ((size_t)p->num_seqs + 1));
+  // rows of 64 tokens, the backward pass's tiles
   if (L.own_chunk) L.chunk = take((size_t)tiles * C * sizeof(float));
   L.total = off;
   return L;
@@ -159,9 +162,7 @@ void fill(const gdn_recurrence_params *p, int num_cus, RecArgs &a) {
   a.pool_rows = p->pool_size;
   a.status = p->status;
   a.num_cus = num_cus;
-  a.ntiles = (int32_t)tiles_of(p);
   a.ncb = (int32_t)((C + kRecChannels - 1) / kRecChannels);
-  a.units = (uint32_t)a.ntiles * (uint32_t)a.ncb;
 }
 
 // Every row of the tensor is whole aligned groups of four elements.
@@ -179,21 +180,27 @@ int run_scan(const gdn_recurrence_params *p, bool backward, hipStream_t s) {
   fill(p, num_cus, a);
   const int64_t C = a.C, xs = size_of(p->x_dtype), gs = size_of(p->g_dtype);
   int32_t *bos = nullptr;
-  if (L.chain) {
-    a.ticket = (uint32_t *)(ws + L.ticket);
-    a.words = (unsigned long long *)(ws + L.words);
-    a.groups = a.words + (int64_t)a.ntiles * a.C;
-  }
+  // a pass's tiles, and its chain where there is more than one
+  auto cut = [&](RecArgs &r, bool back) {
+    r.ntiles = (int32_t)tiles_of(p, back);
+    r.units = (uint32_t)r.ntiles * (uint32_t)r.ncb;
+    if (r.ntiles > 1) {
+      r.ticket = (uint32_t *)(ws + L.ticket);
+      r.words = (unsigned long long *)(ws + L.words);
+      r.groups = r.words + (int64_t)r.ntiles * r.C;
+    }
+  };
   if (L.starts) a.bos = bos = (int32_t *)(ws + L.bos);
   a.chunk = L.own_chunk ? (float *)(ws + L.chunk) : p->chunk_states;
   a.vec = C % 4 == 0 && rows_vec(p->x, a.x_stride, xs) &&
           (p->g_per_head || rows_vec(p->g, a.g_stride, gs));
   hipError_t e = hipSuccess;
-  auto prepare = [&]() {
-    if (e == hipSuccess && (L.chain || L.starts)) e = launch_rec_prepare(a, bos, s);
+  auto prepare = [&](const RecArgs &r) {
+    if (e == hipSuccess && (r.ticket || L.starts)) e = launch_rec_prepare(r, bos, s);
   };
   if (!backward || L.own_chunk) {
     RecArgs f = a;
+    cut(f, false);
     if (!backward) {
       f.out = p->output;
       f.vec = f.vec && rows_vec(p->output, C, xs);
@@ -203,7 +210,7 @@ int run_scan(const gdn_recurrence_params *p, bool backward, hipStream_t s) {
         f.fin_stride = p->output_state_stride ? p->output_state_stride : C;
       }
     }
-    prepare();
+    prepare(f);
     if (e == hipSuccess) e = launch_rec_forward(f, s);
   }
   if (backward) {
@@ -215,7 +222,8 @@ int run_scan(const gdn_recurrence_params *p, bool backward, hipStream_t s) {
     a.dinit = p->dinitial_state;
     a.vec = a.vec && rows_vec(p->doutput, a.dy_stride, xs) && rows_vec(p->dx, C, xs) &&
             (p->g_per_head || rows_vec(p->dg, C, gs));
-    prepare();
+    cut(a, true);
+    prepare(a);
     if (e == hipSuccess) e = launch_rec_backward(a, s);
   }
   return e == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH;

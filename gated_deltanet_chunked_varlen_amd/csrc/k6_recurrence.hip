@@ -1,9 +1,9 @@
 // k6_recurrence.hip -- the gated linear recurrence h_t = g_t h_{t-1} + x_t:
 // forward scan, backward scan and decode step.
 //
-// A tile is 64 tokens x 256 channels, one workgroup of eight waves: wave w
-// holds tokens 8 w .. 8 w + 7 of all 256 channels in registers, four channels
-// per lane, so that x and g are read from memory once.  Over a run of tokens
+// A tile is 64 (or 128) tokens x 256 channels, one workgroup of eight waves:
+// wave w holds tokens 8 w .. 8 w + 7 (16 w .. 16 w + 15) of all 256 channels in
+// registers, four channels per lane, so that x and g are read from memory once.  Over a run of tokens
 // the recurrence is the affine map h -> A h + B (A the product of the gates, B
 // the run's last state from zero), and maps compose, so a tile takes
 //   1. each wave: its (A, B), from registers                       (sweep 1)
@@ -51,8 +51,7 @@ namespace gdn {
 
 namespace {
 
-constexpr int kTok = 8;                     // tokens per wave
-constexpr int kWaves = kRecTile / kTok;     // waves per workgroup
+constexpr int kWaves = 8;                   // waves per workgroup
 constexpr int kThreads = 64 * kWaves;
 constexpr int kWindow = 8;                  // groups looked back over
 constexpr unsigned kPending = 0xFFFFFFFFu, kLast = 0xFFFFFFFEu;
@@ -280,20 +279,24 @@ __device__ __forceinline__ float opaque(float x) {
 
 // ----------------------------------------------------------------- geometry
 
-struct TileGeo {
-  int lo, hi;             // tokens that belong to a sequence
-  int start[kRecTile];    // sequence that starts at this token of the tile, or -1
-  int end[kRecTile];      // sequence that ends with it, or -1
+template <int TOK> struct TileGeo {
+  static constexpr int kTile = kWaves * TOK;
+  int lo, hi;         // tokens that belong to a sequence
+  int start[kTile];   // sequence that starts at this token of the tile, or -1
+  int end[kTile];     // sequence that ends with it, or -1
+  int first[kWaves];  // each wave's Marks::first and last
+  int last[kWaves];
 };
 
 // Marks of the tile that starts at token t0, by the whole workgroup.  The
 // first tile's channel block 0 of a small batch writes the status word.
+template <int TOK>
 __device__ __forceinline__ void tile_geometry(const RecArgs &a, int t0, bool status_unit,
-                                              TileGeo &G) {
+                                              TileGeo<TOK> &G) {
   const int tid = threadIdx.x, lane = tid & 63;
-  if (tid < kRecTile) G.start[tid] = G.end[tid] = -1;
+  if (tid < G.kTile) G.start[tid] = G.end[tid] = -1;
   __syncthreads();
-  const int t1 = t0 + kRecTile;
+  const int t1 = t0 + G.kTile;
   if (!a.bos) {
     if (tid < 64) {
       const SeqLane s = seq_lane(a.cu, a.cu_type, a.N, a.T, lane);
@@ -386,59 +389,58 @@ template <typename Tg, bool VEC> struct Gate<Tg, true, VEC> {
   __device__ __forceinline__ float operator[](int) const { return to_f32(v); }
 };
 
-// The marks of a tile's tokens as wave-uniform bits, and of a wave's: tokens
-// that start and end a sequence, and those that belong to one, [lo, hi).
-struct Marks {
-  unsigned long long firsts, lasts;  // the tile's 64 tokens
-  unsigned first, last;              // this wave's
+// The marks of a wave's tokens as wave-uniform bits: tokens that start and end
+// a sequence, and those that belong to one, [lo, hi).
+template <int TOK> struct Marks {
+  unsigned first, last;
   int lo, hi;
-  int id_first, id_last;  // lane i: sequence that starts / ends at the tile's token i
-  int base;               // the wave's first token within the tile
+  int id_first, id_last;  // lane s: sequence that starts / ends at token s
 
-  __device__ __forceinline__ void read(const TileGeo &G, int t0, int wave, int lane) {
-    id_first = G.start[lane];
-    id_last = G.end[lane];
-    firsts = __ballot(id_first >= 0);
-    lasts = __ballot(id_last >= 0);
-    base = wave * kTok;
-    first = wave_first(wave);
-    last = wave_last(wave);
-    lo = __builtin_amdgcn_readfirstlane(min(max(G.lo - t0 - base, 0), kTok));
-    hi = __builtin_amdgcn_readfirstlane(min(max(G.hi - t0 - base, 0), kTok));
-  }
-  __device__ __forceinline__ unsigned wave_first(int w) const {
-    return (unsigned)(firsts >> (w * kTok)) & ((1u << kTok) - 1);
-  }
-  __device__ __forceinline__ unsigned wave_last(int w) const {
-    return (unsigned)(lasts >> (w * kTok)) & ((1u << kTok) - 1);
+  __device__ __forceinline__ void read(TileGeo<TOK> &G, int t0, int wave, int lane) {
+    const int base = wave * TOK;
+    id_first = G.start[base + (lane & (TOK - 1))];
+    id_last = G.end[base + (lane & (TOK - 1))];
+    first = (unsigned)__ballot(id_first >= 0) & ((1u << TOK) - 1);
+    last = (unsigned)__ballot(id_last >= 0) & ((1u << TOK) - 1);
+    lo = __builtin_amdgcn_readfirstlane(min(max(G.lo - t0 - base, 0), TOK));
+    hi = __builtin_amdgcn_readfirstlane(min(max(G.hi - t0 - base, 0), TOK));
+    if (lane == 0) {
+      G.first[wave] = (int)first;
+      G.last[wave] = (int)last;
+    }
   }
   // no sequence starts or ends here, and every token belongs to one
   __device__ __forceinline__ bool plain() const {
-    return (first | last) == 0 && lo == 0 && hi == kTok;
+    return (first | last) == 0 && lo == 0 && hi == TOK;
   }
   // the wave's last token that starts a sequence
   __device__ __forceinline__ int last_first() const { return 31 - __builtin_clz(first); }
   // sequence that starts / ends at this wave's token s
   __device__ __forceinline__ int seq_first(int s) const {
-    return __builtin_amdgcn_readlane(id_first, base + s);
+    return __builtin_amdgcn_readlane(id_first, s);
   }
   __device__ __forceinline__ int seq_last(int s) const {
-    return __builtin_amdgcn_readlane(id_last, base + s);
+    return __builtin_amdgcn_readlane(id_last, s);
   }
 };
 
+// Bit w: wave w of the tile has a mark of this kind (after a barrier).
+__device__ __forceinline__ unsigned marked_waves(const int (&marks)[kWaves], int lane) {
+  return (unsigned)__ballot(marks[lane & (kWaves - 1)] != 0) & ((1u << kWaves) - 1);
+}
+
 // f(s) for the tokens s of [lo, hi), ascending or descending.  The bounds are
 // wave-uniform, so the conditions are scalar branches.
-template <typename F>
+template <int TOK, typename F>
 __device__ __forceinline__ void ascend(int lo, int hi, F f) {
 #pragma unroll
-  for (int s = 0; s < kTok; ++s)
+  for (int s = 0; s < TOK; ++s)
     if (s >= lo && s < hi) f(s);
 }
-template <typename F>
+template <int TOK, typename F>
 __device__ __forceinline__ void descend(int lo, int hi, F f) {
 #pragma unroll
-  for (int s = kTok - 1; s >= 0; --s)
+  for (int s = TOK - 1; s >= 0; --s)
     if (s >= lo && s < hi) f(s);
 }
 
@@ -446,8 +448,8 @@ __device__ __forceinline__ void descend(int lo, int hi, F f) {
 // sequence, else f(std::false_type): the sweeps of most waves then are straight
 // code without a condition (packed batch of 23 060 x 4096 with head gates: half
 // of all instructions issued were scalar ones for the marks).
-template <typename F>
-__device__ __forceinline__ void by_marks(const Marks &m, F f) {
+template <int TOK, typename F>
+__device__ __forceinline__ void by_marks(const Marks<TOK> &m, F f) {
   if (m.plain()) f(std::true_type{});
   else f(std::false_type{});
 }
@@ -456,9 +458,9 @@ __device__ __forceinline__ void by_marks(const Marks &m, F f) {
 // of the wave's last sequence start, which sweep 2 must not read again: in a
 // pool worked on in place, another wave may have written that sequence's final
 // state over it by then.
-template <typename Tx, bool PLAIN, typename GateT>
-__device__ __forceinline__ void forward_map(const RecArgs &a, const Marks &m,
-                                            const V4<Tx> (&x)[kTok], const GateT (&g)[kTok], int c,
+template <typename Tx, bool PLAIN, int TOK, typename GateT>
+__device__ __forceinline__ void forward_map(const RecArgs &a, const Marks<TOK> &m,
+                                            const V4<Tx> (&x)[TOK], const GateT (&g)[TOK], int c,
                                             int left, float (&A)[4], float (&B)[4],
                                             float (&h0)[4]) {
   int lo = PLAIN ? 0 : m.lo;
@@ -473,7 +475,7 @@ __device__ __forceinline__ void forward_map(const RecArgs &a, const Marks &m,
     A[e] = 1.f;
     B[e] = h0[e];
   }
-  ascend(lo, PLAIN ? kTok : m.hi, [&](int s) {
+  ascend<TOK>(lo, PLAIN ? TOK : m.hi, [&](int s) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float gg = g[s][e];
@@ -485,7 +487,8 @@ __device__ __forceinline__ void forward_map(const RecArgs &a, const Marks &m,
 
 // The state before token s, which starts a sequence.  Every start of the wave
 // but the last has its sequence end in this wave too, after this read.
-__device__ __forceinline__ void start_state(const RecArgs &a, const Marks &m, int s, int c,
+template <int TOK>
+__device__ __forceinline__ void start_state(const RecArgs &a, const Marks<TOK> &m, int s, int c,
                                             int left, const float (&h0)[4], float (&h)[4]) {
   if (s == m.last_first()) {
 #pragma unroll
@@ -497,9 +500,9 @@ __device__ __forceinline__ void start_state(const RecArgs &a, const Marks &m, in
 
 // f(lo, hi, started): the wave's segments in order, `started` where the first
 // token starts a sequence.
-template <bool PLAIN, typename F>
-__device__ __forceinline__ void segments_up(const Marks &m, F f) {
-  if (PLAIN) return f(0, kTok, false);
+template <bool PLAIN, int TOK, typename F>
+__device__ __forceinline__ void segments_up(const Marks<TOK> &m, F f) {
+  if (PLAIN) return f(0, TOK, false);
   unsigned first = m.first;
   int lo = m.lo;
   bool started = false;
@@ -513,9 +516,9 @@ __device__ __forceinline__ void segments_up(const Marks &m, F f) {
   }
 }
 // The same from the last to the first.
-template <bool PLAIN, typename F>
-__device__ __forceinline__ void segments_down(const Marks &m, F f) {
-  if (PLAIN) return f(0, kTok, false);
+template <bool PLAIN, int TOK, typename F>
+__device__ __forceinline__ void segments_down(const Marks<TOK> &m, F f) {
+  if (PLAIN) return f(0, TOK, false);
   unsigned first = m.first;
   int hi = m.hi;
   while (first) {
@@ -529,12 +532,24 @@ __device__ __forceinline__ void segments_down(const Marks &m, F f) {
 
 // ------------------------------------------------------------------ forward
 
+// Tokens per wave: 16 where x and the gates take few registers (head gates or
+// 16-bit gates on 16-bit x), else 8.  Twice the bytes per workgroup halve the
+// chain's traffic and its share of a tile's time; with fp32 gates or fp32 x 16
+// tokens would leave one workgroup per CU instead of two.
+template <typename T> constexpr int code() {
+  return sizeof(T) == 4 ? GDN_F32 : std::is_same<T, bf16>::value ? GDN_BF16 : GDN_F16;
+}
+template <typename Tx, typename Tg, bool PH> constexpr int forward_tokens() {
+  return rec_forward_tile(code<Tx>(), code<Tg>(), PH) / kWaves;
+}
+
 // Bounded by HBM: per element x and g are read once and out written once; the
 // chain adds 8 bytes per tile and channel each for clearing, publishing twice
 // and looking back.
 template <typename Tx, typename Tg, bool PH, bool VEC>
 __global__ void __launch_bounds__(kThreads, 4) rec_forward_kernel(RecArgs a) {
-  __shared__ TileGeo G;
+  constexpr int TOK = forward_tokens<Tx, Tg, PH>();
+  __shared__ TileGeo<TOK> G;
   __shared__ float sA[kWaves][kRecChannels], sB[kWaves][kRecChannels];
   // what is the same for a wave's lanes is kept in scalar registers
   const int tid = threadIdx.x, lane = tid & 63;
@@ -542,16 +557,16 @@ __global__ void __launch_bounds__(kThreads, 4) rec_forward_kernel(RecArgs a) {
   int cb;
   const int tile = take_place(a, cb);
   const int T = (int)a.T;
-  const int t0 = tile * kRecTile, tw = t0 + wave * kTok;
+  const int t0 = tile * G.kTile, tw = t0 + wave * TOK;
   const int c = cb * kRecChannels + 4 * lane;
   const int left = min(4, a.C - c);
   const int head = PH ? min(c, a.C - 1) / a.D : 0;
 
-  V4<Tx> x[kTok];
-  Gate<Tg, PH, VEC> g[kTok];
+  V4<Tx> x[TOK];
+  Gate<Tg, PH, VEC> g[TOK];
   if (left > 0) {
 #pragma unroll
-    for (int s = 0; s < kTok; ++s) {
+    for (int s = 0; s < TOK; ++s) {
       if (tw + s < T) {
         const int64_t t = tw + s;
         x[s] = load4<Tx, VEC>((const Tx *)a.x + t * a.x_stride + c, left);
@@ -560,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 4) rec_forward_kernel(RecArgs a) {
     }
   }
   tile_geometry(a, t0, tile == 0 && cb == 0, G);
-  Marks m;
+  Marks<TOK> m;
   m.read(G, t0, wave, lane);
   float h0[4];
   by_marks(m, [&](auto plain) {
@@ -571,28 +586,29 @@ __global__ void __launch_bounds__(kThreads, 4) rec_forward_kernel(RecArgs a) {
   });
   __syncthreads();
 
+  // (before the branches: every lane of the wave takes part)
+  const unsigned resets = marked_waves(G.first, lane);
   if (tid < kRecChannels) {
     const int ch = cb * kRecChannels + tid;
     if (ch < a.C) {
       float A = 1.f, B = 0.f, h = 0.f;
-      bool reset = false;
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) {
-        const bool r = m.wave_first(w) != 0;
-        B = r ? sB[w][tid] : fmaf(sA[w][tid], B, sB[w][tid]);
+        B = resets >> w & 1 ? sB[w][tid] : fmaf(sA[w][tid], B, sB[w][tid]);
         A *= sA[w][tid];
-        reset |= r;
       }
       if (a.ticket) {
-        h = chain(a, tile, ch, -1, Map{A, B, reset});
+        h = chain(a, tile, ch, -1, Map{A, B, resets != 0});
         reread_lds();
       }
-      if (a.chunk) a.chunk[(int64_t)tile * a.C + ch] = h;
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) {
+        const int tb = t0 + w * TOK;
+        if (w * TOK % GDN_RECURRENCE_CHUNK == 0 && a.chunk && tb < T)
+          a.chunk[(int64_t)(tb / GDN_RECURRENCE_CHUNK) * a.C + ch] = h;
         const float b = sB[w][tid], aa = sA[w][tid];
         sB[w][tid] = h;
-        h = m.wave_first(w) ? b : fmaf(aa, h, b);
+        h = resets >> w & 1 ? b : fmaf(aa, h, b);
       }
     }
   }
@@ -606,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 4) rec_forward_kernel(RecArgs a) {
       constexpr bool P = decltype(plain)::value;
       segments_up<P>(m, [&](int lo, int hi, bool started) {
         if (!P && started) start_state(a, m, lo, c, left, h0, h);
-        ascend(lo, hi, [&](int s) {
+        ascend<TOK>(lo, hi, [&](int s) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) h[e] = fmaf(g[s][e], h[e], to_f32((Tx)x[s][e]));
           if (a.out) store4<Tx, VEC>((Tx *)a.out + (int64_t)(tw + s) * a.C + c, left, h);
@@ -645,23 +661,24 @@ __device__ __forceinline__ float head_sum(float x, int D) {
 // comes through the chain from the tiles behind.  Bounded by HBM.
 template <typename Tx, typename Tg, bool PH, bool VEC>
 __global__ void __launch_bounds__(kThreads, 4) rec_backward_kernel(RecArgs a) {
-  __shared__ TileGeo G;
+  constexpr int TOK = 8;
+  __shared__ TileGeo<TOK> G;
   __shared__ float sA[kWaves][kRecChannels], sF[kWaves][kRecChannels], sB[kWaves][kRecChannels];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int cb;
   const int tile = a.ntiles - 1 - take_place(a, cb);
   const int T = (int)a.T;
-  const int t0 = tile * kRecTile, tw = t0 + wave * kTok;
+  const int t0 = tile * G.kTile, tw = t0 + wave * TOK;
   const int c = cb * kRecChannels + 4 * lane;
   const int left = min(4, a.C - c);
   const int head = PH ? min(c, a.C - 1) / a.D : 0;
 
-  V4<Tx> x[kTok], dy[kTok];
-  Gate<Tg, PH, VEC> g[kTok];
+  V4<Tx> x[TOK], dy[TOK];
+  Gate<Tg, PH, VEC> g[TOK];
   if (left > 0) {
 #pragma unroll
-    for (int s = 0; s < kTok; ++s) {
+    for (int s = 0; s < TOK; ++s) {
       if (tw + s < T) {
         const int64_t t = tw + s;
         x[s] = load4<Tx, VEC>((const Tx *)a.x + t * a.x_stride + c, left);
@@ -671,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 4) rec_backward_kernel(RecArgs a) {
     }
   }
   tile_geometry(a, t0, tile == 0 && cb == 0, G);
-  Marks m;
+  Marks<TOK> m;
   m.read(G, t0, wave, lane);
   float h0[4];
   auto load_dfinal = [&](int i, float (&k)[4]) {
@@ -684,14 +701,14 @@ __global__ void __launch_bounds__(kThreads, 4) rec_backward_kernel(RecArgs a) {
     float A[4], F[4], B[4], P[4] = {1.f, 1.f, 1.f, 1.f};
     forward_map<Tx, PL>(a, m, x, g, c, left, A, F, h0);
     // the map of the carry: over all tokens, or up to the first sequence end
-    int hi = PL ? kTok : m.hi;
+    int hi = PL ? TOK : m.hi;
 #pragma unroll
     for (int e = 0; e < 4; ++e) B[e] = 0.f;
     if (!PL && m.last) {
       hi = __builtin_ctz(m.last) + 1;
       load_dfinal(m.seq_last(hi - 1), B);
     }
-    descend(PL ? 0 : m.lo, hi, [&](int s) {
+    descend<TOK>(PL ? 0 : m.lo, hi, [&](int s) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float gg = g[s][e];
@@ -705,34 +722,32 @@ __global__ void __launch_bounds__(kThreads, 4) rec_backward_kernel(RecArgs a) {
   });
   __syncthreads();
 
+  const unsigned firsts = marked_waves(G.first, lane), lasts = marked_waves(G.last, lane);
   if (tid < kRecChannels) {
     const int ch = cb * kRecChannels + tid;
     if (ch < a.C) {
       float A = 1.f, B = 0.f, k = 0.f;
-      bool reset = false;
 #pragma unroll
       for (int w = kWaves - 1; w >= 0; --w) {
-        const bool r = m.wave_last(w) != 0;
-        B = r ? sB[w][tid] : fmaf(sA[w][tid], B, sB[w][tid]);
+        B = lasts >> w & 1 ? sB[w][tid] : fmaf(sA[w][tid], B, sB[w][tid]);
         A *= sA[w][tid];
-        reset |= r;
       }
       if (a.ticket) {
-        k = chain(a, tile, ch, 1, Map{A, B, reset});
+        k = chain(a, tile, ch, 1, Map{A, B, lasts != 0});
         reread_lds();
       }
-      float h = a.chunk ? a.chunk[(int64_t)tile * a.C + ch] : 0.f;
+      float h = a.chunk && t0 < T ? a.chunk[(int64_t)tile * a.C + ch] : 0.f;
 #pragma unroll
       for (int w = kWaves - 1; w >= 0; --w) {
         const float b = sB[w][tid];
         sB[w][tid] = k;
-        k = m.wave_last(w) ? b : fmaf(sA[w][tid], k, b);
+        k = lasts >> w & 1 ? b : fmaf(sA[w][tid], k, b);
       }
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) {
         const float f = sF[w][tid];
         sF[w][tid] = h;
-        h = m.wave_first(w) ? f : fmaf(sA[w][tid], h, f);
+        h = firsts >> w & 1 ? f : fmaf(sA[w][tid], h, f);
       }
     }
   }
@@ -741,9 +756,9 @@ __global__ void __launch_bounds__(kThreads, 4) rec_backward_kernel(RecArgs a) {
   // the last of a head's lanes writes its gate's gradient
   const bool writes_head = PH && (lane & (a.D / 4 - 1)) == a.D / 4 - 1;
   // gradients of rows outside every sequence are zero
-  if (m.lo > 0 || m.hi < kTok) {
+  if (m.lo > 0 || m.hi < TOK) {
     const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < kTok; ++s) {
+    for (int s = 0; s < TOK; ++s) {
       const int64_t t = tw + s;
       if ((s < m.lo || s >= m.hi) && t < a.T && left > 0) {
         store4<Tx, VEC>((Tx *)a.dx + t * a.C + c, left, zero);
@@ -766,7 +781,7 @@ __global__ void __launch_bounds__(kThreads, 4) rec_backward_kernel(RecArgs a) {
       constexpr bool PL = decltype(plain)::value;
 #pragma unroll
     for (int half = 1; half >= 0; --half) {
-      constexpr int kHalf = kTok / 2;
+      constexpr int kHalf = TOK / 2;
       const int s0 = half * kHalf, s1 = s0 + kHalf;
       float before[kHalf][4], h[4];
 #pragma unroll
@@ -774,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 4) rec_backward_kernel(RecArgs a) {
       segments_up<PL>(m, [&](int lo, int hi, bool started) {
         if (lo >= s1) return;
         if (!PL && started) start_state(a, m, lo, c, left, h0, h);
-        ascend(lo, hi, [&](int s) {
+        ascend<TOK>(lo, hi, [&](int s) {
           if (s >= s1) return;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -786,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 4) rec_backward_kernel(RecArgs a) {
       segments_down<PL>(m, [&](int lo, int hi, bool started) {
         if (lo >= s1 || hi <= s0) return;
         if (!PL && hi <= s1 && (m.last >> (hi - 1) & 1)) load_dfinal(m.seq_last(hi - 1), k);
-        descend(lo, hi, [&](int s) {
+        descend<TOK>(lo, hi, [&](int s) {
           if (s < s0 || s >= s1) return;
           const int64_t t = tw + s;
           float dh[4], dg[4];
