@@ -61,6 +61,7 @@ __device__ __forceinline__ void move_bytes(const char *src, char *dst, int64_t b
   int64_t b = b0 + (int64_t)sizeof(V) * threadIdx.x;
   if constexpr (ZERO) {
     if (!go()) return;
+#pragma unroll 4
     for (; b < b1; b += step) *(V *)(dst + b) = V{};
     return;
   }
@@ -84,6 +85,7 @@ __device__ __forceinline__ void move_bytes(const char *src, char *dst, int64_t b
 template <typename U, bool ZERO>
 __device__ __forceinline__ void move_strided(const PoolArgs &a, const U *src, U *dst, int64_t e0,
                                              int64_t e1) {
+#pragma unroll 1
   for (int64_t e = e0 + threadIdx.x; e < e1; e += kThreads)
     dst[row_offset(a.dst_str, a.d2, a.d3, e)] =
         ZERO ? (U)0 : src[row_offset(a.src_str, a.d2, a.d3, e)];
@@ -122,6 +124,7 @@ __device__ __forceinline__ void move_convert(const PoolArgs &a, int s, int d, in
   struct alignas(sizeof(D) * W) DV { D e[W]; };
   if (!a.flat || a.align < 16) {
     if (!go()) return;
+#pragma unroll 1
     for (int64_t e = e0 + threadIdx.x; e < e1; e += kThreads)
       dst[row_offset(a.dst_str, a.d2, a.d3, e)] =
           from_f32<D>(to_f32(src[row_offset(a.src_str, a.d2, a.d3, e)]));
@@ -156,14 +159,13 @@ __device__ __forceinline__ void move_convert(const PoolArgs &a, int s, int d, in
 // Units of a call: `group` entries by one slice of `slice` elements each.
 struct Units {
   int group;
-  int64_t slice, slices, groups;
-  int64_t total;  // groups * slices
+  int64_t slice;
+  unsigned slices, total;  // slices of a row; units in all, below 2^31
 };
 
 Units cut(const PoolArgs &a, int64_t entries) {
-  const int64_t big = a.src ? (a.src_dtype == GDN_F32 ? 4 : a.src_dtype <= GDN_F16 ? 2 : 1) : 0;
-  const int64_t ds = a.dst_dtype == GDN_F32 ? 4 : a.dst_dtype <= GDN_F16 ? 2 : 1;
-  const int64_t es = big > ds ? big : ds;
+  const int ss = a.src ? elem_size(a.src_dtype) : 0, ds = elem_size(a.dst_dtype);
+  const int64_t es = ss > ds ? ss : ds;
   Units u;
   // slices of whole 16-byte groups in any type: multiples of 16 elements
   u.slice = kUnitBytes / es;
@@ -173,19 +175,21 @@ Units cut(const PoolArgs &a, int64_t entries) {
     // no fewer units than two per compute unit for the sake of larger ones
     const int64_t spread = entries / (2 * (int64_t)a.num_cus);
     int64_t g = fit < spread ? fit : spread;
-    u.group = (int)(g < 1 ? 1 : g > kMaxGroup ? kMaxGroup : g);
+    u.group = (int)(g < 1 || !a.src ? 1 : g > kMaxGroup ? kMaxGroup : g);
   } else {
     u.group = 1;
   }
-  u.slices = (a.row + u.slice - 1) / u.slice;
-  u.groups = (entries + u.group - 1) / u.group;
-  u.total = u.groups * u.slices;
+  const int64_t groups = (entries + u.group - 1) / u.group;
+  auto slices = [&]() { return (a.row + u.slice - 1) / u.slice; };
+  while (groups * slices() > INT32_MAX) u.slice *= 2;
+  u.slices = (unsigned)slices();
+  u.total = (unsigned)(groups * u.slices);
   return u;
 }
 
 unsigned unit_grid(const PoolArgs &a, const Units &u) {
-  const int64_t most = 16 * (int64_t)a.num_cus;
-  return (unsigned)(u.total < most ? u.total : most);
+  const unsigned most = 16u * (unsigned)a.num_cus;
+  return u.total < most ? u.total : most;
 }
 
 // ---------------------------------------------------------------- copy, reset
@@ -248,14 +252,15 @@ template <typename MOVE>
 __global__ void __launch_bounds__(kThreads) pool_list_kernel(PoolArgs a, Units u) {
   extern __shared__ unsigned map[];
   if (a.status && blockIdx.x == gridDim.x - 1) return list_status(a, map);
-  const int64_t workers = (int64_t)gridDim.x - (a.status ? 1 : 0);
+  const unsigned workers = gridDim.x - (a.status ? 1u : 0u);
   constexpr bool kZero = MOVE::kZero;
-  if (u.group == 1) {
-    // long rows: one entry at a time, its rows read as scalars
+  if (kZero || u.group == 1) {
+    // long rows (and zeroed ones, which have no list to check): one entry at a
+    // time, its rows read as scalars
     int64_t seen = -1;
     int src = -1, dst = -1;
-    for (int64_t unit = blockIdx.x; unit < u.total; unit += workers) {
-      const int64_t i = unit / u.slices, e0 = (unit % u.slices) * u.slice;
+    for (unsigned unit = blockIdx.x; unit < u.total; unit += workers) {
+      const int64_t i = unit / u.slices, e0 = unit % u.slices * u.slice;
       const int64_t e1 = e0 + u.slice < a.row ? e0 + u.slice : a.row;
       const bool fresh = i != seen;
       if (fresh) {
@@ -264,39 +269,41 @@ __global__ void __launch_bounds__(kThreads) pool_list_kernel(PoolArgs a, Units u
         src = kZero ? 0 : list_row(a.src_rows, a.rows_type, i, a.src_pool);
       }
       if (dst < 0 || src < 0) continue;
-      bool act = true;
-      MOVE::row(a, src, dst, e0, e1, [&]() {
-        if (!kZero && fresh) act = !skipped(a, i, src, dst);
-        return act;
-      });
-      if (!act) dst = -1;
+      if constexpr (kZero) {
+        MOVE::row(a, src, dst, e0, e1, []() { return true; });
+      } else {
+        bool act = true;
+        MOVE::row(a, src, dst, e0, e1, [&]() {
+          if (fresh) act = !skipped(a, i, src, dst);
+          return act;
+        });
+        if (!act) dst = -1;
+      }
     }
     return;
   }
   __shared__ int s_src[kMaxGroup], s_dst[kMaxGroup], s_skip[kMaxGroup];
-  for (int64_t unit = blockIdx.x; unit < u.total; unit += workers) {
+  for (unsigned unit = blockIdx.x; unit < u.total; unit += workers) {
     // short rows: a group of entries, each whole
-    const int64_t i0 = unit * u.group;
+    const int64_t i0 = (int64_t)unit * u.group;
     const int n = (int)(a.count - i0 < u.group ? a.count - i0 : u.group);
     __syncthreads();
     if ((int)threadIdx.x < n) {
       const int d = list_row(a.dst_rows, a.rows_type, i0 + threadIdx.x, a.dst_pool);
-      const int s = kZero ? 0 : list_row(a.src_rows, a.rows_type, i0 + threadIdx.x, a.src_pool);
+      const int s = list_row(a.src_rows, a.rows_type, i0 + threadIdx.x, a.src_pool);
       s_src[threadIdx.x] = s;
       s_dst[threadIdx.x] = d;
       s_skip[threadIdx.x] = d < 0 || s < 0;
     }
     __syncthreads();
-    if (!kZero) {
-      for (int64_t j = threadIdx.x; j < a.count; j += kThreads) {
-        const int d = list_row(a.dst_rows, a.rows_type, j, a.dst_pool);
-        const int s = list_row(a.src_rows, a.rows_type, j, a.src_pool);
-        if (d < 0 || s < 0) continue;
-        for (int p = 0; p < n; ++p)
-          if (conflict(a, j, d, i0 + p, s_src[p], s_dst[p])) s_skip[p] = 1;
-      }
-      __syncthreads();
+    for (int64_t j = threadIdx.x; j < a.count; j += kThreads) {
+      const int d = list_row(a.dst_rows, a.rows_type, j, a.dst_pool);
+      const int s = list_row(a.src_rows, a.rows_type, j, a.src_pool);
+      if (d < 0 || s < 0) continue;
+      for (int p = 0; p < n; ++p)
+        if (conflict(a, j, d, i0 + p, s_src[p], s_dst[p])) s_skip[p] = 1;
     }
+    __syncthreads();
     for (int p = 0; p < n; ++p)
       if (!s_skip[p]) MOVE::row(a, s_src[p], s_dst[p], 0, a.row, []() { return true; });
   }
@@ -347,7 +354,9 @@ __device__ __forceinline__ int nth_bit(unsigned x, int k) {
 // Every workgroup forms the plan for itself in LDS: a bitmap of the live rows
 // and, per 32-row word, how many rows before it are live behind the new end
 // (movers) or free before it (holes).  The k-th mover and the k-th hole then
-// are two searches.  One launch, and nothing to hand over between workgroups.
+// are two searches.  One launch, and nothing to hand over between workgroups
+// (a planning launch of its own would cost more than the few microseconds that
+// each workgroup spends here).
 __global__ void __launch_bounds__(kThreads) pool_compact_kernel(PoolArgs a, Units u, int nwords) {
   extern __shared__ unsigned map[];  // live bits
   int *movers = (int *)(map + nwords), *holes = movers + nwords;
@@ -364,32 +373,48 @@ __global__ void __launch_bounds__(kThreads) pool_compact_kernel(PoolArgs a, Unit
     else if (r == -2) atomicOr(&s_bits, GDN_STATUS_POOL_ROW);
   }
   __syncthreads();
-  // a thread owns `per` consecutive words
-  const int per = (nwords + kThreads - 1) / kThreads;
-  const int w0 = min(tid * per, nwords), w1 = min(w0 + per, nwords);
-  int n = 0;
-  for (int w = w0; w < w1; ++w) n += __popc(map[w]);
-  block_prefix(n, sh);
-  const int m = sh[0];
+  int m = 0, moves = 0;
   auto before = [&](int w) -> unsigned {  // the word's bits of rows before m
     const int k = m - 32 * w;
     return k >= 32 ? ~0u : k <= 0 ? 0u : (1u << k) - 1u;
   };
-  int nm = 0, nh = 0;
-  for (int w = w0; w < w1; ++w) {
-    nm += __popc(map[w] & ~before(w));
-    nh += __popc(~map[w] & before(w));
+  if (nwords <= 64) {
+    // up to 2 048 rows: every wave forms the whole plan, a word per lane, and
+    // writes it for itself (the waves write the same values): no barriers
+    const int w = tid & 63;
+    const unsigned live = w < nwords ? map[w] : 0u;
+    m = __builtin_amdgcn_readlane(wave_prefix_sum_i(__popc(live)), 63);
+    const int both = __popc(live & ~before(w)) | (w < nwords ? __popc(~live & before(w)) << 16 : 0);
+    const int inc = wave_prefix_sum_i(both);
+    moves = __builtin_amdgcn_readlane(inc, 63) & 0xFFFF;
+    if (w < nwords) {
+      movers[w] = (inc - both) & 0xFFFF;
+      holes[w] = (inc - both) >> 16;
+    }
+  } else {
+    // a thread owns `per` consecutive words
+    const int per = (nwords + kThreads - 1) / kThreads;
+    const int w0 = min(tid * per, nwords), w1 = min(w0 + per, nwords);
+    int n = 0;
+    for (int w = w0; w < w1; ++w) n += __popc(map[w]);
+    block_prefix(n, sh);
+    m = sh[0];
+    int nm = 0, nh = 0;
+    for (int w = w0; w < w1; ++w) {
+      nm += __popc(map[w] & ~before(w));
+      nh += __popc(~map[w] & before(w));
+    }
+    int pm = block_prefix(nm, sh);
+    moves = sh[0];
+    int ph = block_prefix(nh, sh);
+    for (int w = w0; w < w1; ++w) {
+      movers[w] = pm;
+      holes[w] = ph;
+      pm += __popc(map[w] & ~before(w));
+      ph += __popc(~map[w] & before(w));
+    }
+    __syncthreads();
   }
-  int pm = block_prefix(nm, sh);
-  const int moves = sh[0];
-  int ph = block_prefix(nh, sh);
-  for (int w = w0; w < w1; ++w) {
-    movers[w] = pm;
-    holes[w] = ph;
-    pm += __popc(map[w] & ~before(w));
-    ph += __popc(~map[w] & before(w));
-  }
-  __syncthreads();
   // last word whose count of earlier rows is <= k, and the row in it
   auto word_of = [&](const int *pre, int k) {
     int lo = 0, hi = nwords - 1;
@@ -429,11 +454,16 @@ __global__ void __launch_bounds__(kThreads) pool_compact_kernel(PoolArgs a, Unit
     if (a.status) a.status[0] = (int32_t)s_bits;
   }
 
-  for (int64_t unit = blockIdx.x; unit < u.total; unit += gridDim.x) {
-    const int64_t grp = unit / u.slices, e0 = (unit % u.slices) * u.slice;
+  const auto always = []() { return true; };
+  for (unsigned unit = blockIdx.x; unit < u.total; unit += gridDim.x) {
+    const int64_t k0 = (int64_t)(unit / u.slices) * u.group, e0 = unit % u.slices * u.slice;
     const int64_t e1 = e0 + u.slice < a.row ? e0 + u.slice : a.row;
-    const int64_t k0 = grp * u.group;
     if (k0 >= moves) break;  // units of one group after another: none left
+    if (u.group == 1) {
+      move_equal<false>(a, __builtin_amdgcn_readfirstlane(mover_row((int)k0)),
+                        __builtin_amdgcn_readfirstlane(hole_row((int)k0)), e0, e1, always);
+      continue;
+    }
     const int cnt = (int)(moves - k0 < u.group ? moves - k0 : u.group);
     __syncthreads();
     if (tid < cnt) {
@@ -441,8 +471,7 @@ __global__ void __launch_bounds__(kThreads) pool_compact_kernel(PoolArgs a, Unit
       s_dst[tid] = hole_row((int)k0 + tid);
     }
     __syncthreads();
-    for (int p = 0; p < cnt; ++p)
-      move_equal<false>(a, s_src[p], s_dst[p], e0, e1, []() { return true; });
+    for (int p = 0; p < cnt; ++p) move_equal<false>(a, s_src[p], s_dst[p], e0, e1, always);
   }
 }
 
@@ -455,7 +484,7 @@ static size_t status_map_bytes(const PoolArgs &a) {
 template <typename MOVE>
 static hipError_t launch_list(const PoolArgs &a, hipStream_t s) {
   const Units u = cut(a, a.count);
-  const unsigned grid = unit_grid(a, u) + (a.status ? 1u : 0u);
+  const unsigned grid = unit_grid(a, u) + (a.status ? 1u : 0u);  // one for the status word
   if (grid == 0) return hipSuccess;
   pool_list_kernel<MOVE><<<dim3(grid), dim3(kThreads), status_map_bytes(a), s>>>(a, u);
   return hipGetLastError();
