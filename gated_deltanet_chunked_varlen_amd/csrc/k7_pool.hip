@@ -10,6 +10,12 @@
 // Row lists live on the device, so who copies what is settled there: each
 // workgroup reads the whole list for its own entries (a few thousand 4-byte
 // words from L2) instead of waiting for a planning kernel.
+//
+// Measured: four 1 MB rows into 32 (38 MB): 10 us, 3 of them a launch's least;
+// 96 rows from bf16 to fp32 (302 MB): 66 us, 4.6 TB/s; 64 rows of 1 MB zeroed:
+// 11.7 us, 5.7 TB/s; 64 rows of 512 KB moved by a compaction (67 MB): 17 us.
+// Units of 32 and 128 KB and two to four times the loads in flight were no
+// faster (38 MB fork: 10.6 and 16.2 us with 32 and 128 KB units).
 #include "gdn_common.h"
 #include "gdn_internal.h"
 #include "gdn_recurrence.h"
