@@ -15,8 +15,8 @@ int check_device(int *num_cus = nullptr);
 // Tokens of one workgroup's tile in the backward scan, and in the forward scan
 // by its types (eight times k6_recurrence.hip's tokens per wave).
 constexpr int kRecTile = 64;
-constexpr int rec_forward_tile(int x_dtype, int g_dtype, int per_head) {
-  return x_dtype != GDN_F32 && (per_head || g_dtype != GDN_F32) ? 2 * kRecTile : kRecTile;
+constexpr int rec_forward_tile(int x_dtype, int per_head) {
+  return x_dtype != GDN_F32 && per_head ? 2 * kRecTile : kRecTile;
 }
 // Channels of one workgroup's tile: 64 lanes x 4.
 constexpr int kRecChannels = 256;
@@ -57,6 +57,7 @@ struct RecArgs {
   // tiles and their chain
   int32_t ntiles, ncb;
   uint32_t units;             // ntiles * ncb
+  int32_t empties;            // workgroups per channel block for the empty sequences
   uint32_t *ticket;           // [ncb][kTicketStep] next tile of a channel block; NULL: one tile
   unsigned long long *words;  // [ntiles][C], then
   unsigned long long *groups; // [ceil(ntiles / kGroup)][C]

@@ -15,7 +15,7 @@ using namespace gdn;
 namespace {
 
 constexpr size_t kAlign = 256;
-constexpr int64_t kMaxUnits = 1 << 22;  // tiles of 64 tokens x 256 channels
+constexpr int64_t kMaxUnits = (1 << 22) - 1;  // tiles of 64 tokens x 256 channels
 constexpr int64_t kMaxTokens = INT32_MAX - 64;
 
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
@@ -31,7 +31,7 @@ enum Mode { kForward = 0, kBackward = 1, kDecode = 2 };
 
 int64_t tiles_of(const gdn_recurrence_params *p, bool backward) {
   const int64_t tile =
-      backward ? kRecTile : rec_forward_tile(p->x_dtype, p->g_dtype, p->g_per_head);
+      backward ? kRecTile : rec_forward_tile(p->x_dtype, p->g_per_head);
   return std::max<int64_t>(1, (p->total_tokens + tile - 1) / tile);
 }
 
@@ -190,6 +190,10 @@ int run_scan(const gdn_recurrence_params *p, bool backward, hipStream_t s) {
       r.groups = r.words + (int64_t)r.ntiles * r.C;
     }
   };
+  // workgroups for empty sequences, whose states a pass copies: 64 sequences
+  // each, at most 64 of them (and no more than the grid holds beside kMaxUnits)
+  const int32_t empties = (int32_t)std::min<int64_t>(
+      std::min<int64_t>(64, (kMaxUnits - 1) / a.ncb + 1), ((int64_t)p->num_seqs + 63) / 64);
   if (L.starts) a.bos = bos = (int32_t *)(ws + L.bos);
   a.chunk = L.own_chunk ? (float *)(ws + L.chunk) : p->chunk_states;
   a.vec = C % 4 == 0 && rows_vec(p->x, a.x_stride, xs) &&
@@ -208,6 +212,10 @@ int run_scan(const gdn_recurrence_params *p, bool backward, hipStream_t s) {
         f.fin = p->output_state;
         f.fin_dtype = p->output_state_dtype;
         f.fin_stride = p->output_state_stride ? p->output_state_stride : C;
+        // in a pool worked on in place their final states are there already
+        const bool same = f.fin == f.init && f.fin_dtype == f.init_dtype &&
+                          f.fin_stride == f.init_stride;
+        f.empties = f.fin && !same ? empties : 0;
       }
     }
     prepare(f);
@@ -222,6 +230,7 @@ int run_scan(const gdn_recurrence_params *p, bool backward, hipStream_t s) {
     a.dinit = p->dinitial_state;
     a.vec = a.vec && rows_vec(p->doutput, a.dy_stride, xs) && rows_vec(p->dx, C, xs) &&
             (p->g_per_head || rows_vec(p->dg, C, gs));
+    a.empties = a.dinit ? empties : 0;
     cut(a, true);
     prepare(a);
     if (e == hipSuccess) e = launch_rec_backward(a, s);

@@ -344,9 +344,10 @@ __device__ __forceinline__ void tile_geometry(const RecArgs &a, int t0, bool sta
 // Calls f(i) for the empty sequences, four at a time (i[k] the same for all
 // lanes of a wave, -1: none), so that f has four loads on their way: one after
 // the other they took 0.6 us each, 90 us for 170 empty ones in a training step.
-// The waves take eight sequences in turn.
+// A workgroup takes 64 sequences in turn, each wave eight; these workgroups come
+// behind the scan's in the grid and have no part in the chain.
 template <typename F>
-__device__ __forceinline__ void for_empty_sequences(const RecArgs &a, F f) {
+__device__ __forceinline__ void for_empty_sequences(const RecArgs &a, int part, F f) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   auto work = [&](int base, unsigned m) {
@@ -366,10 +367,48 @@ __device__ __forceinline__ void for_empty_sequences(const RecArgs &a, F f) {
     work(8 * wave, (unsigned)(m >> (8 * wave)) & 0xFFu);
     return;
   }
-  for (int base = 8 * wave; base < a.N; base += 8 * kWaves) {
+  for (int base = 8 * (wave + kWaves * part); base < a.N; base += 8 * kWaves * a.empties) {
     const int i = base + (lane & 7);
     work(base, (unsigned)__ballot(i < a.N && a.bos[i] == a.bos[i + 1]) & 0xFFu);
   }
+}
+
+// Final states of the empty sequences: their initial states.
+__device__ __forceinline__ void empty_forward(const RecArgs &a, int part, int c, int left) {
+  for_empty_sequences(a, part, [&](const int(&i)[4]) {
+    if (left <= 0) return;
+    int64_t row[4];
+    float h[4][4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) row[k] = i[k] >= 0 ? state_row(a, i[k]) : -1;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) h[k][e] = 0.f;
+      if (a.init && row[k] >= 0)
+        load_state(a.init, a.init_dtype, row[k] * a.init_stride + c, left, h[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (row[k] >= 0)
+        store_state(a.fin, a.fin_dtype, row[k] * a.fin_stride + c, left, h[k]);
+  });
+}
+// Gradients of their initial states: those of their final states.
+__device__ __forceinline__ void empty_backward(const RecArgs &a, int part, int c, int left) {
+  for_empty_sequences(a, part, [&](const int(&i)[4]) {
+    if (left <= 0) return;
+    float d[4][4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) d[k][e] = 0.f;
+      if (i[k] >= 0 && a.dfin) load_state(a.dfin, GDN_F32, (int64_t)i[k] * a.C + c, left, d[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (i[k] >= 0) store_state(a.dinit, GDN_F32, (int64_t)i[k] * a.C + c, left, d[k]);
+  });
 }
 
 // The channel block of this workgroup and its place in the block's chain.  One
@@ -544,17 +583,17 @@ __device__ __forceinline__ void segments_down(const Marks<TOK> &m, F f) {
 
 // ------------------------------------------------------------------ forward
 
-// Tokens per wave: 16 where x and the gates take few registers (head gates or
-// 16-bit gates on 16-bit x), else 8.  Twice the bytes per workgroup halve the
-// chain's traffic and its share of a tile's time (23 060 tokens x 4096 channels,
-// fp16 with head gates: 104 -> 82.5 us); with fp32 gates or fp32 x 16 tokens
-// would leave one workgroup per CU instead of two, and did not fit the backward
-// pass's registers in any type.
+// Tokens per wave: 16 for 16-bit x with head gates, which take few registers,
+// else 8.  Twice the bytes per workgroup halve the chain's traffic and its share
+// of a tile's time (23 060 tokens x 4096 channels, fp16 with head gates: 104 ->
+// 82.5 us).  16-bit gates per channel gain nothing (2 x 2048 x 2048: 17.9 and
+// 18.9 us); with fp32 gates or fp32 x 16 tokens would leave one workgroup per CU
+// instead of two, and they did not fit the backward pass's registers at all.
 template <typename T> constexpr int code() {
   return sizeof(T) == 4 ? GDN_F32 : std::is_same<T, bf16>::value ? GDN_BF16 : GDN_F16;
 }
-template <typename Tx, typename Tg, bool PH> constexpr int forward_tokens() {
-  return rec_forward_tile(code<Tx>(), code<Tg>(), PH) / kWaves;
+template <typename Tx, bool PH> constexpr int forward_tokens() {
+  return rec_forward_tile(code<Tx>(), PH) / kWaves;
 }
 
 // Bounded by HBM: per element x and g are read once and out written once; the
@@ -567,12 +606,17 @@ template <typename Tx, typename Tg, bool PH> constexpr int forward_tokens() {
 // bytes on their way: with one, the long pass took 666 us.
 template <typename Tx, typename Tg, bool PH, bool VEC>
 __global__ void __launch_bounds__(kThreads, 4) rec_forward_kernel(RecArgs a) {
-  constexpr int TOK = forward_tokens<Tx, Tg, PH>();
+  constexpr int TOK = forward_tokens<Tx, PH>();
   __shared__ TileGeo<TOK> G;
   __shared__ float sA[kWaves][kRecChannels], sB[kWaves][kRecChannels];
   // what is the same for a wave's lanes is kept in scalar registers
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  if (blockIdx.x >= a.units) {
+    const unsigned b = blockIdx.x - a.units;
+    const int ec = (int)(b % (unsigned)a.ncb) * kRecChannels + 4 * lane;
+    return empty_forward(a, (int)(b / (unsigned)a.ncb), ec, min(4, a.C - ec));
+  }
   int cb;
   const int tile = take_place(a, cb);
   const int T = (int)a.T;
@@ -651,28 +695,6 @@ __global__ void __launch_bounds__(kThreads, 4) rec_forward_kernel(RecArgs a) {
       });
     });
   }
-  // an empty sequence's final state is its initial one, which is there already
-  // in a pool worked on in place
-  if (tile == 0 && a.fin && (a.fin != a.init || a.fin_stride != a.init_stride)) {
-    for_empty_sequences(a, [&](const int(&i)[4]) {
-      if (left <= 0) return;
-      int64_t row[4];
-      float h[4][4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) row[k] = i[k] >= 0 ? state_row(a, i[k]) : -1;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) h[k][e] = 0.f;
-        if (a.init && row[k] >= 0)
-          load_state(a.init, a.init_dtype, row[k] * a.init_stride + c, left, h[k]);
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (row[k] >= 0)
-          store_state(a.fin, a.fin_dtype, row[k] * a.fin_stride + c, left, h[k]);
-    });
-  }
 }
 
 // Sum over a head's D / 4 lanes (8, 16 or 32 next to each other) by lane moves
@@ -704,6 +726,11 @@ __global__ void __launch_bounds__(kThreads, 4) rec_backward_kernel(RecArgs a) {
   __shared__ float sA[kWaves][kRecChannels], sF[kWaves][kRecChannels], sB[kWaves][kRecChannels];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  if (blockIdx.x >= a.units) {
+    const unsigned b = blockIdx.x - a.units;
+    const int ec = (int)(b % (unsigned)a.ncb) * kRecChannels + 4 * lane;
+    return empty_backward(a, (int)(b / (unsigned)a.ncb), ec, min(4, a.C - ec));
+  }
   int cb;
   const int tile = a.ntiles - 1 - take_place(a, cb);
   const int T = (int)a.T;
@@ -863,18 +890,6 @@ __global__ void __launch_bounds__(kThreads, 4) rec_backward_kernel(RecArgs a) {
     }
     });
   }
-  if (tile == 0 && a.dinit) {
-    for_empty_sequences(a, [&](const int(&i)[4]) {
-      if (left <= 0) return;
-      float d[4][4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (i[k] >= 0) load_dfinal(i[k], d[k]);
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (i[k] >= 0) store_state(a.dinit, GDN_F32, (int64_t)i[k] * a.C + c, left, d[k]);
-    });
-  }
 }
 
 // ------------------------------------------------------------------- decode
@@ -987,13 +1002,13 @@ hipError_t dispatch(const RecArgs &a, hipStream_t s) {
 
 template <typename Tx, typename Tg, bool PH, bool VEC> struct Fwd {
   static hipError_t go(const RecArgs &a, hipStream_t s) {
-    rec_forward_kernel<Tx, Tg, PH, VEC><<<dim3(a.units), dim3(kThreads), 0, s>>>(a);
+    rec_forward_kernel<Tx, Tg, PH, VEC><<<dim3(a.units + (unsigned)(a.empties * a.ncb)), dim3(kThreads), 0, s>>>(a);
     return hipGetLastError();
   }
 };
 template <typename Tx, typename Tg, bool PH, bool VEC> struct Bwd {
   static hipError_t go(const RecArgs &a, hipStream_t s) {
-    rec_backward_kernel<Tx, Tg, PH, VEC><<<dim3(a.units), dim3(kThreads), 0, s>>>(a);
+    rec_backward_kernel<Tx, Tg, PH, VEC><<<dim3(a.units + (unsigned)(a.empties * a.ncb)), dim3(kThreads), 0, s>>>(a);
     return hipGetLastError();
   }
 };

@@ -303,6 +303,30 @@ def test_thousands_of_sequences():
     _both(d, lens)
 
 
+@pytest.mark.parametrize("n", [63, 64, 65, 6000])
+def test_all_but_one_sequence_empty(n):
+    """Empty sequences' states are copied by workgroups of their own: 64 to a
+    workgroup, and more sequences than those workgroups hold at once."""
+    lens = [0] * n
+    lens[n // 3] = 5
+    d = R.make(19, lens, 2, 150)
+    _both(d, lens)
+    # from a pool of another type, an index out of range among them
+    idx = torch.randperm(n + 2)[:n].to(torch.int32)
+    idx[n - 1] = n + 2
+    pool = torch.randn((n + 2, 2, 150), device="cuda").to(BF16)
+    final = torch.full((n + 2, 2, 150), 7.0, device="cuda")
+    gated_linear_recurrence(d["x"], d["g"], initial_state=pool, output_final_state=True,
+                            cu_seqlens=d["cu"], output_state=final, state_indices=idx.cuda())
+    want = torch.full_like(final, 7.0)
+    for i in range(n - 1):
+        if lens[i] == 0:
+            want[idx[i]] = pool[idx[i]].float()
+    row = int(idx[n // 3])
+    want[row] = final[row]
+    assert torch.equal(final, want)
+
+
 def test_output_in_place_of_x():
     lens = [100, 300]
     d = R.make(14, lens, 3, 32, BF16)
