@@ -3,9 +3,10 @@
 //
 // A tile is 64 (or 128) tokens x 256 channels, one workgroup of eight waves:
 // wave w holds tokens 8 w .. 8 w + 7 (16 w .. 16 w + 15) of all 256 channels in
-// registers, four channels per lane, so that x and g are read from memory once.  Over a run of tokens
-// the recurrence is the affine map h -> A h + B (A the product of the gates, B
-// the run's last state from zero), and maps compose, so a tile takes
+// registers, four channels per lane, so that x and g are read from memory
+// once.  Over a run of tokens the recurrence is the affine map h -> A h + B (A
+// the product of the gates, B the run's last state from zero), and maps
+// compose, so a tile takes
 //   1. each wave: its (A, B), from registers                       (sweep 1)
 //   2. one thread per channel: the tile's (A, B) from the waves' (LDS), the
 //      state before the tile, each wave's start state
@@ -845,49 +846,49 @@ __global__ void __launch_bounds__(kThreads, 4) rec_backward_kernel(RecArgs a) {
     by_marks(m, [&](auto plain) {
       constexpr bool PL = decltype(plain)::value;
 #pragma unroll
-    for (int half = 1; half >= 0; --half) {
-      constexpr int kHalf = TOK / 2;
-      const int s0 = half * kHalf, s1 = s0 + kHalf;
-      float before[kHalf][4], h[4];
+      for (int half = 1; half >= 0; --half) {
+        constexpr int kHalf = TOK / 2;
+        const int s0 = half * kHalf, s1 = s0 + kHalf;
+        float before[kHalf][4], h[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) h[e] = opaque(sF[wave][4 * lane + e]);
-      segments_up<PL>(m, [&](int lo, int hi, bool started) {
-        if (lo >= s1) return;
-        if (!PL && started) start_state(a, m, lo, c, left, h0, h);
-        ascend<TOK>(lo, hi, [&](int s) {
-          if (s >= s1) return;
+        for (int e = 0; e < 4; ++e) h[e] = opaque(sF[wave][4 * lane + e]);
+        segments_up<PL>(m, [&](int lo, int hi, bool started) {
+          if (lo >= s1) return;
+          if (!PL && started) start_state(a, m, lo, c, left, h0, h);
+          ascend<TOK>(lo, hi, [&](int s) {
+            if (s >= s1) return;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (s >= s0) before[s - s0][e] = h[e];
-            h[e] = fmaf(g[s][e], h[e], to_f32((Tx)x[s][e]));
-          }
+            for (int e = 0; e < 4; ++e) {
+              if (s >= s0) before[s - s0][e] = h[e];
+              h[e] = fmaf(g[s][e], h[e], to_f32((Tx)x[s][e]));
+            }
+          });
         });
-      });
-      segments_down<PL>(m, [&](int lo, int hi, bool started) {
-        if (lo >= s1 || hi <= s0) return;
-        if (!PL && hi <= s1 && (m.last >> (hi - 1) & 1)) load_dfinal(m.seq_last(hi - 1), k);
-        descend<TOK>(lo, hi, [&](int s) {
-          if (s < s0 || s >= s1) return;
-          const int64_t t = tw + s;
-          float dh[4], dg[4];
+        segments_down<PL>(m, [&](int lo, int hi, bool started) {
+          if (lo >= s1 || hi <= s0) return;
+          if (!PL && hi <= s1 && (m.last >> (hi - 1) & 1)) load_dfinal(m.seq_last(hi - 1), k);
+          descend<TOK>(lo, hi, [&](int s) {
+            if (s < s0 || s >= s1) return;
+            const int64_t t = tw + s;
+            float dh[4], dg[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            dh[e] = to_f32((Tx)dy[s][e]) + k[e];
-            dg[e] = dh[e] * before[s - s0][e];
-            k[e] = g[s][e] * dh[e];
-          }
-          if constexpr (PH) {
-            const float sum = head_sum((dg[0] + dg[1]) + (dg[2] + dg[3]), a.D);
-            if (writes_head) ((Tg *)a.dg)[t * a.H + head] = from_f32<Tg>(sum);
-          } else {
-            store4<Tg, VEC>((Tg *)a.dg + t * a.C + c, left, dg);
-          }
-          store4<Tx, VEC>((Tx *)a.dx + t * a.C + c, left, dh);
+            for (int e = 0; e < 4; ++e) {
+              dh[e] = to_f32((Tx)dy[s][e]) + k[e];
+              dg[e] = dh[e] * before[s - s0][e];
+              k[e] = g[s][e] * dh[e];
+            }
+            if constexpr (PH) {
+              const float sum = head_sum((dg[0] + dg[1]) + (dg[2] + dg[3]), a.D);
+              if (writes_head) ((Tg *)a.dg)[t * a.H + head] = from_f32<Tg>(sum);
+            } else {
+              store4<Tg, VEC>((Tg *)a.dg + t * a.C + c, left, dg);
+            }
+            store4<Tx, VEC>((Tx *)a.dx + t * a.C + c, left, dh);
+          });
+          if (!PL && lo >= s0 && a.dinit && started)
+            store_state(a.dinit, GDN_F32, (int64_t)m.seq_first(lo) * a.C + c, left, k);
         });
-        if (!PL && lo >= s0 && a.dinit && started)
-          store_state(a.dinit, GDN_F32, (int64_t)m.seq_first(lo) * a.C + c, left, k);
-      });
-    }
+      }
     });
   }
 }
@@ -1000,15 +1001,18 @@ hipError_t dispatch(const RecArgs &a, hipStream_t s) {
 #undef GDN_REC_GO
 }
 
+// A scan's tiles, then the workgroups for empty sequences.
+unsigned scan_grid(const RecArgs &a) { return a.units + (unsigned)(a.empties * a.ncb); }
+
 template <typename Tx, typename Tg, bool PH, bool VEC> struct Fwd {
   static hipError_t go(const RecArgs &a, hipStream_t s) {
-    rec_forward_kernel<Tx, Tg, PH, VEC><<<dim3(a.units + (unsigned)(a.empties * a.ncb)), dim3(kThreads), 0, s>>>(a);
+    rec_forward_kernel<Tx, Tg, PH, VEC><<<dim3(scan_grid(a)), dim3(kThreads), 0, s>>>(a);
     return hipGetLastError();
   }
 };
 template <typename Tx, typename Tg, bool PH, bool VEC> struct Bwd {
   static hipError_t go(const RecArgs &a, hipStream_t s) {
-    rec_backward_kernel<Tx, Tg, PH, VEC><<<dim3(a.units + (unsigned)(a.empties * a.ncb)), dim3(kThreads), 0, s>>>(a);
+    rec_backward_kernel<Tx, Tg, PH, VEC><<<dim3(scan_grid(a)), dim3(kThreads), 0, s>>>(a);
     return hipGetLastError();
   }
 };

@@ -90,7 +90,8 @@ int float_type(at::ScalarType t) {
   return t == at::kFloat ? GDN_F32 : t == at::kBFloat16 ? GDN_BF16 : t == at::kHalf ? GDN_F16 : -1;
 }
 int state_type(at::ScalarType t) {
-  return t == at::kFloat8_e4m3fn ? GDN_FP8_E4M3 : t == at::kFloat8_e5m2 ? GDN_FP8_E5M2 : float_type(t);
+  if (t == at::kFloat8_e4m3fn) return GDN_FP8_E4M3;
+  return t == at::kFloat8_e5m2 ? GDN_FP8_E5M2 : float_type(t);
 }
 int index_type(const char *name, const Tensor &t) {
   BAD_IF(t.scalar_type() != at::kInt && t.scalar_type() != at::kLong, name,

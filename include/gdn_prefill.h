@@ -302,8 +302,8 @@ int gdn_build_chunk_indices(const void *cu_seqlens, int32_t cu_type,
  *     h_t = g_t * h_{t-1} + x_t,      output_t = h_t
  *
  * from the given initial state (or zero).  g is the forget gate itself, in
- * [0, 1] (a gate above 1 is computed, but the products of 64 consecutive
- * gates must stay finite).
+ * [0, 1] (a gate above 1 is computed, but the products of 1 024 consecutive
+ * gates of a sequence must stay finite).
  *
  * Shapes: x, output, doutput, dx [T, H, D] in x_dtype (F32, BF16 or F16); g,
  * dg [T, H, D], or [T, H] with g_per_head (one gate for the D channels of a
@@ -316,6 +316,9 @@ int gdn_build_chunk_indices(const void *cu_seqlens, int32_t cu_type,
  * gdn_prefill_params; output_state may be the same memory as initial_state,
  * and state_indices must be unique where a final state is written.  output may
  * be x itself (contiguous); no other two tensors of a call may overlap.
+ * Tensors start on a boundary of their element size, the workspace on a
+ * 256-byte boundary (GDN_ERR_ALIGN).  Calls that overlap in time need
+ * workspaces of their own.
  * Rows of output outside every sequence are untouched.  An empty sequence's
  * final state is its initial state.  A sequence whose state index is out of
  * range starts from zero and writes no final state.
