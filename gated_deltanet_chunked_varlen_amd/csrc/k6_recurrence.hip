@@ -599,8 +599,8 @@ template <typename Tx, bool PH> constexpr int forward_tokens() {
 
 // Bounded by HBM: per element x and g are read once and out written once; the
 // chain adds 8 bytes per tile and channel each for clearing, publishing and
-// looking back.  65 536 tokens x 4096 channels, bf16 with fp32 gates: 386 us,
-// 5.6 TB/s (a plain copy runs at 4.7 to 5.4 TB/s on the same card), 370 us with
+// looking back.  65 536 tokens x 4096 channels, bf16 with fp32 gates: 388 us,
+// 5.5 TB/s (a plain copy runs at 4.7 to 5.4 TB/s on the same card), 370 us with
 // every wait of the chain taken out.  2 x 2048 tokens x 2048 channels: 18 us,
 // 16 without the waits; it is one round of workgroups, whose loads and stores
 // hardly overlap.  Two workgroups per CU (128 registers) are what keeps enough
