@@ -21,13 +21,19 @@ def _stream(index):
 
 def _workspace(index, stream, need):
     """Workspace of a call on ``stream``, the current one of the current device
-    ``index``: kept per stream, or under capture from the graph's own pool (a
-    graph keeps the address)."""
+    ``index``: kept per stream (in the prefill's cache, but apart from its
+    memory), or under capture from the graph's own pool (a graph keeps the
+    address)."""
     if torch.cuda.is_current_stream_capturing():
         return torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", index))
-    ws = api._ws_cache.get(("cuda", index, stream))
-    return ws if ws is not None and ws.numel() >= need else \
-        api.cached_workspace(torch.device("cuda", index), stream, need)
+    key = ("cuda", index, stream, "recurrence")
+    ws = api._ws_cache.get(key)
+    if ws is None or ws.numel() < need:
+        ws = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", index))
+        api._ws_cache[key] = ws
+        while len(api._ws_cache) > api._WS_CACHE_MAX:
+            api._ws_cache.popitem(last=False)
+    return ws
 
 
 def calls():

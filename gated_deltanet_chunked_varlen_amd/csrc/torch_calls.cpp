@@ -14,7 +14,7 @@
 #include <ATen/ATen.h>
 #include <c10/core/DeviceGuard.h>
 
-#include <string>
+#include <mutex>
 #include <vector>
 
 #include "../../include/gdn_prefill.h"
@@ -54,6 +54,11 @@ void *current_stream(const at::Device &dev) {
   return s;
 }
 
+// A call's kernels go into its stream together: threads that share a stream
+// share its workspace, which the second kernel of a scan must find as the first
+// one left it.
+std::mutex enqueue;
+
 // Launches with the tensors' device current; an error code becomes the
 // binding's exception.
 template <typename F> void launch(const at::Device &dev, F f) {
@@ -61,7 +66,10 @@ template <typename F> void launch(const at::Device &dev, F f) {
   void *stream = current_stream(dev);
   int rc;
   Py_BEGIN_ALLOW_THREADS;
-  rc = f(stream);
+  {
+    const std::lock_guard<std::mutex> lock(enqueue);
+    rc = f(stream);
+  }
   Py_END_ALLOW_THREADS;
   if (rc == GDN_OK) return;
   PyObject *r = PyObject_CallFunction(lib.raise, "i", rc);

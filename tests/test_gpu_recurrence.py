@@ -429,6 +429,28 @@ def test_two_streams_at_once():
                 assert torch.equal(a, b)
 
 
+def test_threads_on_one_stream():
+    """Threads that share a stream share its workspace; a call's kernels stay
+    together."""
+    import threading
+    ds = [R.make(60 + i, [900 + 64 * i, 300], 2, 64, BF16) for i in range(4)]
+    refs = [_run_all(d) for d in ds]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        for _ in range(50):
+            if not all(torch.equal(a, b) for a, b in zip(refs[i], _run_all(ds[i]))):
+                wrong.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
 def test_graph_replay():
     """A training step captured once and replayed on new inputs, with eager
     work between the replays."""
