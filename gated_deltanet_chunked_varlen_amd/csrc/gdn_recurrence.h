@@ -61,10 +61,15 @@ struct RecArgs {
   uint32_t *ticket;           // [ncb][kTicketStep] next tile of a channel block; NULL: one tile
   unsigned long long *words;  // [ntiles][C], then
   unsigned long long *groups; // [ceil(ntiles / kGroup)][C]
+  uint32_t wait_limit;        // looks at words that are not there before a wait gives up
   int32_t *status;
   int32_t vec;  // every row of x, g, dy, out, dx, dg is a whole number of aligned 4-element groups
   int32_t num_cus;
 };
+
+// wait_limit of a call: seconds, where a wait takes microseconds.  A variable for
+// the sake of tests.
+extern uint32_t rec_wait_limit;
 
 // Clears the chain's words and ticket, and for N > 63 forms bos and the status.
 hipError_t launch_rec_prepare(const RecArgs &a, int32_t *bos, hipStream_t s);

@@ -12,6 +12,8 @@
 
 using namespace gdn;
 
+uint32_t gdn::rec_wait_limit = 1u << 20;
+
 namespace {
 
 constexpr size_t kAlign = 256;
@@ -162,6 +164,7 @@ void fill(const gdn_recurrence_params *p, int num_cus, RecArgs &a) {
   a.pool_rows = p->pool_size;
   a.status = p->status;
   a.num_cus = num_cus;
+  a.wait_limit = rec_wait_limit;
   a.ncb = (int32_t)((C + kRecChannels - 1) / kRecChannels);
 }
 

@@ -31,7 +31,12 @@
 // in order (one counter for all made 512 workgroups queue for 5 us).  A tile
 // waits only for earlier tiles of its channel block, which were taken by
 // workgroups that are already running; the first unfinished one waits for
-// nothing, so every wait ends.
+// nothing, so every wait ends.  That needs a workspace that nobody else writes
+// during the call.  If one does (two calls at once given the same one), a wait
+// gives up after wait_limit looks with a NaN for the state, a ticket behind the
+// last tile ends its workgroup, and sequence starts read from the workspace are
+// taken only inside the tile: the results are wrong, but the call ends and
+// writes nothing but its own buffers.
 //
 // Sequence bounds.  A wave walks its tokens segment by segment, a segment
 // being the wave's part of one sequence; where a sequence starts the carry is
@@ -55,7 +60,7 @@ namespace {
 constexpr int kWaves = 8;                   // waves per workgroup
 constexpr int kThreads = 64 * kWaves;
 constexpr int kWindow = 8;                  // groups looked back over
-constexpr unsigned kPending = 0xFFFFFFFFu, kLast = 0xFFFFFFFEu;
+constexpr unsigned kPending = 0xFFFFFFFFu, kLast = 0xFFFFFFFEu, kNaN = 0x7FC00000u;
 
 typedef float f32x4v __attribute__((ext_vector_type(4)));
 
@@ -171,16 +176,17 @@ __device__ __forceinline__ unsigned long long peek(const unsigned long long *w) 
 __device__ __forceinline__ unsigned mark(unsigned long long w) { return (unsigned)(w >> 32); }
 __device__ __forceinline__ float low(unsigned long long w) { return __uint_as_float((unsigned)w); }
 __device__ __forceinline__ unsigned map_bits(float A) {
-  return A != A ? 0x7FC00000u : __float_as_uint(A);
+  return A != A ? kNaN : __float_as_uint(A);
 }
 
 // State behind the group at g, for one channel; `avail` >= 1 groups lie from g
 // on in direction step, and the last of them always publishes kLast by itself.
+// NaN if `limit` looks did not find it.
 __device__ __forceinline__ float look_back(const unsigned long long *groups, int64_t C, int g,
-                                           unsigned c, int step, int avail) {
+                                           unsigned c, int step, int avail, unsigned limit) {
   groups += (int64_t)g * C;
   const int64_t d = (int64_t)step * C;
-  for (;;) {
+  for (unsigned look = 0;; ++look) {
     unsigned long long w[kWindow];
     int found = -1;
     bool open = true;  // every nearer group has published
@@ -208,6 +214,7 @@ __device__ __forceinline__ float look_back(const unsigned long long *groups, int
       }
       return h;
     }
+    if (look >= limit) return __uint_as_float(kNaN);
     __builtin_amdgcn_s_sleep(2);
   }
 }
@@ -231,15 +238,16 @@ __device__ __forceinline__ float chain(const RecArgs &a, int tile, unsigned c, i
   Map m = {1.f, 0.f, false};
   if (before > 0) {
     unsigned long long w[kGroup - 1];
-    for (;;) {
-      bool open = true;
+    bool open;
+    for (unsigned look = 0;; ++look) {
+      open = true;
 #pragma unroll
       for (int j = 0; j < kGroup - 1; ++j)
         if (j < before) w[j] = peek(word + (int64_t)(j + 1) * step * a.C);
 #pragma unroll
       for (int j = 0; j < kGroup - 1; ++j)
         if (j < before && mark(w[j]) == kPending) open = false;
-      if (open) break;
+      if (open || look >= a.wait_limit) break;
       __builtin_amdgcn_s_sleep(2);
     }
 #pragma unroll
@@ -254,6 +262,7 @@ __device__ __forceinline__ float chain(const RecArgs &a, int tile, unsigned c, i
         }
       }
     }
+    if (!open) m = {0.f, __uint_as_float(kNaN), true};  // given up
   }
   const int group = n / kGroup;
   unsigned long long *gword = a.groups + (int64_t)group * a.C + c;
@@ -263,7 +272,7 @@ __device__ __forceinline__ float chain(const RecArgs &a, int tile, unsigned c, i
   if (own.known) all = own;
   if (closes) publish(gword, all.known ? kLast : map_bits(all.A), all.B);
   if (m.known) return m.B;
-  const float h = look_back(a.groups, a.C, group - 1, c, -1, group);
+  const float h = look_back(a.groups, a.C, group - 1, c, -1, group, a.wait_limit);
   if (closes && !all.known) publish(gword, kLast, fmaf(all.A, h, all.B));
   return fmaf(m.A, h, m.B);
 }
@@ -320,23 +329,25 @@ __device__ __forceinline__ void tile_geometry(const RecArgs &a, int t0, bool sta
       }
     }
   } else {
-    // first j with bos[j] >= t0, then every start and end inside the tile
+    // first j with bos[j] >= t0, then every start and end inside the tile (and
+    // inside the tokens, whatever the workspace holds)
+    const int te = min(t1, (int)a.T);
     int lo = 0, hi = a.N + 1;
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
       if (a.bos[mid] >= t0) hi = mid; else lo = mid + 1;
     }
-    for (int base = lo; base <= a.N && a.bos[base] <= t1; base += kThreads) {
+    for (int base = lo; base <= a.N && a.bos[base] <= te; base += kThreads) {
       const int j = base + tid;
       if (j <= a.N) {
         const int b = a.bos[j];
-        if (b < t1 && j < a.N && a.bos[j + 1] > b) G.start[b - t0] = j;
-        if (b > t0 && b <= t1 && j > 0 && a.bos[j - 1] < b) G.end[b - 1 - t0] = j - 1;
+        if (b >= t0 && b < te && j < a.N && a.bos[j + 1] > b) G.start[b - t0] = j;
+        if (b > t0 && b <= te && j > 0 && a.bos[j - 1] < b) G.end[b - 1 - t0] = j - 1;
       }
     }
     if (tid == 0) {
       G.lo = a.bos[0];
-      G.hi = a.bos[a.N];
+      G.hi = min(a.bos[a.N], (int)a.T);
     }
   }
   __syncthreads();
@@ -412,7 +423,8 @@ __device__ __forceinline__ void empty_backward(const RecArgs &a, int part, int c
   });
 }
 
-// The channel block of this workgroup and its place in the block's chain.  One
+// The channel block of this workgroup and its place in the block's chain (-1: a
+// ticket behind the last tile, there is nothing to do).  One
 // round of workgroups after another starts one block further: workgroups go
 // to the eight XCDs in turn, so without the shift a block of a multiple-of-8
 // set would stay on one XCD (65 536 tokens x 16 blocks: 486 us against 410).
@@ -424,7 +436,8 @@ __device__ __forceinline__ int take_place(const RecArgs &a, int &cb) {
     place = (int)__hip_atomic_fetch_add(a.ticket + cb * kTicketStep, 1u, __ATOMIC_RELAXED,
                                         __HIP_MEMORY_SCOPE_AGENT);
   __syncthreads();
-  return __builtin_amdgcn_readfirstlane(place);
+  const int n = __builtin_amdgcn_readfirstlane(place);
+  return (unsigned)n < (unsigned)a.ntiles ? n : -1;
 }
 
 // Gates of one token for a lane's four channels: four values, or their head's.
@@ -620,6 +633,7 @@ __global__ void __launch_bounds__(kThreads, 4) rec_forward_kernel(RecArgs a) {
   }
   int cb;
   const int tile = take_place(a, cb);
+  if (tile < 0) return;
   const int T = (int)a.T;
   const int t0 = tile * G.kTile, tw = t0 + wave * TOK;
   const int c = cb * kRecChannels + 4 * lane;
@@ -733,7 +747,9 @@ __global__ void __launch_bounds__(kThreads, 4) rec_backward_kernel(RecArgs a) {
     return empty_backward(a, (int)(b / (unsigned)a.ncb), ec, min(4, a.C - ec));
   }
   int cb;
-  const int tile = a.ntiles - 1 - take_place(a, cb);
+  const int place = take_place(a, cb);
+  if (place < 0) return;
+  const int tile = a.ntiles - 1 - place;
   const int T = (int)a.T;
   const int t0 = tile * G.kTile, tw = t0 + wave * TOK;
   const int c = cb * kRecChannels + 4 * lane;

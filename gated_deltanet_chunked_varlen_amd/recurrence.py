@@ -57,7 +57,14 @@ def gated_linear_recurrence(x, g, initial_state=None, output_final_state=False, 
     state_indices[i] and leaves its final state in that row of
     ``output_state``, which may be ``initial_state`` itself; rows must then be
     unique (sequences may share a start row where no final state is written).
-    h is fp32 throughout.  ``output`` may be x itself.
+    h is fp32 throughout.  ``output`` may be x itself; no other two tensors of
+    a call may overlap.
+
+    ``workspace`` (optional uint8 device tensor) is used, if it is large
+    enough, instead of the one that is kept for the current stream.  A call
+    needs it for itself until its kernels have ended: calls on two streams at
+    once (or two captured graphs that run at once) with one workspace give
+    wrong values.
 
     Returns ``output`` [T, H, D] (rows outside every sequence are not
     written), then the final state with ``output_final_state``, then with
@@ -104,7 +111,8 @@ def gated_linear_recurrence_backward(doutput, x, g, initial_state=None, dfinal_s
     and g).  Returns (dx, dg), or (dx, dg, dinitial_state) with
     ``output_dinitial_state``: x's and g's shapes and dtypes, float32
     [N, H, D].  Rows of dx and dg outside every sequence are zero.  Results do
-    not depend on the order in which the work runs."""
+    not depend on the order in which the work runs.  No two tensors of a call
+    may overlap, and ``workspace`` is used as in the forward call."""
     return calls().rec_backward(doutput, x, g, initial_state, dfinal_state, cu_seqlens,
                                 chunk_states, output_dinitial_state, dx, dg, dinitial_state,
                                 status, workspace)

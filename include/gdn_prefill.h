@@ -318,7 +318,9 @@ int gdn_build_chunk_indices(const void *cu_seqlens, int32_t cu_type,
  * be x itself (contiguous); no other two tensors of a call may overlap.
  * Tensors start on a boundary of their element size, the workspace on a
  * 256-byte boundary (GDN_ERR_ALIGN).  Calls that overlap in time need
- * workspaces of their own.
+ * workspaces of their own: if something else writes a call's workspace, the
+ * call still ends and writes only its own buffers, but they hold NaN or other
+ * wrong values.
  * Rows of output outside every sequence are untouched.  An empty sequence's
  * final state is its initial state.  A sequence whose state index is out of
  * range starts from zero and writes no final state.
