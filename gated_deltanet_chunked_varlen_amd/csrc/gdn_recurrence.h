@@ -71,6 +71,8 @@ struct RecArgs {
 // the sake of tests.
 extern uint32_t rec_wait_limit;
 
+int32_t rec_empties(uint32_t units, int32_t ncb, int32_t num_seqs);
+
 // Clears the chain's words and ticket, and for N > 63 forms bos and the status.
 hipError_t launch_rec_prepare(const RecArgs &a, int32_t *bos, hipStream_t s);
 hipError_t launch_rec_forward(const RecArgs &a, hipStream_t s);

@@ -14,11 +14,23 @@ using namespace gdn;
 
 uint32_t gdn::rec_wait_limit = 1u << 20;
 
+// Workgroups per channel block for the empty sequences, whose states a pass
+// copies: 64 sequences each, at most 64 of them, and no more than the grid
+// holds beside the scan's `units` (a grid has fewer than 2^32 threads, and a
+// scan's workgroup 512; one fits always: units < 2^22 and ncb <= 2^21).
+int32_t gdn::rec_empties(uint32_t units, int32_t ncb, int32_t num_seqs) {
+  const int64_t room = ((int64_t)(1 << 23) - 1 - units) / ncb;
+  return (int32_t)std::min<int64_t>(std::min<int64_t>(64, room), ((int64_t)num_seqs + 63) / 64);
+}
+
 namespace {
 
 constexpr size_t kAlign = 256;
 constexpr int64_t kMaxUnits = (1 << 22) - 1;  // tiles of 64 tokens x 256 channels
 constexpr int64_t kMaxTokens = INT32_MAX - 64;
+// sequences: what a kernel's 32-bit loops can step behind without an overflow
+constexpr int64_t kMaxSeqs = (int64_t)1 << 30;
+constexpr int64_t kMaxDecodeThreads = ((int64_t)1 << 32) - 256;
 
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
@@ -39,13 +51,16 @@ int64_t tiles_of(const gdn_recurrence_params *p, bool backward) {
 
 int check_shape(const gdn_recurrence_params *p, int mode) {
   if (!p) return GDN_ERR_NULL;
-  if (p->total_tokens < 0 || p->total_tokens > kMaxTokens || p->num_seqs < 0) return GDN_ERR_SHAPE;
+  if (p->total_tokens < 0 || p->total_tokens > kMaxTokens || p->num_seqs < 0 ||
+      p->num_seqs > kMaxSeqs)
+    return GDN_ERR_SHAPE;
   if (p->num_heads < 1 || p->head_size < 1) return GDN_ERR_SHAPE;
   const int64_t C = (int64_t)p->num_heads * p->head_size;
   if (C > INT32_MAX / 4) return GDN_ERR_SHAPE;
   if (mode == kDecode) {
     if (p->total_tokens != p->num_seqs || p->cu_seqlens) return GDN_ERR_SHAPE;
-    if (((C + 3) / 4) * (int64_t)p->num_seqs > (int64_t)1 << 38) return GDN_ERR_SHAPE;
+    // one thread per four channels of a sequence, in whole workgroups of 256
+    if (((C + 3) / 4) * (int64_t)p->num_seqs > kMaxDecodeThreads) return GDN_ERR_SHAPE;
   } else {
     if (!p->cu_seqlens && p->num_seqs != 1) return GDN_ERR_SHAPE;
     const int64_t ncb = (C + kRecChannels - 1) / kRecChannels;
@@ -193,10 +208,6 @@ int run_scan(const gdn_recurrence_params *p, bool backward, hipStream_t s) {
       r.groups = r.words + (int64_t)r.ntiles * r.C;
     }
   };
-  // workgroups for empty sequences, whose states a pass copies: 64 sequences
-  // each, at most 64 of them (and no more than the grid holds beside kMaxUnits)
-  const int32_t empties = (int32_t)std::min<int64_t>(
-      std::min<int64_t>(64, (kMaxUnits - 1) / a.ncb + 1), ((int64_t)p->num_seqs + 63) / 64);
   if (L.starts) a.bos = bos = (int32_t *)(ws + L.bos);
   a.chunk = L.own_chunk ? (float *)(ws + L.chunk) : p->chunk_states;
   a.vec = C % 4 == 0 && rows_vec(p->x, a.x_stride, xs) &&
@@ -218,7 +229,7 @@ int run_scan(const gdn_recurrence_params *p, bool backward, hipStream_t s) {
         // in a pool worked on in place their final states are there already
         const bool same = f.fin == f.init && f.fin_dtype == f.init_dtype &&
                           f.fin_stride == f.init_stride;
-        f.empties = f.fin && !same ? empties : 0;
+        f.empties = f.fin && !same ? rec_empties(f.units, f.ncb, f.N) : 0;
       }
     }
     prepare(f);
@@ -233,8 +244,8 @@ int run_scan(const gdn_recurrence_params *p, bool backward, hipStream_t s) {
     a.dinit = p->dinitial_state;
     a.vec = a.vec && rows_vec(p->doutput, a.dy_stride, xs) && rows_vec(p->dx, C, xs) &&
             (p->g_per_head || rows_vec(p->dg, C, gs));
-    a.empties = a.dinit ? empties : 0;
     cut(a, true);
+    a.empties = a.dinit ? rec_empties(a.units, a.ncb, a.N) : 0;
     prepare(a);
     if (e == hipSuccess) e = launch_rec_backward(a, s);
   }

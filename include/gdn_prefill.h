@@ -308,7 +308,9 @@ int gdn_build_chunk_indices(const void *cu_seqlens, int32_t cu_type,
  * Shapes: x, output, doutput, dx [T, H, D] in x_dtype (F32, BF16 or F16); g,
  * dg [T, H, D], or [T, H] with g_per_head (one gate for the D channels of a
  * head; D must then be 32, 64 or 128), in g_dtype: F32 or x_dtype.  H and D
- * are any positive numbers.  A token's H * D (or H) values are contiguous;
+ * are any positive numbers with H * D < 2^29.  A call takes at most 2^30
+ * sequences, ceil(T / 64) * ceil(H * D / 256) < 2^22 tiles and, in a decode
+ * step, ceil(H * D / 4) * N <= 2^32 - 256 (GDN_ERR_SHAPE).  A token's H * D (or H) values are contiguous;
  * x, g and doutput have token strides in elements (0 = contiguous), every
  * other tensor is contiguous.  States are [rows, H, D] in any state dtype
  * with a row stride in elements (0 = contiguous); the 8-bit types saturate.
