@@ -329,6 +329,8 @@ int pool_plan(const gdn_pool_params *p, int mode, PoolPlan &L) {
     for (int i = 0; i < 4; ++i) L.src_str[i] = L.dst_str[i];
     return GDN_OK;
   }
+  // every entry is compared with every other one (k7_pool.hip)
+  if (p->count > GDN_POOL_MAX_ROWS) return GDN_ERR_SHAPE;
   if (p->src_pool_rows < 0 || p->src_pool_rows > GDN_POOL_MAX_ROWS) return GDN_ERR_SHAPE;
   if (!state_type(p->src_dtype)) return GDN_ERR_DTYPE;
   if (p->count > 0 && !p->src_rows) return GDN_ERR_NULL;

@@ -8,8 +8,10 @@
 // and by launch latency for a few short ones; every call is one kernel.
 //
 // Row lists live on the device, so who copies what is settled there: each
-// workgroup reads the whole list for its own entries (a few thousand 4-byte
-// words from L2) instead of waiting for a planning kernel.
+// workgroup reads the whole list for its own entries instead of waiting for a
+// planning kernel.  That is meant for lists of up to a few thousand entries
+// (4-byte words from L2, less than the rows); a copy's time grows with the
+// square of its list, which is why it takes at most GDN_POOL_MAX_ROWS entries.
 //
 // Measured: four 1 MB rows into 32 (38 MB): 10 us, 3 of them a launch's least;
 // 96 rows from bf16 to fp32 (302 MB): 66 us, 4.6 TB/s; 64 rows of 1 MB zeroed:

@@ -20,7 +20,9 @@ def state_pool_copy(pool, src_rows, dst_rows, src_pool=None, status=None):
     Equal dtypes copy bit for bit, others round to nearest (8-bit types
     saturate).  A destination named twice takes its last entry; inside one
     pool an entry whose source row is another entry's destination is skipped;
-    entries outside the pools are skipped.  ``status`` (optional int32 device
+    entries outside the pools are skipped.  A list holds at most 262144
+    entries; it is meant for a few thousand (each is compared with all
+    others).  ``status`` (optional int32 device
     tensor) receives the matching GDN_STATUS_POOL_* bits.  src_pool may be the
     same view as pool, or share no elements with it.  Returns pool."""
     return calls().pool_copy(pool, src_rows, dst_rows, src_pool, status)

@@ -437,7 +437,8 @@ int gdn_validate_pool_host(const gdn_pool_params *p, int32_t mode);
  * the same view; other views may share no elements (GDN_ERR_STATE where the
  * host can see that they do).  A destination named twice takes its last
  * entry.  In one pool an entry whose source row is another entry's destination
- * is skipped.  Both set their status bit. */
+ * is skipped.  Both set their status bit.  At most GDN_POOL_MAX_ROWS entries
+ * (GDN_ERR_SHAPE): each is compared with all others. */
 int gdn_pool_copy(const gdn_pool_params *p, void *stream);
 
 /* dst[dst_rows[i]] = 0 (rows freed, or taken for a new sequence). */

@@ -54,3 +54,18 @@ def test_empty_sequences_fit_the_grid_of_a_scan():
                 assert (e > 0) == (n > 0) and e <= 64 and 64 * (e - 1) <= n
                 assert (units + e * ncb) * 512 < 2 ** 32
     assert empties(16, 16, 100) == 2 and empties(16, 16, 10 ** 6) == 64
+
+
+def test_lists_of_a_copy():
+    """A copy compares its entries with each other: as many as a pool has rows."""
+    p = nat.PoolParams()
+    p.extent = nat._i64x3(1, 1, 4)
+    p.src, p.dst = ctypes.c_void_p(0x100000), ctypes.c_void_p(0x900000)
+    p.src_pool_rows = p.dst_pool_rows = 16
+    p.src_rows = p.dst_rows = FAKE
+    check = lambda mode: nat.lib().gdn_validate_pool_host(ctypes.byref(p), mode)  # noqa: E731
+    for mode in (0, 1, 2):
+        p.count = nat.POOL_MAX_ROWS
+        assert check(mode) == 0
+        p.count += 1
+        assert check(mode) == (SHAPE if mode == 0 else 0)
