@@ -13,6 +13,8 @@
 
 #include <ATen/ATen.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/core/GradMode.h>
+#include <c10/util/SmallVector.h>
 
 #include <mutex>
 #include <vector>
@@ -109,9 +111,31 @@ int index_type(const char *name, const Tensor &t) {
   return t.scalar_type() == at::kLong ? GDN_I64 : GDN_I32;
 }
 
-void *status_word(PyObject *o, const at::Device &dev) {
+// The tensors that a call writes, for autograd: as with torch's own in-place
+// operators, one that requires a gradient is refused, and after the launch their
+// versions advance, so that a graph that saved one of them raises instead of
+// using what is there now.
+struct Writes {
+  c10::SmallVector<const Tensor *, 8> all;
+
+  void add(const char *name, const Tensor &t) {
+    BAD_IF(c10::GradMode::is_enabled() && t.requires_grad(), name,
+           " requires a gradient and cannot be written; use torch.no_grad()");
+    all.push_back(&t);
+  }
+  void add(const char *name, const Tensor *t) {
+    if (t) add(name, *t);
+  }
+  void done() const {
+    for (const Tensor *t : all)  // (an inference tensor has no version)
+      if (!t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+  }
+};
+
+void *status_word(PyObject *o, const at::Device &dev, Writes &writes) {
   const Tensor *t = optional("status", o, dev);
   BAD_IF(t && (t->scalar_type() != at::kInt || t->numel() < 1), "status must be an int32 tensor");
+  writes.add("status", t);
   return ptr(t);
 }
 
@@ -165,6 +189,7 @@ struct Rec {
   const Tensor &x, &g;
   at::Device dev;
   int64_t T, H, D, N = 1;
+  Writes writes;
   Tensor init_copy;  // an expanded initial state, made contiguous
   Tensor memory;
 
@@ -245,6 +270,7 @@ struct Rec {
     initial(init, rows);
     if (!with_final) return Tensor();
     BAD_IF(!out && idx, "output_state (the pool) is required with state_indices");
+    writes.add("output_state", out);
     Tensor fin = out ? *out : states(N);
     check_state("output_state", fin, rows);
     BAD_IF(expanded(fin), "output_state must not be an expanded view (a stride of 0 on a "
@@ -259,6 +285,7 @@ struct Rec {
   Tensor output(PyObject *o) {
     const Tensor *t = optional("output", o, dev);
     if (t) exactly("output", *t, x.sizes(), x.scalar_type());
+    writes.add("output", t);
     Tensor out = t ? *t : like_x();
     p.output = out.data_ptr();
     return out;
@@ -305,7 +332,7 @@ PyObject *rec_forward(PyObject *const *a) {
   const bool with_final = PyObject_IsTrue(a[3]) == 1, keep = PyObject_IsTrue(a[8]) == 1;
   const Tensor out = r.output(a[5]);
   const Tensor fin = r.forward_states(a[2], with_final, a[6], a[7]);
-  r.p.status = (int32_t *)status_word(a[9], r.dev);
+  r.p.status = (int32_t *)status_word(a[9], r.dev, r.writes);
   Tensor kept;
   if (keep) {
     kept = fresh(r.chunk_shape(), at::kFloat, r.dev);
@@ -313,6 +340,7 @@ PyObject *rec_forward(PyObject *const *a) {
   }
   r.take_workspace(a[10], false);
   launch(r.dev, [&](void *s) { return lib.rec_forward(&r.p, s); });
+  r.writes.done();
   return pack({give(out), give_or_none(with_final, fin), give_or_none(keep, kept)});
 }
 
@@ -340,7 +368,10 @@ PyObject *rec_backward(PyObject *const *a) {
   const Tensor *dx_ = buffer("dx", a[8], r.x.sizes(), r.x.scalar_type());
   const Tensor *dg_ = buffer("dg", a[9], r.g.sizes(), r.g.scalar_type());
   const Tensor *di_ = buffer("dinitial_state", a[10], rows, at::kFloat);
-  r.p.status = (int32_t *)status_word(a[11], r.dev);
+  r.writes.add("dx", dx_);
+  r.writes.add("dg", dg_);
+  if (with_init) r.writes.add("dinitial_state", di_);
+  r.p.status = (int32_t *)status_word(a[11], r.dev, r.writes);
   const Tensor dx = dx_ ? *dx_ : r.like_x();
   const Tensor dg = dg_ ? *dg_ : fresh(r.g.sizes(), r.g.scalar_type(), r.dev);
   r.p.dx = dx.data_ptr();
@@ -352,6 +383,7 @@ PyObject *rec_backward(PyObject *const *a) {
   }
   r.take_workspace(a[12], true);
   launch(r.dev, [&](void *s) { return lib.rec_backward(&r.p, s); });
+  r.writes.done();
   return with_init ? pack({give(dx), give(dg), give(di)}) : pack({give(dx), give(dg)});
 }
 
@@ -362,8 +394,9 @@ PyObject *rec_decode(PyObject *const *a) {
   const bool with_final = PyObject_IsTrue(a[3]) == 1;
   const Tensor out = r.output(a[4]);
   const Tensor fin = r.forward_states(a[2], with_final, a[5], a[6]);
-  r.p.status = (int32_t *)status_word(a[7], r.dev);
+  r.p.status = (int32_t *)status_word(a[7], r.dev, r.writes);
   launch(r.dev, [&](void *s) { return lib.rec_decode(&r.p, s); });
+  r.writes.done();
   return with_final ? pack({give(out), give(fin)}) : give(out);
 }
 
@@ -426,7 +459,9 @@ PyObject *pool_copy(PyObject *const *a) {
          "src_rows and dst_rows must share a dtype");
   BAD_IF(src_rows.numel() != dst_rows.numel(),
          "src_rows and dst_rows must have the same length");
-  p.status = (int32_t *)status_word(a[4], dev);
+  Writes writes;
+  writes.add("pool", pool);
+  p.status = (int32_t *)status_word(a[4], dev, writes);
   Tensor from = a[3] == Py_None ? pool : tensor("src_pool", a[3]);
   BAD_IF(from.device() != dev, "src_pool must be on ", dev);
   if (expanded(from)) from = from.contiguous();
@@ -444,6 +479,7 @@ PyObject *pool_copy(PyObject *const *a) {
     BAD_IF(p.count > 0, "a pool without rows cannot be copied from or into");
   } else {
     launch(dev, [&](void *s) { return lib.pool_copy(&p, s); });
+    writes.done();
   }
   Py_INCREF(a[0]);
   return a[0];
@@ -456,10 +492,13 @@ PyObject *pool_reset(PyObject *const *a) {
   gdn_pool_params p{};
   set_destination(p, PoolView("pool", pool, true));
   p.rows_type = index_type("rows", rows);
-  p.status = (int32_t *)status_word(a[2], pool.device());
+  Writes writes;
+  writes.add("pool", pool);
+  p.status = (int32_t *)status_word(a[2], pool.device(), writes);
   p.dst_rows = rows.data_ptr();
   p.count = rows.numel();
   launch(pool.device(), [&](void *s) { return lib.pool_reset(&p, s); });
+  writes.done();
   Py_INCREF(a[0]);
   return a[0];
 }
@@ -481,11 +520,15 @@ PyObject *pool_compact(PyObject *const *a) {
   BAD_IF(map && (map->scalar_type() != at::kInt || map->dim() != 1 || first.dim() < 1 ||
                  map->size(0) != first.size(0) || !map->is_contiguous()),
          "row_map must be contiguous int32 [rows] on ", dev);
-  int32_t *status = (int32_t *)status_word(a[4], dev);
+  Writes writes;
+  writes.add("output_indices", out_);
+  writes.add("row_map", map);
+  int32_t *status = (int32_t *)status_word(a[4], dev, writes);
   std::vector<gdn_pool_params> calls((size_t)n);
   for (Py_ssize_t i = 0; i < n; ++i) {
     const Tensor &pool = tensor("pool", PyList_GET_ITEM(a[0], i));
     BAD_IF(pool.device() != dev, "pools must share a device");
+    writes.add("pool", pool);
     gdn_pool_params p{};
     set_destination(p, PoolView("pool", pool, true));
     BAD_IF(pool.size(0) != first.size(0), "pools must share a number of rows");
@@ -502,6 +545,7 @@ PyObject *pool_compact(PyObject *const *a) {
       return lib.pool_compact(&p, out.data_ptr(), (int32_t *)live.data_ptr(), (int32_t *)ptr(map),
                               s);
     });
+  writes.done();
   return pack({give(out), give(live)});
 }
 

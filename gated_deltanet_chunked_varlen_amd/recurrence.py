@@ -71,6 +71,9 @@ def gated_linear_recurrence(x, g, initial_state=None, output_final_state=False, 
     ``return_chunk_states`` the float32 states that
     ``gated_linear_recurrence_backward`` starts from.
 
+    A tensor that the call writes must not require a gradient (but under
+    torch.no_grad()), and its autograd version advances.
+
     Where x, g or initial_state require a gradient (and grad mode is on) the
     call is differentiable; it then takes no output buffers, state_indices,
     status or workspace, initial_state is float32, bfloat16 or float16, and it

@@ -5,7 +5,9 @@ A pool is any tensor whose first dimension counts rows and whose other one to
 three dimensions are a state: [rows, H, V, K] of ``chunk_gated_delta_rule``,
 [rows, H, D] of ``gated_linear_recurrence``, or [rows, n].  Views are taken as
 they are (a layer's slice of a [rows, layers, ...] pool).  Row lists are int32
-or int64 device tensors; an entry of -1 is padding.
+or int64 device tensors; an entry of -1 is padding.  As with torch's in-place
+operators a pool must not require a gradient (but under torch.no_grad()), and
+its autograd version advances.
 """
 from __future__ import annotations
 

@@ -1,0 +1,121 @@
+"""GPU tests of what the recurrence and the state-pool calls owe to autograd: writes
+in place are seen by graphs that saved the tensor, and nothing is detached from a
+gradient without a word."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from gated_deltanet_chunked_varlen_amd import (  # noqa: E402
+    gated_linear_recurrence, gated_linear_recurrence_backward, gated_linear_recurrence_decode,
+    state_pool_compact, state_pool_copy, state_pool_reset)
+from tests import recurrence_testlib as R  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    yield
+
+
+def _rows(*r):
+    return torch.tensor(r, dtype=torch.int32, device="cuda")
+
+
+LENS = [10, 7]
+
+
+def _writers(d, pool):
+    """Calls that write a [4, 2, 32] pool in place, by name."""
+    idx = _rows(0, 3)
+    one = d["x"][:2]
+    gate = d["g"][:2]
+    other = torch.zeros_like(pool)
+    return {
+        "reset": lambda: state_pool_reset(pool, _rows(0)),
+        "copy": lambda: state_pool_copy(pool, _rows(2), _rows(0)),
+        "copy in": lambda: state_pool_copy(pool, _rows(2), _rows(0), src_pool=other),
+        "compact": lambda: state_pool_compact([other, pool], _rows(3, 1)),
+        "forward": lambda: gated_linear_recurrence(
+            d["x"], d["g"], initial_state=pool, output_final_state=True, cu_seqlens=d["cu"],
+            output_state=pool, state_indices=idx),
+        "decode": lambda: gated_linear_recurrence_decode(
+            one, gate, initial_state=pool, output_state=pool, state_indices=idx),
+    }
+
+
+@pytest.mark.parametrize("name", ["reset", "copy", "copy in", "compact", "forward", "decode"])
+def test_pool_writes_are_seen_by_the_graph(name):
+    """A differentiable call that starts from pool rows; the pool is written
+    before the backward pass: it raises, as after torch's in-place operators."""
+    d = R.make(80, LENS, 2, 32)
+    pool = torch.randn((4, 2, 32), device="cuda")
+    x = d["x"].clone().requires_grad_()
+    out = gated_linear_recurrence(x, d["g"], initial_state=pool[:2], cu_seqlens=d["cu"])
+    version = pool._version
+    _writers(d, pool)[name]()
+    assert pool._version > version
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        out.sum().backward()
+
+
+def test_buffer_writes_are_seen_by_the_graph():
+    d = R.make(81, LENS, 2, 32)
+    buf = d["x"].clone()
+    g = d["g"].clone().requires_grad_()
+    out = gated_linear_recurrence(buf, g, cu_seqlens=d["cu"])
+    gated_linear_recurrence(buf, d["g"], cu_seqlens=d["cu"], output=buf)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        out.sum().backward()
+    # every buffer that the calls take
+    T, N = d["x"].shape[0], 2
+    bufs = {k: torch.empty_like(d[v]) for k, v in
+            (("dx", "x"), ("dg", "g"), ("dinitial_state", "h0"))}
+    st = _rows(0)
+    gated_linear_recurrence_backward(d["dy"], d["x"], d["g"], cu_seqlens=d["cu"],
+                                     output_dinitial_state=True, status=st, **bufs)
+    assert all(b._version == 1 for b in bufs.values()) and st._version == 1
+    ren, where = _rows(0, 0), _rows(0, 0, 0, 0)
+    state_pool_compact(torch.zeros((4, 8), device="cuda"), _rows(1, 2), output_indices=ren,
+                       row_map=where, status=st)
+    assert ren._version == where._version == 1 and st._version == 2
+    out1 = torch.empty((2, 2, 32), device="cuda")
+    gated_linear_recurrence_decode(d["x"][:2], d["g"][:2], output=out1, output_final_state=False,
+                                   status=st)
+    assert out1._version == 1 and st._version == 3
+    # what is only read does not change its version
+    assert d["x"]._version == d["g"]._version == d["h0"]._version == 0
+
+
+def test_written_tensors_that_require_a_gradient():
+    d = R.make(82, LENS, 2, 32)
+    leaf = torch.randn((4, 2, 32), device="cuda", requires_grad=True)
+    keep = leaf.detach().clone()
+    for pool in (leaf, leaf * 1.0):
+        for name, call in _writers(d, pool).items():
+            if name == "forward":
+                continue  # differentiable there, and then takes no output_state
+            with pytest.raises(ValueError):
+                call()
+        with pytest.raises(ValueError):
+            gated_linear_recurrence(d["x"], d["g"], output=torch.empty_like(d["x"],
+                                                                            requires_grad=True))
+    assert torch.equal(leaf.detach(), keep)
+    with torch.no_grad():
+        state_pool_reset(leaf, _rows(1))
+    keep[1] = 0
+    assert torch.equal(leaf.detach(), keep)
+
+
+def test_inference_tensors():
+    d = R.make(83, LENS, 2, 32)
+    with torch.inference_mode():
+        pool = torch.randn((4, 2, 32), device="cuda")
+        state_pool_reset(pool, _rows(1))
+        assert (pool[1] == 0).all()
+        gated_linear_recurrence_decode(d["x"][:2], d["g"][:2], initial_state=pool,
+                                       output_state=pool, state_indices=_rows(0, 3))
+    state_pool_reset(pool, _rows(2))
+    assert (pool[2] == 0).all()
