@@ -12,6 +12,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ATen.h>
+#include <c10/core/AutogradState.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/core/GradMode.h>
 #include <c10/util/SmallVector.h>
@@ -111,16 +112,25 @@ int index_type(const char *name, const Tensor &t) {
   return t.scalar_type() == at::kLong ? GDN_I64 : GDN_I32;
 }
 
+// Refuses a tensor whose derivatives the call would drop without a word: one that
+// requires a gradient while gradients are recorded, or a dual tensor of forward
+// mode.
+void no_derivative(const char *name, const Tensor &t) {
+  BAD_IF(c10::GradMode::is_enabled() && t.requires_grad(), name,
+         " requires a gradient, but this call is not differentiable; use torch.no_grad()");
+  BAD_IF(c10::AutogradState::get_tls_state().get_fw_grad_mode() && t._fw_grad(0).defined(), name,
+         " has a tangent, but there is no forward-mode derivative");
+}
+
 // The tensors that a call writes, for autograd: as with torch's own in-place
-// operators, one that requires a gradient is refused, and after the launch their
-// versions advance, so that a graph that saved one of them raises instead of
+// operators on leaves, one that requires a gradient is refused, and after the
+// launch their versions advance, so that a graph that saved one of them raises instead of
 // using what is there now.
 struct Writes {
   c10::SmallVector<const Tensor *, 8> all;
 
   void add(const char *name, const Tensor &t) {
-    BAD_IF(c10::GradMode::is_enabled() && t.requires_grad(), name,
-           " requires a gradient and cannot be written; use torch.no_grad()");
+    no_derivative(name, t);
     all.push_back(&t);
   }
   void add(const char *name, const Tensor *t) {
@@ -196,6 +206,8 @@ struct Rec {
   Rec(PyObject *x_, PyObject *g_, PyObject *cu_, bool decode)
       : x(tensor("x", x_)), g(tensor("g", g_)), dev(x.device()) {
     BAD_IF(!x.is_cuda(), "x must be a device tensor");
+    no_derivative("x", x);
+    no_derivative("g", g);
     BAD_IF(g.device() != dev, "g must be on ", dev);
     BAD_IF(x.dim() != 3, "x must be [total_seq_len, heads, head_size]");
     p.x_dtype = float_type(x.scalar_type());
@@ -242,6 +254,7 @@ struct Rec {
   void initial(const Tensor *t, int64_t rows) {
     if (!t) return;
     check_state("initial_state", *t, rows);
+    no_derivative("initial_state", *t);
     if (expanded(*t)) {
       init_copy = t->contiguous();
       t = &init_copy;
@@ -353,6 +366,7 @@ PyObject *rec_backward(PyObject *const *a) {
   BAD_IF(dout.device() != r.dev, "doutput must be on ", r.dev);
   BAD_IF(dout.scalar_type() != r.x.scalar_type() || dout.sizes() != r.x.sizes(),
          "doutput must have x's shape and dtype");
+  no_derivative("doutput", dout);
   r.p.doutput = dout.data_ptr();
   r.p.doutput_stride = row_stride("doutput", dout, r.H * r.D);
   r.initial(optional("initial_state", a[3], r.dev), r.N);
@@ -360,6 +374,7 @@ PyObject *rec_backward(PyObject *const *a) {
   auto buffer = [&](const char *name, PyObject *o, at::IntArrayRef shape, at::ScalarType type) {
     const Tensor *t = optional(name, o, r.dev);
     if (t) exactly(name, *t, shape, type);
+    if (t) no_derivative(name, *t);
     return t;
   };
   r.p.dfinal_state = (const float *)ptr(buffer("dfinal_state", a[4], rows, at::kFloat));
@@ -464,6 +479,7 @@ PyObject *pool_copy(PyObject *const *a) {
   p.status = (int32_t *)status_word(a[4], dev, writes);
   Tensor from = a[3] == Py_None ? pool : tensor("src_pool", a[3]);
   BAD_IF(from.device() != dev, "src_pool must be on ", dev);
+  no_derivative("src_pool", from);
   if (expanded(from)) from = from.contiguous();
   const PoolView v("src_pool", from, false);
   for (int i = 0; i < 3; ++i)

@@ -77,7 +77,8 @@ def gated_linear_recurrence(x, g, initial_state=None, output_final_state=False, 
     Where x, g or initial_state require a gradient (and grad mode is on) the
     call is differentiable; it then takes no output buffers, state_indices,
     status or workspace, initial_state is float32, bfloat16 or float16, and it
-    cannot be captured into a graph."""
+    cannot be captured into a graph.  There are no forward-mode derivatives:
+    dual tensors are refused."""
     needs = torch.is_grad_enabled() and any(
         isinstance(t, torch.Tensor) and t.requires_grad for t in (x, g, initial_state))
     if needs:
@@ -115,7 +116,9 @@ def gated_linear_recurrence_backward(doutput, x, g, initial_state=None, dfinal_s
     ``output_dinitial_state``: x's and g's shapes and dtypes, float32
     [N, H, D].  Rows of dx and dg outside every sequence are zero.  Results do
     not depend on the order in which the work runs.  No two tensors of a call
-    may overlap, and ``workspace`` is used as in the forward call."""
+    may overlap, and ``workspace`` is used as in the forward call.  The call
+    itself is not differentiable: tensors that require a gradient are refused
+    (but under torch.no_grad())."""
     return calls().rec_backward(doutput, x, g, initial_state, dfinal_state, cu_seqlens,
                                 chunk_states, output_dinitial_state, dx, dg, dinitial_state,
                                 status, workspace)
@@ -125,6 +128,8 @@ def gated_linear_recurrence_decode(x, g, initial_state=None, output_final_state=
                                    output_state=None, state_indices=None, status=None):
     """One decode step: token i of x, g [N, ...] is the new token of sequence
     i.  States and ``state_indices`` are those of ``gated_linear_recurrence``.
-    Returns ``output`` [N, H, D], or ``(output, final_state)``."""
+    Returns ``output`` [N, H, D], or ``(output, final_state)``.  The call is
+    not differentiable: tensors that require a gradient are refused (but under
+    torch.no_grad())."""
     return calls().rec_decode(x, g, initial_state, output_final_state, output, output_state,
                               state_indices, status)

@@ -7,7 +7,8 @@ three dimensions are a state: [rows, H, V, K] of ``chunk_gated_delta_rule``,
 they are (a layer's slice of a [rows, layers, ...] pool).  Row lists are int32
 or int64 device tensors; an entry of -1 is padding.  As with torch's in-place
 operators a pool must not require a gradient (but under torch.no_grad()), and
-its autograd version advances.
+its autograd version advances.  No call is differentiable: a src_pool that
+requires a gradient is refused too.
 """
 from __future__ import annotations
 

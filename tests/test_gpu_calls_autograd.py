@@ -119,3 +119,59 @@ def test_inference_tensors():
                                        output_state=pool, state_indices=_rows(0, 3))
     state_pool_reset(pool, _rows(2))
     assert (pool[2] == 0).all()
+
+
+def test_calls_that_are_not_differentiable():
+    """Tensors that require a gradient are refused where the result would be
+    detached from them, and taken under no_grad."""
+    d = R.make(84, LENS, 2, 32)
+    need = lambda t: t.clone().requires_grad_()  # noqa: E731
+    pool = torch.zeros((4, 2, 32), device="cuda")
+    x, g, one, gate, h0 = d["x"], d["g"], d["x"][:2], d["g"][:2], d["h0"]
+    kw = dict(cu_seqlens=d["cu"])
+    calls = [
+        lambda t: gated_linear_recurrence_decode(t(one), gate),
+        lambda t: gated_linear_recurrence_decode(one, t(gate)),
+        lambda t: gated_linear_recurrence_decode(one, gate, initial_state=t(h0)),
+        lambda t: state_pool_copy(pool, _rows(0), _rows(0), src_pool=t(pool)),
+        lambda t: gated_linear_recurrence_backward(t(d["dy"]), x, g, **kw),
+        lambda t: gated_linear_recurrence_backward(d["dy"], t(x), g, **kw),
+        lambda t: gated_linear_recurrence_backward(d["dy"], x, t(g), **kw),
+        lambda t: gated_linear_recurrence_backward(d["dy"], x, g, initial_state=t(h0), **kw),
+        lambda t: gated_linear_recurrence_backward(d["dy"], x, g, dfinal_state=t(d["dfinal"]),
+                                                   **kw),
+        lambda t: gated_linear_recurrence_backward(
+            d["dy"], x, g, chunk_states=t(torch.zeros((1, 2, 32), device="cuda")), **kw),
+    ]
+    for call in calls:
+        call(lambda t: t)
+        with pytest.raises(ValueError):
+            call(need)
+        with torch.no_grad():
+            call(need)
+
+
+def test_forward_mode_is_refused():
+    import torch.autograd.forward_ad as fwAD
+    d = R.make(85, LENS, 2, 32)
+    pool = torch.zeros((4, 2, 32), device="cuda")
+    with fwAD.dual_level():
+        dual = lambda t: fwAD.make_dual(t.clone(), torch.ones_like(t))  # noqa: E731
+        calls = [
+            lambda t: gated_linear_recurrence(t(d["x"]), d["g"]),
+            lambda t: gated_linear_recurrence(d["x"], t(d["g"])),
+            lambda t: gated_linear_recurrence(d["x"], d["g"], initial_state=t(d["h0"]),
+                                              cu_seqlens=d["cu"]),
+            lambda t: gated_linear_recurrence_decode(t(d["x"]), d["g"]),
+            lambda t: state_pool_reset(t(pool), _rows(0)),
+            lambda t: state_pool_copy(pool, _rows(0), _rows(0), src_pool=t(pool)),
+        ]
+        for call in calls:
+            call(lambda t: t)
+            for grad in (torch.enable_grad(), torch.no_grad()):
+                with grad, pytest.raises(ValueError):
+                    call(dual)
+        # a tensor that requires a gradient and has a tangent
+        with pytest.raises((RuntimeError, ValueError)):
+            gated_linear_recurrence(fwAD.make_dual(d["x"].clone().requires_grad_(),
+                                                   torch.ones_like(d["x"])), d["g"])
