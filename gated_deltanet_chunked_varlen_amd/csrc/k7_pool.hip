@@ -221,11 +221,18 @@ __device__ __forceinline__ void list_status(const PoolArgs &a, unsigned *map) {
   }
   __syncthreads();
   if (a.same) {
-    for (int64_t i = threadIdx.x; i < a.count; i += kThreads) {
-      const int d = list_row(a.dst_rows, a.rows_type, i, a.dst_pool);
-      const int s = list_row(a.src_rows, a.rows_type, i, a.src_pool);
-      if (d >= 0 && s >= 0 && s != d && s < a.dst_pool && (map[s >> 5] >> (s & 31) & 1))
-        bits |= GDN_STATUS_POOL_OVERLAP;
+    // the rows that change: destinations of entries other than a row onto itself
+    for (int i = threadIdx.x; i < words; i += kThreads) map[i] = 0u;
+    __syncthreads();
+    for (int pass = 0; pass < 2; ++pass) {
+      for (int64_t i = threadIdx.x; i < a.count; i += kThreads) {
+        const int d = list_row(a.dst_rows, a.rows_type, i, a.dst_pool);
+        const int s = list_row(a.src_rows, a.rows_type, i, a.src_pool);
+        if (d < 0 || s < 0 || s == d) continue;
+        if (pass == 0) atomicOr(&map[d >> 5], 1u << (d & 31));
+        else if (s < a.dst_pool && (map[s >> 5] >> (s & 31) & 1)) bits |= GDN_STATUS_POOL_OVERLAP;
+      }
+      __syncthreads();
     }
   }
   if (bits) atomicOr(&s_bits, bits);
@@ -233,11 +240,11 @@ __device__ __forceinline__ void list_status(const PoolArgs &a, unsigned *map) {
   if (threadIdx.x == 0) a.status[0] = (int32_t)s_bits;
 }
 
-// Entry j (destination dj) keeps entry i (source si, destination di) from
-// acting.
-__device__ __forceinline__ bool conflict(const PoolArgs &a, int64_t j, int dj, int64_t i, int si,
-                                         int di) {
-  return (j > i && dj == di) || (a.same && j != i && dj == si && si != di);
+// Entry j (source sj, destination dj) keeps entry i from acting: it has the same
+// destination and comes later, or it changes entry i's source row.
+__device__ __forceinline__ bool conflict(const PoolArgs &a, int64_t j, int sj, int dj, int64_t i,
+                                         int si, int di) {
+  return (j > i && dj == di) || (a.same && j != i && dj == si && sj != dj && si != di);
 }
 
 // Some entry of the list keeps entry i from acting; for the whole workgroup.
@@ -246,14 +253,15 @@ __device__ __forceinline__ bool skipped(const PoolArgs &a, int64_t i, int si, in
   for (int64_t j = threadIdx.x; j < a.count; j += kThreads) {
     const int d = list_row(a.dst_rows, a.rows_type, j, a.dst_pool);
     const int s = list_row(a.src_rows, a.rows_type, j, a.src_pool);
-    if (d >= 0 && s >= 0) hit |= conflict(a, j, d, i, si, di);
+    if (d >= 0 && s >= 0) hit |= conflict(a, j, s, d, i, si, di);
   }
   return __syncthreads_or(hit) != 0;
 }
 
 // Which entries act: entry i is skipped if a later entry has its destination,
-// or (in one pool) if another entry's destination is its source.  Entries with
-// a row outside its pool take no part.
+// or (in one pool) if another entry's destination is its source, unless that
+// entry copies the row onto itself (such an entry has nothing to do, but wins its
+// destination).  Entries with a row outside its pool take no part.
 //
 // MOVE::row moves elements of a row; MOVE::kZero: there are no sources.
 template <typename MOVE>
@@ -276,7 +284,7 @@ __global__ void __launch_bounds__(kThreads) pool_list_kernel(PoolArgs a, Units u
         dst = list_row(a.dst_rows, a.rows_type, i, a.dst_pool);
         src = kZero ? 0 : list_row(a.src_rows, a.rows_type, i, a.src_pool);
       }
-      if (dst < 0 || src < 0) continue;
+      if (dst < 0 || src < 0 || (!kZero && a.same && src == dst)) continue;
       if constexpr (kZero) {
         MOVE::row(a, src, dst, e0, e1, []() { return true; });
       } else {
@@ -301,7 +309,7 @@ __global__ void __launch_bounds__(kThreads) pool_list_kernel(PoolArgs a, Units u
       const int s = list_row(a.src_rows, a.rows_type, i0 + threadIdx.x, a.src_pool);
       s_src[threadIdx.x] = s;
       s_dst[threadIdx.x] = d;
-      s_skip[threadIdx.x] = d < 0 || s < 0;
+      s_skip[threadIdx.x] = d < 0 || s < 0 || (a.same && s == d);
     }
     __syncthreads();
     for (int64_t j = threadIdx.x; j < a.count; j += kThreads) {
@@ -309,7 +317,7 @@ __global__ void __launch_bounds__(kThreads) pool_list_kernel(PoolArgs a, Units u
       const int s = list_row(a.src_rows, a.rows_type, j, a.src_pool);
       if (d < 0 || s < 0) continue;
       for (int p = 0; p < n; ++p)
-        if (conflict(a, j, d, i0 + p, s_src[p], s_dst[p])) s_skip[p] = 1;
+        if (conflict(a, j, s, d, i0 + p, s_src[p], s_dst[p])) s_skip[p] = 1;
     }
     __syncthreads();
     for (int p = 0; p < n; ++p)

@@ -22,7 +22,9 @@ def state_pool_copy(pool, src_rows, dst_rows, src_pool=None, status=None):
 
     Equal dtypes copy bit for bit, others round to nearest (8-bit types
     saturate).  A destination named twice takes its last entry; inside one
-    pool an entry whose source row is another entry's destination is skipped;
+    pool an entry whose source row is another entry's destination is skipped,
+    unless that one copies the row onto itself (src [0, 0], dst [0, 1] keeps
+    row 0 and forks it; a swap is skipped both ways);
     entries outside the pools are skipped.  A list holds at most 262144
     entries; it is meant for a few thousand (each is compared with all
     others).  ``status`` (optional int32 device

@@ -87,7 +87,7 @@ typedef enum { GDN_I32 = 0, GDN_I64 = 1 } gdn_itype;
 #define GDN_STATUS_CHUNK_CAPACITY 8u    /* more chunks than the sync-free bound (never expected) */
 #define GDN_STATUS_POOL_ROW 16u         /* a pool row index outside its pool (-1 is padding, not an error) */
 #define GDN_STATUS_POOL_DUPLICATE 32u   /* a destination row named twice (the last entry wins) */
-#define GDN_STATUS_POOL_OVERLAP 64u     /* a source row that another entry overwrites (that entry is skipped) */
+#define GDN_STATUS_POOL_OVERLAP 64u     /* a source row that another entry overwrites (the entry that reads it is skipped) */
 
 /*
  * Parameters of one prefill call (gitcode, section "API 全参数解析"; the
@@ -437,7 +437,8 @@ int gdn_validate_pool_host(const gdn_pool_params *p, int32_t mode);
  * the same view; other views may share no elements (GDN_ERR_STATE where the
  * host can see that they do).  A destination named twice takes its last
  * entry.  In one pool an entry whose source row is another entry's destination
- * is skipped.  Both set their status bit.  At most GDN_POOL_MAX_ROWS entries
+ * is skipped, unless that one copies the row onto itself (it changes nothing, so
+ * a row can be kept and forked in one list).  Both set their status bit.  At most GDN_POOL_MAX_ROWS entries
  * (GDN_ERR_SHAPE): each is compared with all others. */
 int gdn_pool_copy(const gdn_pool_params *p, void *stream);
 

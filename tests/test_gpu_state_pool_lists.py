@@ -1,0 +1,64 @@
+"""GPU tests of the state-pool operators' lists: rows kept and forked in one list,
+conflicts by the rule, against a plain copy of the rule."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from gated_deltanet_chunked_varlen_amd import state_pool_copy  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+OUT, DUP, OVER = 16, 32, 64
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    yield
+
+
+def _rows(values, dtype=torch.int32):
+    return torch.tensor(values, dtype=dtype, device="cuda")
+
+
+def _copy_rule(pool, src, dst):
+    """The pool and the status bits after a copy inside it, entry by entry."""
+    n = pool.shape[0]
+    want, bits = pool.clone(), 0
+    ok = [s >= 0 and d >= 0 and s < n and d < n for s, d in zip(src, dst)]
+    if any(v >= n or v < -1 for v in list(src) + list(dst)):
+        bits |= OUT
+    entries = [(i, s, d) for i, (s, d) in enumerate(zip(src, dst)) if ok[i]]
+    for i, s, d in entries:
+        later = any(j > i and e == d for j, _, e in entries)
+        changed = s != d and any(j != i and e == s and f != e for j, f, e in entries)
+        bits |= (DUP if later else 0) | (OVER if changed else 0)
+        if not later and not changed:
+            want[d] = pool[s]
+    return want, bits
+
+
+# long rows go one entry at a time, short ones in groups once there are many
+@pytest.mark.parametrize("rows,row", [(16, (64, 128)), (4000, (4,)), (4000, (3,))])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rows_kept_and_forked(rows, row, dtype):
+    gen = torch.Generator().manual_seed(rows)
+    ref = torch.randn((rows,) + row, generator=gen).to(dtype).cuda()
+    lists = [([0, 0], [0, 1]), ([0, 0], [1, 0]), ([3, 5, 3, 5, 3], [3, 5, 6, 7, 8]),
+             # a row kept and overwritten by an earlier or a later entry
+             ([2, 0, 0], [0, 0, 1]), ([0, 2, 0], [0, 0, 1]),
+             ([1, 0], [0, 1]), ([4, 4], [4, 4])]
+    if rows > 1000:  # each of the first half kept, and forked into the second half
+        half = list(range(rows // 2))
+        lists.append((half + half, half + [rows // 2 + r for r in half]))
+        mix = torch.randint(-2, rows + 2, (2, 3000), generator=gen).tolist()
+        mix[0][::7] = mix[1][::7]  # kept rows among them
+        lists.append((mix[0], mix[1]))
+    for src, dst in lists:
+        want, bits = _copy_rule(ref.cpu(), src, dst)
+        for status in (None, _rows([-1])):
+            pool = ref.clone()
+            state_pool_copy(pool, _rows(src), _rows(dst), status=status)
+            assert torch.equal(pool.cpu(), want), (src[:8], dst[:8])
+            assert status is None or status.item() == bits
