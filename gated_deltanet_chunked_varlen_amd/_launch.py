@@ -48,7 +48,8 @@ def calls():
                               "`python -m gated_deltanet_chunked_varlen_amd.build`") from None
         address = [ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
             "gdn_recurrence_workspace_size", "gdn_recurrence", "gdn_recurrence_backward",
-            "gdn_recurrence_decode", "gdn_pool_copy", "gdn_pool_reset", "gdn_pool_compact")]
+            "gdn_recurrence_decode", "gdn_pool_copy", "gdn_pool_reset", "gdn_pool_compact",
+            "gdn_validate_pool_host")]
         # torch's own accessor of the raw handle where it has one: a tenth of the time
         stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream)
         _calls.bind(*address, api._raise, stream, _workspace)

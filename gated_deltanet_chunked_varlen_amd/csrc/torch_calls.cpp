@@ -36,6 +36,7 @@ struct Bound {
   int (*pool_copy)(const gdn_pool_params *, void *) = nullptr;
   int (*pool_reset)(const gdn_pool_params *, void *) = nullptr;
   int (*pool_compact)(const gdn_pool_params *, void *, int32_t *, int32_t *, void *) = nullptr;
+  int (*pool_validate)(const gdn_pool_params *, int32_t) = nullptr;
   PyObject *raise = nullptr;      // raise(code): the exception of an error code
   PyObject *stream = nullptr;     // stream(device index) -> handle of its current stream
   PyObject *workspace = nullptr;  // workspace(device index, stream, bytes) -> uint8 tensor
@@ -62,8 +63,16 @@ void *current_stream(const at::Device &dev) {
 // one left it.
 std::mutex enqueue;
 
-// Launches with the tensors' device current; an error code becomes the
-// binding's exception.
+// An error code becomes the binding's exception.
+void check(int rc) {
+  if (rc == GDN_OK) return;
+  PyObject *r = PyObject_CallFunction(lib.raise, "i", rc);
+  Py_XDECREF(r);
+  if (r) PyErr_SetString(PyExc_RuntimeError, "the library returned an error code");
+  throw PythonError{};
+}
+
+// Launches with the tensors' device current.
 template <typename F> void launch(const at::Device &dev, F f) {
   const c10::DeviceGuard guard(dev);
   void *stream = current_stream(dev);
@@ -74,11 +83,7 @@ template <typename F> void launch(const at::Device &dev, F f) {
     rc = f(stream);
   }
   Py_END_ALLOW_THREADS;
-  if (rc == GDN_OK) return;
-  PyObject *r = PyObject_CallFunction(lib.raise, "i", rc);
-  Py_XDECREF(r);
-  if (r) PyErr_SetString(PyExc_RuntimeError, "the library returned an error code");
-  throw PythonError{};
+  check(rc);
 }
 
 // --------------------------------------------------------------------- tensors
@@ -552,6 +557,7 @@ PyObject *pool_compact(PyObject *const *a) {
     p.status = status;
     p.dst_rows = idx.data_ptr();
     p.count = idx.numel();
+    check(lib.pool_validate(&p, 2));  // every pool before the first is moved
     calls[(size_t)i] = p;
   }
   const Tensor out = out_ ? *out_ : fresh(idx.sizes(), idx.scalar_type(), dev);
@@ -586,14 +592,15 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// bind(seven addresses, raise, stream, workspace)
+// bind(eight addresses, raise, stream, workspace)
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
-  if (n != 10) {
-    PyErr_SetString(PyExc_TypeError, "ten arguments expected");
+  constexpr int kEntries = 8;
+  if (n != kEntries + 3) {
+    PyErr_SetString(PyExc_TypeError, "eleven arguments expected");
     return nullptr;
   }
-  void *f[7];
-  for (int i = 0; i < 7; ++i) {
+  void *f[kEntries];
+  for (int i = 0; i < kEntries; ++i) {
     f[i] = PyLong_AsVoidPtr(a[i]);
     if (!f[i]) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "a NULL entry point");
@@ -607,10 +614,11 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
   lib.pool_copy = (decltype(lib.pool_copy))f[4];
   lib.pool_reset = (decltype(lib.pool_reset))f[5];
   lib.pool_compact = (decltype(lib.pool_compact))f[6];
-  for (int i = 7; i < 10; ++i) Py_INCREF(a[i]);
-  lib.stream = a[8];
-  lib.workspace = a[9];
-  lib.raise = a[7];
+  lib.pool_validate = (decltype(lib.pool_validate))f[7];
+  for (int i = kEntries; i < kEntries + 3; ++i) Py_INCREF(a[i]);
+  lib.stream = a[kEntries + 1];
+  lib.workspace = a[kEntries + 2];
+  lib.raise = a[kEntries];
   Py_RETURN_NONE;
 }
 

@@ -48,7 +48,8 @@ def state_pool_compact(pools, state_indices, output_indices=None, row_map=None, 
     (ascending) is copied to the k-th row before m that is not live; no other
     row changes, so rows at or behind m can be dropped or reused.  ``pools`` is
     one pool or a list of pools with the same number of rows and the same use
-    of them (the layers of a model), all moved alike.  Returns (state_indices
+    of them (the layers of a model), all moved alike, or none if one of them is
+    refused.  Returns (state_indices
     with the moved rows renamed, num_live int32 [1]); output_indices, if given,
     receives the renamed list and must not overlap state_indices.  row_map
     (int32 [rows]) receives each row's new place, -1 for rows not live.

@@ -4,7 +4,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from gated_deltanet_chunked_varlen_amd import state_pool_copy  # noqa: E402
+from gated_deltanet_chunked_varlen_amd import state_pool_compact, state_pool_copy  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -62,3 +62,20 @@ def test_rows_kept_and_forked(rows, row, dtype):
             state_pool_copy(pool, _rows(src), _rows(dst), status=status)
             assert torch.equal(pool.cpu(), want), (src[:8], dst[:8])
             assert status is None or status.item() == bits
+
+
+def test_compact_moves_all_pools_or_none():
+    first = torch.arange(12, device="cuda", dtype=torch.float32).view(12, 1).repeat(1, 8)
+    want = first.clone()
+    base = torch.zeros(400, device="cuda")
+    overlapping = base.as_strided((12, 8), (4, 1))  # rows that share elements
+    out, where = _rows([-5, -5]), _rows([-5] * 12)
+    for bad in (overlapping, base[:12].view(12, 1).expand(12, 8), first.double(), first[:11],
+                first.cpu()):
+        with pytest.raises(ValueError):
+            state_pool_compact([first, bad], _rows([11, 7]), output_indices=out, row_map=where)
+        assert torch.equal(first, want)
+        assert (out == -5).all() and (where == -5).all()
+    ren, n = state_pool_compact([first, want.clone()], _rows([11, 7]), output_indices=out)
+    assert ren.tolist() == [1, 0] and n.item() == 2
+    assert first[:2, 0].tolist() == [7, 11]
