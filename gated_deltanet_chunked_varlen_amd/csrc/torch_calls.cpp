@@ -47,6 +47,13 @@ struct Bound {
 // A Python callable was left with an exception.
 struct PythonError {};
 
+// A flag as Python reads it (its own exception where it has no truth value).
+bool truth(PyObject *o) {
+  const int r = PyObject_IsTrue(o);
+  if (r < 0) throw PythonError{};
+  return r == 1;
+}
+
 void *current_stream(const at::Device &dev) {
   PyObject *index = PyLong_FromLong(dev.index());
   PyObject *r = index ? PyObject_CallOneArg(lib.stream, index) : nullptr;
@@ -347,7 +354,7 @@ struct Rec {
 // -> (output, final state or None, chunk states or None)
 PyObject *rec_forward(PyObject *const *a) {
   Rec r(a[0], a[1], a[4], false);
-  const bool with_final = PyObject_IsTrue(a[3]) == 1, keep = PyObject_IsTrue(a[8]) == 1;
+  const bool with_final = truth(a[3]), keep = truth(a[8]);
   const Tensor out = r.output(a[5]);
   const Tensor fin = r.forward_states(a[2], with_final, a[6], a[7]);
   r.p.status = (int32_t *)status_word(a[9], r.dev, r.writes);
@@ -384,7 +391,7 @@ PyObject *rec_backward(PyObject *const *a) {
   };
   r.p.dfinal_state = (const float *)ptr(buffer("dfinal_state", a[4], rows, at::kFloat));
   r.p.chunk_states = (float *)ptr(buffer("chunk_states", a[6], r.chunk_shape(), at::kFloat));
-  const bool with_init = PyObject_IsTrue(a[7]) == 1;
+  const bool with_init = truth(a[7]);
   const Tensor *dx_ = buffer("dx", a[8], r.x.sizes(), r.x.scalar_type());
   const Tensor *dg_ = buffer("dg", a[9], r.g.sizes(), r.g.scalar_type());
   const Tensor *di_ = buffer("dinitial_state", a[10], rows, at::kFloat);
@@ -411,7 +418,7 @@ PyObject *rec_backward(PyObject *const *a) {
 //  state_indices, status) -> output or (output, final state)
 PyObject *rec_decode(PyObject *const *a) {
   Rec r(a[0], a[1], Py_None, true);
-  const bool with_final = PyObject_IsTrue(a[3]) == 1;
+  const bool with_final = truth(a[3]);
   const Tensor out = r.output(a[4]);
   const Tensor fin = r.forward_states(a[2], with_final, a[5], a[6]);
   r.p.status = (int32_t *)status_word(a[7], r.dev, r.writes);

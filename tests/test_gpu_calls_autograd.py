@@ -175,3 +175,20 @@ def test_forward_mode_is_refused():
         with pytest.raises((RuntimeError, ValueError)):
             gated_linear_recurrence(fwAD.make_dual(d["x"].clone().requires_grad_(),
                                                    torch.ones_like(d["x"])), d["g"])
+
+
+def test_flags_without_a_truth_value():
+    """The exception of the flag itself, before anything is launched."""
+    d = R.make(86, LENS, 2, 32)
+    both = torch.tensor([True, False])
+    out = torch.full_like(d["x"], 7.0)
+    for kw in (dict(output_final_state=both), dict(return_chunk_states=both)):
+        with pytest.raises(RuntimeError, match="ambiguous"):
+            gated_linear_recurrence(d["x"], d["g"], cu_seqlens=d["cu"], output=out, **kw)
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        gated_linear_recurrence_backward(d["dy"], d["x"], d["g"], output_dinitial_state=both,
+                                         dx=out)
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        gated_linear_recurrence_decode(d["x"], d["g"], output=out, output_final_state=both)
+    torch.cuda.synchronize()
+    assert (out == 7).all()
