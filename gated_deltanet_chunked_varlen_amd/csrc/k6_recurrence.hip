@@ -41,7 +41,9 @@
 // Sequence bounds.  A wave walks its tokens segment by segment, a segment
 // being the wave's part of one sequence; where a sequence starts the carry is
 // replaced by its initial state, never multiplied by zero, so a NaN or
-// infinity of one sequence does not reach the next.  Sweep 1 needs the last
+// infinity of one sequence does not reach the next.  Within a sequence an
+// infinite state stays infinite under gates above 0, so a product of such gates
+// that underflows is kept at kTiny (0 * infinity would be NaN).  Sweep 1 needs the last
 // segment only (the first one, going backward): what lies before a start does
 // not leave the wave.  The backward scan runs the chain from the last tile to
 // the first, with the carry k_t = g_t dh_t.
@@ -173,6 +175,18 @@ __device__ __forceinline__ void publish(unsigned long long *w, unsigned hi, floa
 __device__ __forceinline__ unsigned long long peek(const unsigned long long *w) {
   return __hip_atomic_load(w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
+// True for some lane, which is unusual: the same for the whole wave, so that what
+// it guards is a scalar branch to code that lies out of the way.
+__device__ __forceinline__ bool rare(bool b) { return __builtin_expect(__ballot(b) != 0, 0); }
+
+// The product of two runs' gates.  It is 0 only if a gate is.  (Elsewhere several
+// runs' products are multiplied plainly, and a 0 is looked into afterwards.)
+constexpr float kTiny = 0x1p-149f;
+__device__ __forceinline__ float gates_product(float A, float B) {
+  const float p = A * B;
+  return p == 0.f && A != 0.f && B != 0.f ? kTiny : p;
+}
+
 __device__ __forceinline__ unsigned mark(unsigned long long w) { return (unsigned)(w >> 32); }
 __device__ __forceinline__ float low(unsigned long long w) { return __uint_as_float((unsigned)w); }
 __device__ __forceinline__ unsigned map_bits(float A) {
@@ -219,6 +233,14 @@ __device__ __forceinline__ float look_back(const unsigned long long *groups, int
   }
 }
 
+// No wave's product of gates is 0, for one channel.
+__device__ __forceinline__ bool all_above_zero(const float (&sA)[kWaves][kRecChannels], int ch) {
+  bool positive = true;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) positive = positive && sA[w][ch] != 0.f;
+  return positive;
+}
+
 // A composed map h -> A h + B, or (known) the constant B.
 struct Map {
   float A, B;
@@ -262,13 +284,20 @@ __device__ __forceinline__ float chain(const RecArgs &a, int tile, unsigned c, i
         }
       }
     }
+    if (rare(m.A == 0.f && !m.known)) {
+      bool positive = true;
+#pragma unroll
+      for (int j = 0; j < kGroup - 1; ++j)
+        if (j < before) positive = positive && __uint_as_float(mark(w[j])) != 0.f;
+      if (m.A == 0.f && positive) m.A = kTiny;
+    }
     if (!open) m = {0.f, __uint_as_float(kNaN), true};  // given up
   }
   const int group = n / kGroup;
   unsigned long long *gword = a.groups + (int64_t)group * a.C + c;
   const bool closes = before == kGroup - 1;
   if (group == 0) m.known = true;  // nothing before: the state is zero
-  Map all = {m.A * own.A, fmaf(own.A, m.B, own.B), m.known};
+  Map all = {gates_product(m.A, own.A), fmaf(own.A, m.B, own.B), m.known};
   if (own.known) all = own;
   if (closes) publish(gword, all.known ? kLast : map_bits(all.A), all.B);
   if (m.known) return m.B;
@@ -519,6 +548,22 @@ __device__ __forceinline__ void by_marks(const Marks<TOK> &m, F f) {
   else f(std::false_type{});
 }
 
+// The product A of a plain wave's gates, formed by plain multiplications: kTiny
+// where it underflowed and no gate is 0.  Only a plain wave's product takes part
+// in a state that is used: before a wave with a start, or behind the last end, it
+// is replaced or belongs to no token.
+template <int TOK, typename GateT>
+__device__ __forceinline__ void keep_above_zero(const GateT (&g)[TOK], float (&A)[4]) {
+  if (!rare(A[0] == 0.f || A[1] == 0.f || A[2] == 0.f || A[3] == 0.f)) return;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    bool positive = A[e] == 0.f;
+#pragma unroll
+    for (int s = 0; s < TOK; ++s) positive = positive && g[s][e] != 0.f;
+    if (positive) A[e] = kTiny;
+  }
+}
+
 // Sweep 1 of the forward map: the wave's (A, B).  h0 receives the initial state
 // of the wave's last sequence start, which sweep 2 must not read again: in a
 // pool worked on in place, another wave may have written that sequence's final
@@ -548,6 +593,7 @@ __device__ __forceinline__ void forward_map(const RecArgs &a, const Marks<TOK> &
       A[e] *= gg;
     }
   });
+  if (PLAIN) keep_above_zero<TOK>(g, A);
 }
 
 // The state before token s, which starts a sequence.  Every start of the wave
@@ -675,6 +721,7 @@ __global__ void __launch_bounds__(kThreads, 4) rec_forward_kernel(RecArgs a) {
         B = resets >> w & 1 ? sB[w][tid] : fmaf(sA[w][tid], B, sB[w][tid]);
         A *= sA[w][tid];
       }
+      if (rare(A == 0.f) && A == 0.f && all_above_zero(sA, tid)) A = kTiny;
       if (a.ticket) {
         h = chain(a, tile, ch, -1, Map{A, B, resets != 0});
         reread_lds();
@@ -798,6 +845,7 @@ __global__ void __launch_bounds__(kThreads, 4) rec_backward_kernel(RecArgs a) {
         P[e] *= gg;
       }
     });
+    if (PL) keep_above_zero<TOK>(g, P);
     *reinterpret_cast<f32x4v *>(&sA[wave][4 * lane]) = f32x4v{P[0], P[1], P[2], P[3]};
     *reinterpret_cast<f32x4v *>(&sF[wave][4 * lane]) = f32x4v{F[0], F[1], F[2], F[3]};
     *reinterpret_cast<f32x4v *>(&sB[wave][4 * lane]) = f32x4v{B[0], B[1], B[2], B[3]};
@@ -814,6 +862,7 @@ __global__ void __launch_bounds__(kThreads, 4) rec_backward_kernel(RecArgs a) {
         B = lasts >> w & 1 ? sB[w][tid] : fmaf(sA[w][tid], B, sB[w][tid]);
         A *= sA[w][tid];
       }
+      if (rare(A == 0.f) && A == 0.f && all_above_zero(sA, tid)) A = kTiny;
       if (a.ticket) {
         k = chain(a, tile, ch, 1, Map{A, B, lasts != 0});
         reread_lds();

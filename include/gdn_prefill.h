@@ -303,7 +303,9 @@ int gdn_build_chunk_indices(const void *cu_seqlens, int32_t cu_type,
  *
  * from the given initial state (or zero).  g is the forget gate itself, in
  * [0, 1] (a gate above 1 is computed, but the products of 1 024 consecutive
- * gates of a sequence must stay finite).
+ * gates of a sequence must stay finite).  An infinite state stays infinite under
+ * gates above 0 and becomes NaN under a gate of 0, as the formula has it; states
+ * that would leave fp32's range only halfway may become infinite.
  *
  * Shapes: x, output, doutput, dx [T, H, D] in x_dtype (F32, BF16 or F16); g,
  * dg [T, H, D], or [T, H] with g_per_head (one gate for the D channels of a
