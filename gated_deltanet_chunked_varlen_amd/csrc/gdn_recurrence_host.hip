@@ -291,6 +291,53 @@ bool row_contiguous(const int64_t s[4], const int64_t ext[3]) {
          (ext[0] == 1 || s[1] == ext[1] * ext[2]);
 }
 
+// One dimension of two views: the distance in bytes from an index of the one to
+// the next, and the range of (source index - destination index).
+struct Steps {
+  int64_t bytes, lo, hi;
+};
+
+// Some element of the source view (ss bytes, the first at byte `at`) and some of
+// the destination view (ds bytes, the first at byte 0) share a byte.  The
+// dimensions go from the longest step to the shortest; as a view's elements do
+// not overlap, few differences come into question in each.
+bool meet(int64_t at, const Steps *d, int n, int64_t ss, int64_t ds) {
+  if (n == 0) return -ss < at && at < ds;
+  int64_t below = 0, above = 0;  // what the shorter steps can add
+  for (int k = 1; k < n; ++k) {
+    below += d[k].lo * d[k].bytes;
+    above += d[k].hi * d[k].bytes;
+  }
+  // -ss < at + i * bytes + (below .. above) < ds
+  const int64_t from = std::max(d->lo, (-ss - at - above) / d->bytes - 1);
+  const int64_t to = std::min(d->hi, (ds - at - below) / d->bytes + 1);
+  for (int64_t i = from; i <= to; ++i)
+    if (meet(at + i * d->bytes, d + 1, n - 1, ss, ds)) return true;
+  return false;
+}
+
+// The two views share no byte: their rows do not meet as whole stretches, or
+// where they are interleaved closer than that, their elements do not.  False
+// also where the views' steps differ, so that this is not settled.
+bool views_apart(int64_t at, const int64_t ss[4], int64_t srows, int64_t se, const int64_t ds[4],
+                 int64_t drows, int64_t de, const int64_t ext[3]) {
+  Steps d[4];
+  int n = 0;
+  auto dim = [&](int64_t s, int64_t sn, int64_t t, int64_t tn) {
+    s *= se;
+    t *= de;
+    if (sn > 1 && tn > 1 && s != t) return false;
+    if (sn > 1 || tn > 1) d[n++] = {sn > 1 ? s : t, 1 - tn, sn - 1};
+    return true;
+  };
+  if (!dim(ss[0], srows, ds[0], drows)) return false;
+  if (!meet(at, d, n, row_span(ss, ext, se), row_span(ds, ext, de))) return true;
+  for (int i = 0; i < 3; ++i)
+    if (!dim(ss[i + 1], ext[i], ds[i + 1], ext[i])) return false;
+  std::sort(d, d + n, [](const Steps &x, const Steps &y) { return x.bytes > y.bytes; });
+  return !meet(at, d, n, se, de);
+}
+
 struct PoolPlan {
   int64_t src_str[4], dst_str[4];
   bool same, flat;
@@ -319,12 +366,14 @@ int pool_plan(const gdn_pool_params *p, int mode, PoolPlan &L) {
   pool_strides(p->dst_strides, p->extent, L.dst_str);
   L.flat = row_contiguous(L.dst_str, p->extent);
   L.same = false;
-  auto width = [&](const void *base, const int64_t s[4], int64_t es) {
+  // (a pool of one row is never stepped over, whatever its row stride)
+  auto width = [&](const void *base, int64_t rows, const int64_t s[4], int64_t es) {
+    const int64_t step = rows > 1 ? s[0] * es : 0;
     int64_t w = 16;
-    while (w > 1 && ((uintptr_t)base % w || (s[0] * es) % w || (row * es) % w)) w /= 2;
+    while (w > 1 && ((uintptr_t)base % w || step % w || (row * es) % w)) w /= 2;
     return (int)w;
   };
-  L.align = width(p->dst, L.dst_str, ds);
+  L.align = width(p->dst, p->dst_pool_rows, L.dst_str, ds);
   if (mode != kCopy) {
     for (int i = 0; i < 4; ++i) L.src_str[i] = L.dst_str[i];
     return GDN_OK;
@@ -340,7 +389,7 @@ int pool_plan(const gdn_pool_params *p, int mode, PoolPlan &L) {
   if (!pool_strides_ok(p->src_strides, p->src_pool_rows, p->extent)) return GDN_ERR_STRIDES;
   pool_strides(p->src_strides, p->extent, L.src_str);
   L.flat = L.flat && row_contiguous(L.src_str, p->extent);
-  L.align = std::min(L.align, width(p->src, L.src_str, ss));
+  L.align = std::min(L.align, width(p->src, p->src_pool_rows, L.src_str, ss));
   // the same view, or no shared elements
   bool strides_equal = p->src_dtype == p->dst_dtype;
   for (int i = 0; i < 4; ++i) strides_equal = strides_equal && L.src_str[i] == L.dst_str[i];
@@ -350,15 +399,11 @@ int pool_plan(const gdn_pool_params *p, int mode, PoolPlan &L) {
     const int64_t sr = row_span(L.src_str, p->extent, ss), dr = row_span(L.dst_str, p->extent, ds);
     const uintptr_t s1 = s0 + (uintptr_t)((p->src_pool_rows - 1) * L.src_str[0] * ss + sr);
     const uintptr_t d1 = d0 + (uintptr_t)((p->dst_pool_rows - 1) * L.dst_str[0] * ds + dr);
-    if (s0 < d1 && d0 < s1) {
-      // interleaved rows of one buffer (the layers of a [rows, layers, ...]
-      // pool) are apart if they keep apart within one row distance
-      const int64_t step = L.dst_str[0] * ds;
-      if (step <= 0 || L.src_str[0] * ss != step) return GDN_ERR_STATE;
-      int64_t off = ((int64_t)(s0 - d0)) % step;
-      if (off < 0) off += step;
-      if (off < dr || off + sr > step) return GDN_ERR_STATE;
-    }
+    // interleaved views of one buffer (the layers of a [rows, layers, ...] pool)
+    if (s0 < d1 && d0 < s1 &&
+        !views_apart((int64_t)(s0 - d0), L.src_str, p->src_pool_rows, ss, L.dst_str,
+                     p->dst_pool_rows, ds, p->extent))
+      return GDN_ERR_STATE;
   }
   return GDN_OK;
 }

@@ -29,7 +29,8 @@ def state_pool_copy(pool, src_rows, dst_rows, src_pool=None, status=None):
     entries; it is meant for a few thousand (each is compared with all
     others).  ``status`` (optional int32 device
     tensor) receives the matching GDN_STATUS_POOL_* bits.  src_pool may be the
-    same view as pool, or share no elements with it.  Returns pool."""
+    same view as pool, or share no elements with it (views whose address
+    ranges cross need equal strides).  Returns pool."""
     return calls().pool_copy(pool, src_rows, dst_rows, src_pool, status)
 
 

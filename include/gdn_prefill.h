@@ -436,8 +436,9 @@ int gdn_validate_pool_host(const gdn_pool_params *p, int32_t mode);
  * several destinations), moving rows, or bringing rows of another pool or a
  * checkpoint buffer in, with conversion between state dtypes (to nearest; the
  * 8-bit types saturate; equal types copy bit for bit).  src and dst may be
- * the same view; other views may share no elements (GDN_ERR_STATE where the
- * host can see that they do).  A destination named twice takes its last
+ * the same view; other views may share no elements (GDN_ERR_STATE where they
+ * do; and where their address ranges cross with different strides, so that the
+ * host does not settle it).  A destination named twice takes its last
  * entry.  In one pool an entry whose source row is another entry's destination
  * is skipped, unless that one copies the row onto itself (it changes nothing, so
  * a row can be kept and forked in one list).  Both set their status bit.  At most GDN_POOL_MAX_ROWS entries

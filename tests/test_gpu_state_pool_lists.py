@@ -79,3 +79,43 @@ def test_compact_moves_all_pools_or_none():
     ren, n = state_pool_compact([first, want.clone()], _rows([11, 7]), output_indices=out)
     assert ren.tolist() == [1, 0] and n.item() == 2
     assert first[:2, 0].tolist() == [7, 11]
+
+
+@pytest.mark.parametrize("row", [(4, 128, 128), (16, 128), (5, 7), (1,), (2, 4100)])
+@pytest.mark.parametrize("frm,to", [(torch.bfloat16, torch.float32), (torch.float32, torch.float32),
+                                    (torch.float32, torch.bfloat16),
+                                    (torch.bfloat16, torch.bfloat16)])
+def test_pools_of_one_row(row, frm, to):
+    """One checkpoint forked into a pool, and a row brought into a pool of one,
+    at aligned and unaligned places."""
+    gen = torch.Generator().manual_seed(1)
+    n = 1
+    for e in row:
+        n *= e
+    for off in (0, 1):
+        store = torch.randn(n + off, generator=gen).to(frm).cuda()
+        one = store[off:].view((1,) + row)
+        pool = torch.randn((6,) + row, generator=gen).to(to).cuda()
+        want = pool.clone()
+        want[[1, 4]] = one[0].to(to)
+        state_pool_copy(pool, _rows([0, 0]), _rows([4, 1]), src_pool=one)
+        assert torch.equal(pool, want)
+        back = torch.full((n + off,), 3.0, device="cuda").to(frm)
+        state_pool_copy(back[off:].view((1,) + row), _rows([5]), _rows([0]), src_pool=pool)
+        assert torch.equal(back[off:].view(row), pool[5].to(frm)) and (back[:off] == 3).all()
+
+
+def test_one_row_of_a_layer_and_all_rows_of_another():
+    big = torch.randn((6, 3, 2, 32), device="cuda")
+    ref = big.clone()
+    state_pool_copy(big[:, 1], _rows([0, 0]), _rows([5, 2]), src_pool=big[4:5, 0])
+    ref[[5, 2], 1] = ref[4, 0]
+    assert torch.equal(big, ref)
+    state_pool_copy(big[3:4, 2], _rows([5]), _rows([0]), src_pool=big[:, 1])
+    ref[3, 2] = ref[5, 1]
+    assert torch.equal(big, ref)
+    state_pool_copy(big[:, :, :, :16], _rows([1]), _rows([0]), src_pool=big[:, :, :, 16:])
+    ref[0, :, :, :16] = ref[1, :, :, 16:]
+    assert torch.equal(big, ref)
+    with pytest.raises(ValueError):
+        state_pool_copy(big[:, 1], _rows([0]), _rows([5]), src_pool=big[4:5, 1])
