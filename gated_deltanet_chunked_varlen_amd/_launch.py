@@ -6,6 +6,8 @@ Both are built together; without either the calls raise ImportError.
 from __future__ import annotations
 
 import ctypes
+import threading
+from collections import OrderedDict
 
 import torch
 
@@ -13,6 +15,8 @@ from . import _native as nat
 from . import api
 
 _bound = None
+_ws_cache: "OrderedDict[tuple, torch.Tensor]" = OrderedDict()
+_ws_lock = threading.RLock()
 
 
 def _stream(index):
@@ -21,19 +25,23 @@ def _stream(index):
 
 def _workspace(index, stream, need):
     """Workspace of a call on ``stream``, the current one of the current device
-    ``index``: kept per stream (in the prefill's cache, but apart from its
-    memory), or under capture from the graph's own pool (a graph keeps the
-    address)."""
+    ``index``: kept per stream, or under capture from the graph's own pool (a
+    graph keeps the address).  The prefill's workspaces and their number are
+    apart; of either kind those least recently used go first."""
     if torch.cuda.is_current_stream_capturing():
-        return torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", index))
-    key = ("cuda", index, stream, "recurrence")
-    ws = api._ws_cache.get(key)
-    if ws is None or ws.numel() < need:
-        ws = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", index))
-        api._ws_cache[key] = ws
-        while len(api._ws_cache) > api._WS_CACHE_MAX:
-            api._ws_cache.popitem(last=False)
+        return _memory(index, need)
+    with _ws_lock:
+        ws = _ws_cache.pop((index, stream), None)
+        if ws is None or ws.numel() < need:
+            ws = _memory(index, need)
+        _ws_cache[index, stream] = ws
+        while len(_ws_cache) > api._WS_CACHE_MAX:
+            _ws_cache.popitem(last=False)
     return ws
+
+
+def _memory(index, need):
+    return torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", index))
 
 
 def calls():

@@ -260,7 +260,11 @@ def cached_workspace(device, stream: int, need: int) -> torch.Tensor:
 
 
 def clear_workspace_cache() -> None:
+    """Frees the workspaces kept per stream, the recurrence's too."""
+    from . import _launch
     _ws_cache.clear()
+    with _launch._ws_lock:
+        _launch._ws_cache.clear()
 
 
 def workspace_size(p: nat.Params) -> int:
