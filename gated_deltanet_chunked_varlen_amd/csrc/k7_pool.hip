@@ -395,18 +395,19 @@ __global__ void __launch_bounds__(kThreads) pool_compact_kernel(PoolArgs a, Unit
     return k >= 32 ? ~0u : k <= 0 ? 0u : (1u << k) - 1u;
   };
   if (nwords <= 64) {
-    // up to 2 048 rows: every wave forms the whole plan, a word per lane, and
-    // writes it for itself (the waves write the same values): no barriers
+    // up to 2 048 rows: every wave forms the whole plan, a word per lane, and the
+    // first one writes it: one barrier
     const int w = tid & 63;
     const unsigned live = w < nwords ? map[w] : 0u;
     m = __builtin_amdgcn_readlane(wave_prefix_sum_i(__popc(live)), 63);
     const int both = __popc(live & ~before(w)) | (w < nwords ? __popc(~live & before(w)) << 16 : 0);
     const int inc = wave_prefix_sum_i(both);
     moves = __builtin_amdgcn_readlane(inc, 63) & 0xFFFF;
-    if (w < nwords) {
+    if (tid < nwords) {
       movers[w] = (inc - both) & 0xFFFF;
       holes[w] = (inc - both) >> 16;
     }
+    __syncthreads();
   } else {
     // a thread owns `per` consecutive words
     const int per = (nwords + kThreads - 1) / kThreads;
