@@ -23,6 +23,16 @@ import torch
 
 from . import _native as nat
 
+try:
+    # tells autograd that a call has written its buffers, as torch's in-place
+    # operators do: a graph that saved one of them (a differentiable
+    # ``gated_linear_recurrence`` from pool rows, or on a reused output buffer)
+    # then raises instead of using what is there now
+    from ._calls import advance_versions as _advance_versions
+except ImportError:  # not built (0.6 us a call from Python instead of 0.1)
+    def _advance_versions(*tensors):
+        torch.autograd.graph.increment_version([t for t in tensors if t is not None])
+
 _QKV_DTYPES = {torch.float32: nat.GDN_F32, torch.bfloat16: nat.GDN_BF16,
                torch.float16: nat.GDN_F16}
 _STATE_DTYPES = {torch.float32: nat.GDN_F32, torch.bfloat16: nat.GDN_BF16,
@@ -317,6 +327,8 @@ def chunk_gated_delta_rule(q, k, v, g=None, beta=None, scale=None,
         rc = lib.gdn_prefill(ctypes.byref(p), ctypes.c_void_p(stream))
     if rc != 0:
         _raise(rc)
+    _advance_versions(output, output_state if output_final_state else None, state_checkpoints,
+                      status)
     if output_final_state:
         return output, output_state
     return output
@@ -353,6 +365,8 @@ def chunk_gated_delta_rule_noalloc(q, k, v, g=None, beta=None, scale=None,
         rc = lib.gdn_prefill_noalloc(ctypes.byref(p), ctypes.c_void_p(stream))
     if rc != 0:
         _raise(rc)
+    _advance_versions(output, output_state if output_final_state else None, state_checkpoints,
+                      status)
     if output_final_state:
         return output, output_state
     return output
@@ -377,6 +391,7 @@ def gated_delta_rule_decode(q, k, v, g=None, beta=None, scale=None,
         rc = lib.gdn_decode(ctypes.byref(p), ctypes.c_void_p(stream))
     if rc != 0:
         _raise(rc)
+    _advance_versions(output, output_state if output_final_state else None, status)
     if output_final_state:
         return output, output_state
     return output
@@ -482,4 +497,8 @@ class PrefillGraphs:
         self._graphs.move_to_end(key)
         graph, res, _ = hit
         graph.replay()
+        # (output is given by name, so everything behind it is too)
+        _advance_versions(kwargs["output"],
+                          kwargs.get("output_state") if kwargs.get("output_final_state") else None,
+                          kwargs.get("state_checkpoints"), kwargs.get("status"))
         return res

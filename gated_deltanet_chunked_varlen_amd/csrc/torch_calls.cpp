@@ -149,8 +149,10 @@ struct Writes {
     if (t) add(name, *t);
   }
   void done() const {
-    for (const Tensor *t : all)  // (an inference tensor has no version)
-      if (!t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+    for (const Tensor *t : all) advance(*t);
+  }
+  static void advance(const Tensor &t) {  // (an inference tensor has no version)
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
   }
 };
 
@@ -599,6 +601,15 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// advance_versions(tensors or None ...): what other calls have written.
+PyObject *advance_versions(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  for (Py_ssize_t i = 0; i < n; ++i)
+    if (a[i] != Py_None) Writes::advance(tensor("a written buffer", a[i]));
+  Py_RETURN_NONE;
+  END_HANDLE_TH_ERRORS
+}
+
 // bind(eight addresses, raise, stream, workspace)
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
   constexpr int kEntries = 8;
@@ -632,6 +643,7 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
 #define CALL(name, f, n) {name, (PyCFunction)(void (*)(void))entry<f, n>, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {
     {"bind", (PyCFunction)(void (*)(void))bind, METH_FASTCALL, nullptr},
+    {"advance_versions", (PyCFunction)(void (*)(void))advance_versions, METH_FASTCALL, nullptr},
     CALL("rec_forward", rec_forward, 11),
     CALL("rec_backward", rec_backward, 13),
     CALL("rec_decode", rec_decode, 8),

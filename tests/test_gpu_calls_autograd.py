@@ -6,7 +6,8 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from gated_deltanet_chunked_varlen_amd import (  # noqa: E402
-    gated_linear_recurrence, gated_linear_recurrence_backward, gated_linear_recurrence_decode,
+    PrefillGraphs, chunk_gated_delta_rule, chunk_gated_delta_rule_noalloc,
+    gated_delta_rule_decode, gated_linear_recurrence, gated_linear_recurrence_backward, gated_linear_recurrence_decode,
     state_pool_compact, state_pool_copy, state_pool_reset)
 from tests import recurrence_testlib as R  # noqa: E402
 
@@ -192,3 +193,40 @@ def test_flags_without_a_truth_value():
         gated_linear_recurrence_decode(d["x"], d["g"], output=out, output_final_state=both)
     torch.cuda.synchronize()
     assert (out == 7).all()
+
+
+@pytest.mark.parametrize("name", ["prefill", "noalloc", "graphs", "decode"])
+def test_writes_of_the_delta_rule_are_seen_by_the_graph(name):
+    """Its output buffer is the recurrence's x, its pool holds the recurrence's
+    initial states too: written again before the backward pass, both raise."""
+    H, D = 2, 32
+    gen = torch.Generator(device="cuda").manual_seed(87)
+    rand = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    T = 3 if name == "decode" else 20
+    q, k, v = rand(T, H, D), rand(T, H, D), rand(T, H, D)
+    buf, pool = torch.zeros((T, H, D), device="cuda"), rand(4, H, D, D)
+    rows = _rows(0, 3, 1) if name == "decode" else _rows(2)
+    st = _rows(0)
+    call = {"prefill": chunk_gated_delta_rule, "noalloc": chunk_gated_delta_rule_noalloc,
+            "graphs": PrefillGraphs(), "decode": gated_delta_rule_decode}[name]
+
+    def step():
+        call(q, k, v, initial_state=pool, output_final_state=True, output=buf, output_state=pool,
+             state_indices=rows, use_qk_l2norm_in_kernel=True, status=st)
+
+    step()
+    gate = torch.rand((T, H, D), generator=gen, device="cuda").requires_grad_()
+    start = pool.view(4 * D, H, D)[:1]
+    for kw in (dict(), dict(initial_state=start)):
+        x = buf if not kw else rand(T, H, D)
+        gated_linear_recurrence(x, gate, **kw).sum().backward()
+        out = gated_linear_recurrence(x, gate, **kw)
+        versions = buf._version, pool._version, st._version
+        step()
+        assert all(a > b for a, b in zip((buf._version, pool._version, st._version), versions))
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            out.sum().backward()
+    assert q._version == 0
+    with torch.inference_mode():
+        o = chunk_gated_delta_rule(q, k, v)
+    assert o.is_inference()
