@@ -13,6 +13,15 @@ from ._launch import calls
 from .api import _QKV_DTYPES
 
 
+def _capturing(t):
+    """Whether the current stream of a device tensor's own device is being
+    captured (another device may be the current one)."""
+    if not t.is_cuda:
+        return False
+    with torch.cuda.device(t.device):
+        return torch.cuda.is_current_stream_capturing()
+
+
 class _Recurrence(torch.autograd.Function):
     """The forward call with its gradient; the arguments are the tensors that
     take one, then cu_seqlens and whether the final state is returned."""
@@ -28,10 +37,10 @@ class _Recurrence(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dout, dfinal=None):
-        if torch.cuda.is_current_stream_capturing():
+        x, g, initial_state, cu_seqlens, kept = ctx.saved_tensors
+        if _capturing(x):
             raise RuntimeError("autograd through gated_linear_recurrence cannot be captured into "
                                "a graph; capture gated_linear_recurrence_backward instead")
-        x, g, initial_state, cu_seqlens, kept = ctx.saved_tensors
         want0 = initial_state is not None and ctx.needs_input_grad[2]
         dout = torch.zeros_like(x, memory_format=torch.contiguous_format) if dout is None \
             else dout.contiguous()
@@ -90,7 +99,7 @@ def gated_linear_recurrence(x, g, initial_state=None, output_final_state=False, 
         if initial_state is not None and initial_state.dtype not in _QKV_DTYPES:
             raise ValueError("a differentiable call's initial_state must be float32, bfloat16 "
                              "or float16")
-        if torch.cuda.is_available() and torch.cuda.is_current_stream_capturing():
+        if isinstance(x, torch.Tensor) and _capturing(x):
             raise RuntimeError("a differentiable gated_linear_recurrence cannot be captured into "
                                "a graph; use torch.no_grad() and "
                                "gated_linear_recurrence_backward")
