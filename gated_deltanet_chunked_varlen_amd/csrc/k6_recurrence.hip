@@ -645,8 +645,8 @@ __device__ __forceinline__ void segments_down(const Marks<TOK> &m, F f) {
 
 // Tokens per wave: 16 for 16-bit x with head gates, which take few registers,
 // else 8.  Twice the bytes per workgroup halve the chain's traffic and its share
-// of a tile's time (23 060 tokens x 4096 channels, fp16 with head gates: 104 ->
-// 82.5 us).  16-bit gates per channel gain nothing (2 x 2048 x 2048: 17.9 and
+// of a tile's time (23 060 tokens x 4096 channels, fp16 with head gates: 104 us
+// with 8, 87 with 16).  16-bit gates per channel gain nothing (2 x 2048 x 2048: 17.9 and
 // 18.9 us); with fp32 gates or fp32 x 16 tokens would leave one workgroup per CU
 // instead of two, and they did not fit the backward pass's registers at all.
 template <typename T> constexpr int code() {
@@ -658,11 +658,13 @@ template <typename Tx, bool PH> constexpr int forward_tokens() {
 
 // Bounded by HBM: per element x and g are read once and out written once; the
 // chain adds 8 bytes per tile and channel each for clearing, publishing and
-// looking back.  65 536 tokens x 4096 channels, bf16 with fp32 gates: 388 us,
-// 5.5 TB/s (a plain copy runs at 4.7 to 5.4 TB/s on the same card), 370 us with
-// every wait of the chain taken out.  2 x 2048 tokens x 2048 channels: 18 us,
-// 16 without the waits; it is one round of workgroups, whose loads and stores
-// hardly overlap.  Two workgroups per CU (128 registers) are what keeps enough
+// looking back.  65 536 tokens x 4096 channels, bf16 with fp32 gates: 394 us,
+// 5.5 TB/s (a plain copy runs at 4.7 to 5.4 TB/s on the same card).  2 x 2048
+// tokens x 2048 channels: 19 us; it is one round of workgroups, whose loads and
+// stores hardly overlap.  515 x 2048 in fp32: 10 us; the code is 60 KB, and what
+// a short call runs of it comes into the instruction cache first (2.5 KB more for
+// the infinities' sake cost 0.4 us, so that what is rare lies out of the way and
+// only plain waves have it).  Two workgroups per CU (128 registers) are what keeps enough
 // bytes on their way: with one, the long pass took 666 us.
 template <typename Tx, typename Tg, bool PH, bool VEC>
 __global__ void __launch_bounds__(kThreads, 4) rec_forward_kernel(RecArgs a) {
@@ -777,10 +779,10 @@ __device__ __forceinline__ float head_sum(float x, int D) {
 // One pass over x, g and dy: the states before each token are formed again
 // from the tile's saved start state, in fp32, while the carry of the gradient
 // comes through the chain from the tiles behind.  2 x 2048 tokens x 2048
-// channels, bf16 with fp32 gates: 26 us, 4.5 TB/s (23 without the chain's
-// waits).  23 060 x 4096, fp16 with head gates: 150 us, 3.8 TB/s; there the
-// vector units are busy a third of the time and a tile's 14 us are split
-// between its loads, some 700 vector instructions per wave and the chain.
+// channels, bf16 with fp32 gates: 26 us, 4.5 TB/s.  23 060 x 4096, fp16 with
+// head gates: 155 us, 3.7 TB/s; there the vector units are busy a third of the
+// time and a tile's 14 us are split between its loads, some 700 vector
+// instructions per wave and the chain.
 template <typename Tx, typename Tg, bool PH, bool VEC>
 __global__ void __launch_bounds__(kThreads, 4) rec_backward_kernel(RecArgs a) {
   constexpr int TOK = 8;
@@ -962,8 +964,8 @@ __global__ void __launch_bounds__(kThreads, 4) rec_backward_kernel(RecArgs a) {
 
 // One thread per four channels of one sequence: the state row is read,
 // updated and written back.  Bounded by launch latency below a few hundred
-// sequences (6 x 2048 channels: 3.1 us), by memory above (256 x 4096 channels
-// with fp32 states, 17 MB: 4.4 us).
+// sequences (6 x 2048 channels: 3.0 us), by memory above (256 x 4096 channels
+// with fp32 states, 17 MB: 4.8 us).
 template <typename Tx, typename Tg, bool PH, bool VEC>
 __global__ void __launch_bounds__(256) rec_decode_kernel(RecArgs a) {
   if (blockIdx.x == 0 && a.status) {
