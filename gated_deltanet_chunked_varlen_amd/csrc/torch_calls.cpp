@@ -173,6 +173,7 @@ bool expanded(const Tensor &t) {
 // Distance in elements of the first dimension's entries, each of which holds
 // `inner` contiguous values.
 int64_t row_stride(const char *name, const Tensor &t, int64_t inner) {
+  if (t.numel() == 0) return inner;  // (contiguous() keeps an empty tensor's strides)
   int64_t want = 1;
   for (int64_t i = t.dim() - 1; i > 0; --i) {
     BAD_IF(t.size(i) > 1 && t.stride(i) != want, name,

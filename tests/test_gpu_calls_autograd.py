@@ -230,3 +230,22 @@ def test_writes_of_the_delta_rule_are_seen_by_the_graph(name):
     with torch.inference_mode():
         o = chunk_gated_delta_rule(q, k, v)
     assert o.is_inference()
+
+
+def test_autograd_without_tokens_or_sequences():
+    """The incoming gradients of sums are expanded, and an empty tensor stays so
+    when it is made contiguous."""
+    x = torch.zeros((0, 2, 32), device="cuda", requires_grad=True)
+    g = torch.zeros((0, 2, 32), device="cuda")
+    h0 = torch.randn((3, 2, 32), device="cuda", requires_grad=True)
+    out, fin = gated_linear_recurrence(x, g, initial_state=h0, output_final_state=True,
+                                       cu_seqlens=_rows(0, 0, 0, 0))
+    (out.sum() + 2 * fin.sum()).backward()
+    assert (h0.grad == 2).all() and x.grad.shape == x.shape
+    x = torch.randn((5, 2, 32), device="cuda", requires_grad=True)
+    h0 = torch.zeros((1, 2, 1), device="cuda", requires_grad=True)
+    out, fin = gated_linear_recurrence(x, x.detach().sigmoid(), cu_seqlens=_rows(0),
+                                       initial_state=h0.expand(1, 2, 32)[:0],
+                                       output_final_state=True)
+    fin.sum().backward()
+    assert (x.grad == 0).all() and (h0.grad == 0).all() and fin.shape == (0, 2, 32)
