@@ -488,14 +488,14 @@ template <typename Tg, bool VEC> struct Gate<Tg, true, VEC> {
 template <int TOK> struct Marks {
   unsigned first, last;
   int lo, hi;
-  int id_first, id_last;  // lane s: sequence that starts / ends at token s
+  const int *start, *end;  // of the wave's tokens, in LDS
 
   __device__ __forceinline__ void read(TileGeo<TOK> &G, int t0, int wave, int lane) {
     const int base = wave * TOK;
-    id_first = G.start[base + (lane & (TOK - 1))];
-    id_last = G.end[base + (lane & (TOK - 1))];
-    first = (unsigned)__ballot(id_first >= 0) & ((1u << TOK) - 1);
-    last = (unsigned)__ballot(id_last >= 0) & ((1u << TOK) - 1);
+    start = G.start + base;
+    end = G.end + base;
+    first = (unsigned)__ballot(start[lane & (TOK - 1)] >= 0) & ((1u << TOK) - 1);
+    last = (unsigned)__ballot(end[lane & (TOK - 1)] >= 0) & ((1u << TOK) - 1);
     lo = __builtin_amdgcn_readfirstlane(min(max(G.lo - t0 - base, 0), TOK));
     hi = __builtin_amdgcn_readfirstlane(min(max(G.hi - t0 - base, 0), TOK));
     if (lane == 0) {
@@ -509,12 +509,15 @@ template <int TOK> struct Marks {
   }
   // the wave's last token that starts a sequence
   __device__ __forceinline__ int last_first() const { return 31 - __builtin_clz(first); }
-  // sequence that starts / ends at this wave's token s
+  // sequence that starts / ends at this wave's token s.  Read from LDS, the same
+  // for all lanes, where it is needed: kept one per lane it would have to be read
+  // from lanes that have no channels, and a register that the compiler puts aside
+  // is brought back for the lanes that do.
   __device__ __forceinline__ int seq_first(int s) const {
-    return __builtin_amdgcn_readlane(id_first, s);
+    return __builtin_amdgcn_readfirstlane(start[s]);
   }
   __device__ __forceinline__ int seq_last(int s) const {
-    return __builtin_amdgcn_readlane(id_last, s);
+    return __builtin_amdgcn_readfirstlane(end[s]);
   }
 };
 
