@@ -179,13 +179,9 @@ __device__ __forceinline__ unsigned long long peek(const unsigned long long *w) 
 // it guards is a scalar branch to code that lies out of the way.
 __device__ __forceinline__ bool rare(bool b) { return __builtin_expect(__ballot(b) != 0, 0); }
 
-// The product of two runs' gates.  It is 0 only if a gate is.  (Elsewhere several
-// runs' products are multiplied plainly, and a 0 is looked into afterwards.)
+// What a product of gates is kept at where it underflows.  Products are formed
+// plainly, and a 0 is looked into afterwards: no gate is 0 if no factor is.
 constexpr float kTiny = 0x1p-149f;
-__device__ __forceinline__ float gates_product(float A, float B) {
-  const float p = A * B;
-  return p == 0.f && A != 0.f && B != 0.f ? kTiny : p;
-}
 
 __device__ __forceinline__ unsigned mark(unsigned long long w) { return (unsigned)(w >> 32); }
 __device__ __forceinline__ float low(unsigned long long w) { return __uint_as_float((unsigned)w); }
@@ -258,6 +254,7 @@ __device__ __forceinline__ float chain(const RecArgs &a, int tile, unsigned c, i
   // the tiles before this one in its group, nearest first up to a known state
   const int before = n % kGroup;
   Map m = {1.f, 0.f, false};
+  float A = own.A;  // of the tiles before and this one
   if (before > 0) {
     unsigned long long w[kGroup - 1];
     bool open;
@@ -278,18 +275,20 @@ __device__ __forceinline__ float chain(const RecArgs &a, int tile, unsigned c, i
         if (mark(w[j]) == kLast) {
           m = {0.f, low(w[j]), true};
         } else {
-          const float A = __uint_as_float(mark(w[j]));
-          m.B = fmaf(A, m.B, low(w[j]));
-          m.A *= A;
+          const float Aj = __uint_as_float(mark(w[j]));
+          m.B = fmaf(Aj, m.B, low(w[j]));
+          m.A *= Aj;
         }
       }
     }
-    if (rare(m.A == 0.f && !m.known)) {
+    A *= m.A;
+    if (rare(A == 0.f && !m.known)) {
       bool positive = true;
 #pragma unroll
       for (int j = 0; j < kGroup - 1; ++j)
         if (j < before) positive = positive && __uint_as_float(mark(w[j])) != 0.f;
       if (m.A == 0.f && positive) m.A = kTiny;
+      if (A == 0.f && m.A != 0.f && own.A != 0.f) A = kTiny;
     }
     if (!open) m = {0.f, __uint_as_float(kNaN), true};  // given up
   }
@@ -297,7 +296,7 @@ __device__ __forceinline__ float chain(const RecArgs &a, int tile, unsigned c, i
   unsigned long long *gword = a.groups + (int64_t)group * a.C + c;
   const bool closes = before == kGroup - 1;
   if (group == 0) m.known = true;  // nothing before: the state is zero
-  Map all = {gates_product(m.A, own.A), fmaf(own.A, m.B, own.B), m.known};
+  Map all = {A, fmaf(own.A, m.B, own.B), m.known};
   if (own.known) all = own;
   if (closes) publish(gword, all.known ? kLast : map_bits(all.A), all.B);
   if (m.known) return m.B;
@@ -557,7 +556,7 @@ __device__ __forceinline__ void by_marks(const Marks<TOK> &m, F f) {
 // is replaced or belongs to no token.
 template <int TOK, typename GateT>
 __device__ __forceinline__ void keep_above_zero(const GateT (&g)[TOK], float (&A)[4]) {
-  if (!rare(A[0] == 0.f || A[1] == 0.f || A[2] == 0.f || A[3] == 0.f)) return;
+  if (!rare(fminf(fminf(fabsf(A[0]), fabsf(A[1])), fminf(fabsf(A[2]), fabsf(A[3]))) == 0.f)) return;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     bool positive = A[e] == 0.f;
