@@ -128,6 +128,7 @@ int index_type(const char *name, const Tensor &t) {
 // requires a gradient while gradients are recorded, or a dual tensor of forward
 // mode.
 void no_derivative(const char *name, const Tensor &t) {
+  if (!t.unsafeGetTensorImpl()->autograd_meta()) return;  // neither, as for most tensors
   BAD_IF(c10::GradMode::is_enabled() && t.requires_grad(), name,
          " requires a gradient, but this call is not differentiable; use torch.no_grad()");
   BAD_IF(c10::AutogradState::get_tls_state().get_fw_grad_mode() && t._fw_grad(0).defined(), name,
