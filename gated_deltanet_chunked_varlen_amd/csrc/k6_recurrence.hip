@@ -175,8 +175,8 @@ __device__ __forceinline__ void publish(unsigned long long *w, unsigned hi, floa
 __device__ __forceinline__ unsigned long long peek(const unsigned long long *w) {
   return __hip_atomic_load(w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-// True for some lane, which is unusual: the same for the whole wave, so that what
-// it guards is a scalar branch to code that lies out of the way.
+// True for some lane, which is unusual: the same for the whole wave, so that it is
+// a scalar branch.
 __device__ __forceinline__ bool rare(bool b) { return __builtin_expect(__ballot(b) != 0, 0); }
 
 // What a product of gates is kept at where it underflows.  Products are formed
@@ -660,13 +660,13 @@ template <typename Tx, bool PH> constexpr int forward_tokens() {
 
 // Bounded by HBM: per element x and g are read once and out written once; the
 // chain adds 8 bytes per tile and channel each for clearing, publishing and
-// looking back.  65 536 tokens x 4096 channels, bf16 with fp32 gates: 394 us,
+// looking back.  65 536 tokens x 4096 channels, bf16 with fp32 gates: 393 us,
 // 5.5 TB/s (a plain copy runs at 4.7 to 5.4 TB/s on the same card).  2 x 2048
 // tokens x 2048 channels: 19 us; it is one round of workgroups, whose loads and
-// stores hardly overlap.  515 x 2048 in fp32: 10 us; the code is 60 KB, and what
+// stores hardly overlap.  515 x 2048 in fp32: 10.3 us; the code is 60 KB, and what
 // a short call runs of it comes into the instruction cache first (2.5 KB more for
-// the infinities' sake cost 0.4 us, so that what is rare lies out of the way and
-// only plain waves have it).  Two workgroups per CU (128 registers) are what keeps enough
+// the infinities' sake cost 0.4 us, a form for plain waves alone half of that).
+// Two workgroups per CU (128 registers) are what keeps enough
 // bytes on their way: with one, the long pass took 666 us.
 template <typename Tx, typename Tg, bool PH, bool VEC>
 __global__ void __launch_bounds__(kThreads, 4) rec_forward_kernel(RecArgs a) {
@@ -782,7 +782,7 @@ __device__ __forceinline__ float head_sum(float x, int D) {
 // from the tile's saved start state, in fp32, while the carry of the gradient
 // comes through the chain from the tiles behind.  2 x 2048 tokens x 2048
 // channels, bf16 with fp32 gates: 26 us, 4.5 TB/s.  23 060 x 4096, fp16 with
-// head gates: 155 us, 3.7 TB/s; there the vector units are busy a third of the
+// head gates: 154 us, 3.7 TB/s; there the vector units are busy a third of the
 // time and a tile's 14 us are split between its loads, some 700 vector
 // instructions per wave and the chain.
 template <typename Tx, typename Tg, bool PH, bool VEC>
@@ -967,7 +967,7 @@ __global__ void __launch_bounds__(kThreads, 4) rec_backward_kernel(RecArgs a) {
 // One thread per four channels of one sequence: the state row is read,
 // updated and written back.  Bounded by launch latency below a few hundred
 // sequences (6 x 2048 channels: 3.0 us), by memory above (256 x 4096 channels
-// with fp32 states, 17 MB: 4.8 us).
+// with fp32 states, 17 MB: 4.4 to 5 us).
 template <typename Tx, typename Tg, bool PH, bool VEC>
 __global__ void __launch_bounds__(256) rec_decode_kernel(RecArgs a) {
   if (blockIdx.x == 0 && a.status) {

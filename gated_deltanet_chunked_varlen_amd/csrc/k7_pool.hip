@@ -13,9 +13,9 @@
 // (4-byte words from L2, less than the rows); a copy's time grows with the
 // square of its list, which is why it takes at most GDN_POOL_MAX_ROWS entries.
 //
-// Measured: four 1 MB rows into 32 (38 MB): 9.4 us, 3 of them a launch's least;
+// Measured: four 1 MB rows into 32 (38 MB): 10 us, 3 of them a launch's least;
 // 96 rows from bf16 to fp32 (302 MB): 66 us, 4.6 TB/s; 64 rows of 1 MB zeroed:
-// 11.3 us, 5.9 TB/s; 64 rows of 512 KB moved by a compaction (67 MB): 15.3 us;
+// 11.8 us, 5.7 TB/s; 64 rows of 512 KB moved by a compaction (67 MB): 15 us;
 // one row of 1 MB from bf16 to 2 MB of fp32: 5.9 us a call.
 // Units of 32 and 128 KB and two to four times the loads in flight were no
 // faster (38 MB fork: 10.6 and 16.2 us with 32 and 128 KB units).
