@@ -1,5 +1,5 @@
-"""The compiled marshalling of the recurrence and state-pool calls (``_calls``,
-from csrc/torch_calls.cpp), bound to the loaded library.
+"""The compiled marshalling of the recurrence, layer, beam and state-pool calls
+(``_calls``, from csrc/torch_calls.cpp and torch_layer_calls.cpp), bound to the loaded library.
 
 Both are built together; without either the calls raise ImportError.
 """
@@ -57,7 +57,11 @@ def calls():
         address = [ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
             "gdn_recurrence_workspace_size", "gdn_recurrence", "gdn_recurrence_backward",
             "gdn_recurrence_decode", "gdn_pool_copy", "gdn_pool_reset", "gdn_pool_compact",
-            "gdn_validate_pool_host")]
+            "gdn_validate_pool_host",
+            "gdn_convolution_workspace_size", "gdn_convolution", "gdn_convolution_backward",
+            "gdn_convolution_decode", "gdn_scan_chunk", "gdn_scan_workspace_size", "gdn_scan",
+            "gdn_scan_backward", "gdn_scan_decode", "gdn_beam_workspace_size", "gdn_beam_select",
+            "gdn_pool_reorder")]
         # torch's own accessor of the raw handle where it has one: a tenth of the time
         stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream)
         _calls.bind(*address, api._raise, stream, _workspace)

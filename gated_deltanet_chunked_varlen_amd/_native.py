@@ -36,6 +36,7 @@ STATUS_POOL_DUPLICATE = 32
 STATUS_POOL_OVERLAP = 64
 RECURRENCE_CHUNK = 64
 POOL_MAX_ROWS = 262144
+BEAM_MAX = 64
 
 # every symbol include/gdn_prefill.h declares
 EXPORTS = [
@@ -46,6 +47,12 @@ EXPORTS = [
     "gdn_recurrence_workspace_size", "gdn_validate_recurrence_host", "gdn_recurrence",
     "gdn_recurrence_backward", "gdn_recurrence_decode", "gdn_validate_pool_host",
     "gdn_pool_copy", "gdn_pool_reset", "gdn_pool_compact",
+    "gdn_convolution_workspace_size", "gdn_validate_convolution_host", "gdn_convolution",
+    "gdn_convolution_backward", "gdn_convolution_decode",
+    "gdn_scan_chunk", "gdn_scan_workspace_size", "gdn_validate_scan_host", "gdn_scan",
+    "gdn_scan_backward", "gdn_scan_decode",
+    "gdn_beam_workspace_size", "gdn_validate_beam_host", "gdn_beam_select",
+    "gdn_validate_reorder_host", "gdn_pool_reorder",
 ]
 
 _i64x4 = ctypes.c_int64 * 4
@@ -157,6 +164,140 @@ class PoolParams(ctypes.Structure):
     ]
 
 
+class ConvolutionParams(ctypes.Structure):
+    _fields_ = [
+        ("total_tokens", ctypes.c_int64),
+        ("num_seqs", ctypes.c_int32),
+        ("channels", ctypes.c_int32),
+        ("width", ctypes.c_int32),
+        ("x_dtype", ctypes.c_int32),
+        ("weight_dtype", ctypes.c_int32),
+        ("silu", ctypes.c_int32),
+        ("x", ctypes.c_void_p),
+        ("x_stride", ctypes.c_int64),
+        ("weight", ctypes.c_void_p),
+        ("bias", ctypes.c_void_p),
+        ("cu_seqlens", ctypes.c_void_p),
+        ("cu_seqlens_type", ctypes.c_int32),
+        ("output", ctypes.c_void_p),
+        ("initial_state", ctypes.c_void_p),
+        ("initial_state_dtype", ctypes.c_int32),
+        ("initial_state_stride", ctypes.c_int64),
+        ("output_final_state", ctypes.c_int32),
+        ("output_state", ctypes.c_void_p),
+        ("output_state_dtype", ctypes.c_int32),
+        ("output_state_stride", ctypes.c_int64),
+        ("state_indices", ctypes.c_void_p),
+        ("state_indices_type", ctypes.c_int32),
+        ("pool_size", ctypes.c_int64),
+        ("doutput", ctypes.c_void_p),
+        ("doutput_stride", ctypes.c_int64),
+        ("dfinal_state", ctypes.c_void_p),
+        ("dx", ctypes.c_void_p),
+        ("dweight", ctypes.c_void_p),
+        ("dbias", ctypes.c_void_p),
+        ("dinitial_state", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+        ("status", ctypes.c_void_p),
+    ]
+
+
+class ScanParams(ctypes.Structure):
+    _fields_ = [
+        ("total_tokens", ctypes.c_int64),
+        ("num_seqs", ctypes.c_int32),
+        ("channels", ctypes.c_int32),
+        ("num_states", ctypes.c_int32),
+        ("groups", ctypes.c_int32),
+        ("x_dtype", ctypes.c_int32),
+        ("delta_softplus", ctypes.c_int32),
+        ("x", ctypes.c_void_p),
+        ("delta", ctypes.c_void_p),
+        ("z", ctypes.c_void_p),
+        ("x_stride", ctypes.c_int64),
+        ("delta_stride", ctypes.c_int64),
+        ("z_stride", ctypes.c_int64),
+        ("A", ctypes.c_void_p),
+        ("B", ctypes.c_void_p),
+        ("C", ctypes.c_void_p),
+        ("b_stride", ctypes.c_int64),
+        ("c_stride", ctypes.c_int64),
+        ("D", ctypes.c_void_p),
+        ("delta_bias", ctypes.c_void_p),
+        ("cu_seqlens", ctypes.c_void_p),
+        ("cu_seqlens_type", ctypes.c_int32),
+        ("output", ctypes.c_void_p),
+        ("initial_state", ctypes.c_void_p),
+        ("initial_state_dtype", ctypes.c_int32),
+        ("initial_state_stride", ctypes.c_int64),
+        ("output_final_state", ctypes.c_int32),
+        ("output_state", ctypes.c_void_p),
+        ("output_state_dtype", ctypes.c_int32),
+        ("output_state_stride", ctypes.c_int64),
+        ("state_indices", ctypes.c_void_p),
+        ("state_indices_type", ctypes.c_int32),
+        ("pool_size", ctypes.c_int64),
+        ("chunk_states", ctypes.c_void_p),
+        ("doutput", ctypes.c_void_p),
+        ("doutput_stride", ctypes.c_int64),
+        ("dfinal_state", ctypes.c_void_p),
+        ("dx", ctypes.c_void_p),
+        ("ddelta", ctypes.c_void_p),
+        ("dz", ctypes.c_void_p),
+        ("dB", ctypes.c_void_p),
+        ("dC", ctypes.c_void_p),
+        ("dA", ctypes.c_void_p),
+        ("dD", ctypes.c_void_p),
+        ("ddelta_bias", ctypes.c_void_p),
+        ("dinitial_state", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+        ("status", ctypes.c_void_p),
+    ]
+
+
+class BeamParams(ctypes.Structure):
+    _fields_ = [
+        ("num_groups", ctypes.c_int32),
+        ("num_beams", ctypes.c_int32),
+        ("vocab", ctypes.c_int32),
+        ("num_candidates", ctypes.c_int32),
+        ("logits_dtype", ctypes.c_int32),
+        ("logits", ctypes.c_void_p),
+        ("logits_stride", ctypes.c_int64),
+        ("scores", ctypes.c_void_p),
+        ("out_scores", ctypes.c_void_p),
+        ("out_parents", ctypes.c_void_p),
+        ("out_tokens", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class ReorderPool(ctypes.Structure):
+    _fields_ = [
+        ("pool", ctypes.c_void_p),
+        ("dtype", ctypes.c_int32),
+        ("extent", _i64x3),
+        ("strides", _i64x4),
+    ]
+
+
+class ReorderParams(ctypes.Structure):
+    _fields_ = [
+        ("num_groups", ctypes.c_int32),
+        ("num_beams", ctypes.c_int32),
+        ("num_pools", ctypes.c_int32),
+        ("pool_rows", ctypes.c_int64),
+        ("pools", ctypes.c_void_p),
+        ("state_indices", ctypes.c_void_p),
+        ("parents", ctypes.c_void_p),
+        ("new_indices", ctypes.c_void_p),
+        ("index_type", ctypes.c_int32),
+        ("status", ctypes.c_void_p),
+    ]
+
 _lib = None
 
 
@@ -214,6 +355,26 @@ def lib():
         L.gdn_pool_compact.restype = ctypes.c_int
         L.gdn_pool_compact.argtypes = [pool, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                        ctypes.c_void_p]
+        for what, cls in (("convolution", ConvolutionParams), ("scan", ScanParams)):
+            block = ctypes.POINTER(cls)
+            size = getattr(L, "gdn_%s_workspace_size" % what)
+            size.restype, size.argtypes = ctypes.c_size_t, [block, ctypes.c_int32]
+            check = getattr(L, "gdn_validate_%s_host" % what)
+            check.restype, check.argtypes = ctypes.c_int, [block, ctypes.c_int32]
+            for name in ("gdn_%s", "gdn_%s_backward", "gdn_%s_decode"):
+                getattr(L, name % what).restype = ctypes.c_int
+                getattr(L, name % what).argtypes = [block, ctypes.c_void_p]
+        L.gdn_scan_chunk.restype = ctypes.c_int64
+        L.gdn_scan_chunk.argtypes = [ctypes.POINTER(ScanParams)]
+        beam, order = ctypes.POINTER(BeamParams), ctypes.POINTER(ReorderParams)
+        L.gdn_beam_workspace_size.restype = ctypes.c_size_t
+        L.gdn_beam_workspace_size.argtypes = [beam]
+        for name, block in (("gdn_validate_beam_host", beam), ("gdn_validate_reorder_host", order)):
+            getattr(L, name).restype = ctypes.c_int
+            getattr(L, name).argtypes = [block]
+        for name, block in (("gdn_beam_select", beam), ("gdn_pool_reorder", order)):
+            getattr(L, name).restype = ctypes.c_int
+            getattr(L, name).argtypes = [block, ctypes.c_void_p]
         _lib = L
     return _lib
 

@@ -2,7 +2,7 @@
 
 Each source compiles to its own object in parallel, then one link step makes
 the shared library.  _calls.so, the CPython module that marshals the
-recurrence's and the state pool's calls, is host code against torch's headers.
+calls of all operators but the delta rule's, is host code against torch's headers.
 
 Usage: python -m gated_deltanet_chunked_varlen_amd.build
 """
@@ -19,7 +19,9 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libgdn_prefill.so")
 SOURCES = ["gdn_host.hip", "k0_chunk_index.hip", "k1_intra.hip",
            "k2_state.hip", "k3_output.hip", "k4_decode.hip", "k5_cp.hip",
-           "gdn_recurrence_host.hip", "k6_recurrence.hip", "k7_pool.hip"]
+           "gdn_recurrence_host.hip", "k6_recurrence.hip", "k7_pool.hip",
+           "gdn_layers_host.hip", "k8_convolution.hip", "k9_scan.hip", "k10_scan_backward.hip",
+           "k11_beam.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
@@ -30,6 +32,7 @@ FLAGS = [
 
 
 CALLS = os.path.join(HERE, "_calls.so")
+CALLS_SOURCES = ["torch_calls.cpp", "torch_layer_calls.cpp"]
 CXX = os.environ.get("CXX", "g++")
 
 
@@ -42,13 +45,13 @@ def build_calls(verbose: bool = False, out: str = CALLS) -> str:
     cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
            "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI)]
     cmd += ["-isystem" + p for p in include_paths() + [sysconfig.get_paths()["include"]]]
-    cmd += [os.path.join(CSRC, "torch_calls.cpp"), "-o", tmp]
+    cmd += [os.path.join(CSRC, s) for s in CALLS_SOURCES] + ["-o", tmp]
     cmd += ["-L" + p for p in library_paths()] + ["-ltorch_python", "-ltorch_cpu", "-lc10"]
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError("%s failed on torch_calls.cpp:\n%s" % (CXX, r.stderr))
+        raise RuntimeError("%s failed on the calls:\n%s" % (CXX, r.stderr))
     os.replace(tmp, out)
     return out
 

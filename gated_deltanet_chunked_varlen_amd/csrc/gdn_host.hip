@@ -207,17 +207,17 @@ const char *gdn_status_string(int code) {
   switch (code) {
     case GDN_OK: return "ok";
     case GDN_ERR_NULL: return "a required pointer is NULL";
-    case GDN_ERR_SHAPE: return "invalid token, sequence or head counts, or head size not in {32, 64, 128}";
+    case GDN_ERR_SHAPE: return "invalid token, sequence, head or other counts (head size in {32, 64, 128}, convolution width 2 to 4, states 1 to 64, beams and candidates 1 to 64), or more than a grid holds";
     case GDN_ERR_HEAD_RATIO: return "illegal head sharing: need (hq == hk and hv % hq == 0) or (hk == hv and hq % hk == 0)";
     case GDN_ERR_DTYPE: return "unsupported dtype or index type";
     case GDN_ERR_CHECKPOINT: return "checkpoint_every_n_tokens must be a non-negative multiple of 64 and state_checkpoints / checkpoint_cu_starts must be given together";
-    case GDN_ERR_STATE: return "inconsistent state arguments (output_state required for a final state; pool_size required with state_indices; no state_indices in a backward pass, no chunk_states in a decode step; pool views or row lists that share elements)";
+    case GDN_ERR_STATE: return "inconsistent state arguments (output_state required for a final state; pool_size required with state_indices; no state_indices in a backward pass, no chunk_states in a decode step; pool views or row lists that share elements; an output that overlaps an input)";
     case GDN_ERR_MAX_SEQLEN: return "max_seqlen outside [ceil(total_tokens / num_seqs), total_tokens]";
-    case GDN_ERR_WORKSPACE: return "workspace missing or smaller than gdn_prefill_workspace_size() / gdn_recurrence_workspace_size()";
-    case GDN_ERR_STRIDES: return "state strides must be all zero (contiguous) or positive and non-overlapping";
+    case GDN_ERR_WORKSPACE: return "workspace missing or smaller than the call's gdn_*_workspace_size()";
+    case GDN_ERR_STRIDES: return "strides must be zero (contiguous) or positive and non-overlapping";
     case GDN_ERR_DEVICE: return "current device is not gfx950 (MI355X)";
     case GDN_ERR_LAUNCH: return "kernel launch failed";
-    case GDN_ERR_ALIGN: return "q, k, v and output must be 16-byte aligned (recurrence and pool tensors: to their element size) and the workspace 256-byte aligned";
+    case GDN_ERR_ALIGN: return "q, k, v and output must be 16-byte aligned (tensors of the other operators: to their element size) and the workspace 256-byte aligned";
     case GDN_ERR_CP: return "use_cp must be 0 (auto), 1 (on) or 2 (off) and cp_chunk_len a non-negative multiple of 64; use_cp = on needs bf16 or fp16 inputs, head size 128 and at most 63 sequences";
     case GDN_ERR_SCRATCH: return "gdn_prefill_noalloc: the call needs more workspace than the static scratch (GDN_NOALLOC_SCRATCH_BYTES) or its address is unavailable";
     case (int)GDN_STATUS_CU_SEQLENS: return "status: cu_seqlens not non-decreasing within [0, total_tokens]";

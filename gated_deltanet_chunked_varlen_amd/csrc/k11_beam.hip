@@ -1,0 +1,397 @@
+// k11_beam.hip -- beam search over state pools: selection of the best
+// continuations, and the rows of state pools brought in the order of the
+// selected parents.
+//
+// Selection.  Continuation v of beam k scores score_k + logit_kv - log sum_v
+// exp(logit_kv); the M best of a group's K V are wanted, ties to the lowest
+// (beam, token).  Within a beam the order is that of the logits, so the first
+// kernel reads every row once, cut into parts: a workgroup keeps its part in
+// registers, sums the exponentials relative to the part's largest logit, and
+// finds the part's M largest (logit, token) keys: the M-th largest of the
+// threads' largest keys bounds them from below, at most M threads hold a key at
+// or above it, and these few are ranked by counting.  The second kernel, a
+// workgroup per group, combines the sums (in fp64: scores of different beams
+// are compared) and takes the M best of the parts' candidates in the same way.
+// Bounded by HBM for a batch (the logits), by latency for one request.
+//
+// Reordering.  Within a group the first child of a parent keeps its row; the
+// other children take the rows of beams without a child, in order, and only
+// those are copied.  A row is never both source and destination, so nothing has
+// to be set aside: one kernel, in which every workgroup works out its group's
+// plan from the parents (a wave, by ballots).
+#include "gdn_layers.h"
+
+#include <algorithm>
+
+#pragma clang fp contract(off)
+
+namespace gdn {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxM = GDN_BEAM_MAX;  // candidates of a group, beams of a group
+constexpr float kInf = __builtin_inff();
+
+typedef unsigned long long u64;
+
+// A key orders by value first and by place (ascending) second; none is 0.
+__device__ __forceinline__ u64 key_of(float v, unsigned place) {
+  const unsigned b = __float_as_uint(v + 0.f);  // -0 is 0
+  const unsigned o = b & 0x80000000u ? ~b : b | 0x80000000u;
+  return (u64)o << 32 | (0xFFFFFFFFu - place);
+}
+__device__ __forceinline__ float key_value(u64 k) {
+  const unsigned o = (unsigned)(k >> 32);
+  return __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
+}
+__device__ __forceinline__ unsigned key_place(u64 k) { return 0xFFFFFFFFu - (unsigned)k; }
+
+// The M largest of the workgroup's keys, E per thread (Key{}: none), sorted into
+// `best` (LDS, M entries, Key{} behind the last one).
+template <typename Key, int E, int M> struct Largest {
+  static constexpr int kKeys = M * E < kThreads ? kThreads : M * E;
+  Key top[kThreads];
+  Key cand[kKeys];
+  Key best[M];
+  unsigned count;
+  Key bound;
+
+  __device__ __forceinline__ void find(const Key (&k)[E], int m) {
+    const int tid = threadIdx.x;
+    Key mine{};
+#pragma unroll
+    for (int e = 0; e < E; ++e) if (k[e] > mine) mine = k[e];
+    top[tid] = mine;
+    if (tid < M) best[tid] = Key{};
+    if (tid == 0) {
+      count = 0;
+      bound = Key{};
+    }
+    __syncthreads();
+    // this thread's rank among the largest keys (keys are distinct but for Key{})
+    int rank = 0;
+#pragma unroll 8
+    for (int i = 0; i < kThreads; ++i) rank += top[i] > mine;
+    if (rank == m - 1 && mine > Key{}) bound = mine;
+    __syncthreads();
+    const Key from = bound;
+    if (!(from > mine)) {
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (!(from > k[e]) && k[e] > Key{}) cand[atomicAdd(&count, 1u)] = k[e];
+    }
+    __syncthreads();
+    const int n = (int)count;
+    for (int i = tid; i < n; i += kThreads) {
+      const Key x = cand[i];
+      int r = 0;
+      for (int j = 0; j < n; ++j) r += cand[j] > x;
+      if (r < m) best[r] = x;
+    }
+    __syncthreads();
+  }
+};
+
+__device__ __forceinline__ float wave_max(float x) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor(x, o));
+  return x;
+}
+__device__ __forceinline__ double wave_sum(double x) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o);
+  return x;
+}
+
+// A part of one row, E logits per thread.  VEC: rows are whole aligned groups of
+// 16 bytes.
+template <typename T, int E, int M, bool VEC>
+__global__ void __launch_bounds__(kThreads) beam_rows_kernel(BeamArgs a) {
+  constexpr int V = VEC ? 16 / (int)sizeof(T) : 1;
+  constexpr int S = E / V;  // vectors per thread
+  __shared__ Largest<u64, E, M> L;
+  __shared__ float s_max[kThreads / 64];
+  __shared__ double s_sum[kThreads / 64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int row = blockIdx.x / a.parts, part = blockIdx.x % a.parts;
+  const int from = part * a.part_len, to = min(from + a.part_len, a.V);
+  const T *p = (const T *)a.logits + (int64_t)row * a.stride;
+  const bool live = a.scores[row] > -kInf;
+  float x[E];
+#pragma unroll
+  for (int s = 0; s < S; ++s) {
+    const int at = from + (s * kThreads + tid) * V;
+    float o[V];
+    if (at < to) {
+      widen(load_vec<T, V>(p + at), o);
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[e] = -kInf;
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) x[s * V + e] = o[e] == o[e] ? o[e] : -kInf;  // NaN: never taken
+  }
+  float top = -kInf;
+#pragma unroll
+  for (int e = 0; e < E; ++e) top = fmaxf(top, x[e]);
+  top = wave_max(top);
+  if (lane == 0) s_max[wave] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
+  // relative to the largest one, which counts 1 also where it is infinite
+  float sum = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    sum += x[e] == top ? 1.f : __builtin_amdgcn_exp2f(kLog2E * (x[e] - top));
+  const double all = wave_sum(top == -kInf ? 0.0 : (double)sum);
+  if (lane == 0) s_sum[wave] = all;
+  u64 k[E];
+#pragma unroll
+  for (int s = 0; s < S; ++s)
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const int at = from + (s * kThreads + tid) * V + e;
+      // the continuations of a beam that has ended are all alike
+      k[s * V + e] = at < to ? key_of(live ? x[s * V + e] : -kInf, (unsigned)at) : 0;
+    }
+  L.find(k, a.M);
+  const int64_t o = (int64_t)blockIdx.x;
+  if (tid < a.M) {
+    const u64 b = L.best[tid];
+    a.best[o * a.M + tid] = b ? key_value(b) : -kInf;
+    a.where[o * a.M + tid] = b ? (int)key_place(b) : -1;
+  }
+  if (tid == 0) {
+    a.stat[2 * o] = top;
+    a.stat[2 * o + 1] = (float)((s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3]));
+  }
+}
+
+// A score in fp64, in the order of whole numbers, and (beam, token) descending.
+struct Score {
+  u64 value, place;
+  __device__ __forceinline__ bool operator>(const Score &o) const {
+    return value > o.value || (value == o.value && place > o.place);
+  }
+};
+__device__ __forceinline__ u64 order_of(double v) {
+  const u64 b = (u64)__double_as_longlong(v + 0.0);
+  return b >> 63 ? ~b : b | 1ull << 63;
+}
+__device__ __forceinline__ double value_of(u64 o) {
+  return __longlong_as_double((long long)(o >> 63 ? o & ~(1ull << 63) : ~o));
+}
+
+constexpr int kTake = 8;  // candidates per thread and round
+
+template <int M> __global__ void __launch_bounds__(kThreads) beam_group_kernel(BeamArgs a) {
+  __shared__ Largest<Score, kTake + 1, M> L;
+  __shared__ double s_log[kMaxM];
+  __shared__ float s_top[kMaxM];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, b = blockIdx.x;
+  const int per = a.parts * a.M;
+  const int64_t first = (int64_t)b * a.K * a.parts, n = (int64_t)a.K * per;
+  for (int k = wave; k < a.K; k += kThreads / 64) {
+    const float *st = a.stat + 2 * (first + (int64_t)k * a.parts);
+    float top = -kInf;
+    for (int i = lane; i < a.parts; i += 64) top = fmaxf(top, st[2 * i]);
+    top = wave_max(top);
+    double sum = 0.0;
+    for (int i = lane; i < a.parts; i += 64) {
+      const double own = st[2 * i + 1];
+      sum += st[2 * i] == top ? own : own * exp((double)st[2 * i] - (double)top);
+    }
+    sum = wave_sum(sum);
+    if (lane == 0) {
+      s_top[k] = top;
+      s_log[k] = log(sum);
+    }
+  }
+  __syncthreads();
+  Score mine{};
+  for (int64_t base = 0; base < n; base += kTake * kThreads) {
+    Score c[kTake + 1];
+    bool any = false;
+#pragma unroll
+    for (int e = 0; e < kTake; ++e) {
+      const int64_t i = base + e * kThreads + tid;
+      c[e] = Score{};
+      if (i >= n) continue;
+      const int k = (int)(i / per), at = a.where[first * a.M + i];
+      if (at < 0) continue;
+      const float logit = a.best[first * a.M + i], score = a.scores[(int64_t)b * a.K + k];
+      double v = -(double)kInf;
+      // (of an infinite largest logit the others have no share)
+      if (logit > -kInf && score > -kInf) {
+        const double own = logit == s_top[k] ? 0.0 : (double)logit - (double)s_top[k];
+        if (own > -(double)kInf) v = (double)score + (own - s_log[k]);
+      }
+      c[e] = Score{order_of(v), ~((u64)k * (u64)a.V + (u64)at)};
+      any |= c[e] > L.best[a.M - 1] || base == 0;
+    }
+    // nothing better than what there is: on to the next ones
+    if (!__syncthreads_or(any)) continue;
+    c[kTake] = mine;  // the best so far, one a thread
+    L.find(c, a.M);
+    mine = tid < a.M ? L.best[tid] : Score{};
+  }
+  if (tid >= a.M) return;
+  const u64 flat = ~mine.place;
+  const int64_t o = (int64_t)b * a.M + tid;
+  a.out_scores[o] = (float)value_of(mine.value);
+  a.parents[o] = (int)(flat / (u64)a.V);
+  a.tokens[o] = (int)(flat % (u64)a.V);
+}
+
+// -------------------------------------------------------------------- reorder
+
+// Child j's share of its group's plan: the beam whose old row it takes, and the
+// parent if that row has to be overwritten with its row (else -1).
+struct Share {
+  int row_of, from;
+};
+
+// For the whole wave; parents of the group, one a lane.
+__device__ __forceinline__ Share share_of(int parent, int K, int j) {
+  u64 used = 0, first = 0;
+  for (int i = 0; i < K; ++i) {
+    const int q = __builtin_amdgcn_readlane(parent, i);
+    if ((unsigned)q < (unsigned)K && !(used >> q & 1)) {
+      used |= 1ull << q;
+      first |= 1ull << i;
+    }
+  }
+  const int own = __builtin_amdgcn_readlane(parent, j);
+  if (first >> j & 1) return {own, -1};
+  // of the children that keep no row the r-th takes the r-th row that is left
+  const u64 all = K < 64 ? (1ull << K) - 1 : ~0ull;
+  u64 left = ~used & all;
+  for (int r = __builtin_popcountll(~first & ((1ull << j) - 1)); r > 0; --r) left &= left - 1;
+  return {__builtin_ctzll(left), (unsigned)own < (unsigned)K ? own : -1};
+}
+
+// The status word, by a workgroup of its own.
+__device__ __forceinline__ void reorder_status(const ReorderArgs &a, unsigned *map) {
+  __shared__ unsigned s_bits;
+  const int words = (a.rows + 31) / 32;
+  for (int i = threadIdx.x; i < words; i += kThreads) map[i] = 0u;
+  if (threadIdx.x == 0) s_bits = 0u;
+  __syncthreads();
+  unsigned bits = 0;
+  for (int64_t i = threadIdx.x; i < (int64_t)a.B * a.K; i += kThreads) {
+    const int64_t r = load_index_any(a.idx, a.type, i), p = load_index_any(a.parents, a.type, i);
+    if (p < -1 || p >= a.K || r < -1 || r >= a.rows) bits |= GDN_STATUS_POOL_ROW;
+    if (r >= 0 && r < a.rows && (atomicOr(&map[r >> 5], 1u << (r & 31)) >> (r & 31) & 1))
+      bits |= GDN_STATUS_POOL_DUPLICATE;
+  }
+  if (bits) atomicOr(&s_bits, bits);
+  __syncthreads();
+  if (threadIdx.x == 0) a.status[0] = (int32_t)s_bits;
+}
+
+template <typename V>
+__device__ __forceinline__ void copy_bytes(const char *src, char *dst, int64_t b0, int64_t b1) {
+  constexpr int U = 4;
+  constexpr int64_t step = (int64_t)sizeof(V) * kThreads;
+  for (int64_t b = b0 + (int64_t)sizeof(V) * threadIdx.x; b < b1; b += U * step) {
+    V v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (b + u * step < b1) v[u] = *(const V *)(src + b + u * step);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (b + u * step < b1) *(V *)(dst + b + u * step) = v[u];
+  }
+}
+
+template <typename U>
+__device__ __forceinline__ void copy_strided(const ReorderArgs::Pool &p, const char *src, char *dst,
+                                             int64_t e0, int64_t e1) {
+  for (int64_t e = e0 + threadIdx.x; e < e1; e += kThreads) {
+    const int64_t k = e % p.d3, r = e / p.d3;
+    const int64_t off = (r / p.d2) * p.str[1] + (r % p.d2) * p.str[2] + k * p.str[3];
+    *(U *)(dst + off) = *(const U *)(src + off);
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) pool_reorder_kernel(ReorderArgs a) {
+  extern __shared__ unsigned map[];
+  const ReorderArgs::Pool &p = a.pool[blockIdx.y];
+  const int64_t unit = blockIdx.x, beam = unit / p.units;
+  if (beam >= (int64_t)a.B * a.K) {
+    if (a.status && blockIdx.y == 0 && blockIdx.x == gridDim.x - 1) reorder_status(a, map);
+    return;
+  }
+  const int lane = threadIdx.x & 63, j = (int)(beam % a.K);
+  const int64_t group = beam - j;
+  int parent = -1;
+  if (lane < a.K) {
+    const int64_t q = load_index_any(a.parents, a.type, group + lane);
+    parent = q >= 0 && q < a.K ? (int)q : -1;
+  }
+  const Share s = share_of(parent, a.K, j);
+  const int64_t to = load_index_any(a.idx, a.type, group + s.row_of);
+  const int slice = (int)(unit % p.units);
+  if (a.new_idx && blockIdx.y == 0 && slice == 0 && threadIdx.x == 0) {
+    if (a.type == GDN_I64) ((int64_t *)a.new_idx)[beam] = to;
+    else ((int32_t *)a.new_idx)[beam] = (int32_t)to;
+  }
+  if (s.from < 0) return;
+  const int64_t from = load_index_any(a.idx, a.type, group + s.from);
+  if (to < 0 || to >= a.rows || from < 0 || from >= a.rows || from == to) return;
+  const char *src = p.p + from * p.str[0];
+  char *dst = p.p + to * p.str[0];
+  const int64_t e0 = (int64_t)slice * p.unit, e1 = min(e0 + p.unit, p.row);
+  if (p.flat) {
+    if (p.align >= 16) copy_bytes<u32x4>(src, dst, e0 * p.es, e1 * p.es);
+    else if (p.es == 4) copy_bytes<uint32_t>(src, dst, e0 * 4, e1 * 4);
+    else if (p.es == 2) copy_bytes<uint16_t>(src, dst, e0 * 2, e1 * 2);
+    else copy_bytes<uint8_t>(src, dst, e0, e1);
+  } else if (p.es == 4) {
+    copy_strided<uint32_t>(p, src, dst, e0, e1);
+  } else if (p.es == 2) {
+    copy_strided<uint16_t>(p, src, dst, e0, e1);
+  } else {
+    copy_strided<uint8_t>(p, src, dst, e0, e1);
+  }
+}
+
+// ------------------------------------------------------------------- launches
+
+template <typename T, int E, int M> hipError_t rows(const BeamArgs &a, hipStream_t s) {
+  const dim3 grid((unsigned)((int64_t)a.B * a.K * a.parts)), block(kThreads);
+  if (a.vec) beam_rows_kernel<T, E, M, true><<<grid, block, 0, s>>>(a);
+  else beam_rows_kernel<T, E, M, false><<<grid, block, 0, s>>>(a);
+  return hipGetLastError();
+}
+template <typename T> hipError_t rows_of(const BeamArgs &a, hipStream_t s) {
+  if (a.part_len > 8 * kThreads)
+    return a.M <= 16 ? rows<T, 32, 16>(a, s) : rows<T, 32, kMaxM>(a, s);
+  return a.M <= 16 ? rows<T, 8, 16>(a, s) : rows<T, 8, kMaxM>(a, s);
+}
+
+}  // namespace
+
+hipError_t launch_beam_select(const BeamArgs &a, hipStream_t s) {
+  const hipError_t e = a.dtype == GDN_F32    ? rows_of<float>(a, s)
+                       : a.dtype == GDN_BF16 ? rows_of<bf16>(a, s)
+                                             : rows_of<f16>(a, s);
+  if (e != hipSuccess) return e;
+  if (a.M <= 16) beam_group_kernel<16><<<dim3(a.B), dim3(kThreads), 0, s>>>(a);
+  else beam_group_kernel<kMaxM><<<dim3(a.B), dim3(kThreads), 0, s>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_pool_reorder(const ReorderArgs &a, hipStream_t s) {
+  int64_t units = 0;
+  for (int i = 0; i < a.pools; ++i) units = std::max<int64_t>(units, a.pool[i].units);
+  units *= (int64_t)a.B * a.K;
+  const unsigned x = (unsigned)units + (a.status ? 1u : 0u);
+  if (x == 0) return hipSuccess;
+  const int lds = a.status ? (a.rows + 31) / 32 * 4 : 0;
+  pool_reorder_kernel<<<dim3(x, (unsigned)a.pools), dim3(kThreads), lds, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace gdn

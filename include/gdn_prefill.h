@@ -459,6 +459,256 @@ int gdn_pool_reset(const gdn_pool_params *p, void *stream);
 int gdn_pool_compact(const gdn_pool_params *p, void *new_rows, int32_t *num_live,
                      int32_t *row_map, void *stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Short causal depthwise convolution of packed sequences, as layers put it in
+ * front of a recurrence.  With x~ a sequence's state (its W - 1 last inputs from
+ * before, zero without one) followed by its tokens,
+ *
+ *     output_t = act(bias + sum_j weight_j x~_{t + j}),  j < W, act: none or SiLU
+ *
+ * in fp32, rounded once; the final state is the last W - 1 rows of x~.
+ *
+ * Shapes: x, output, doutput, dx [T, C] in x_dtype (F32, BF16 or F16); weight
+ * [C, W], bias [C] (or NULL) in weight_dtype: F32 or x_dtype; W is 2, 3 or 4.
+ * x and doutput have token strides in elements (0 = contiguous); every other
+ * tensor is contiguous.  States are [rows, W - 1, C], oldest row first, in any
+ * state dtype with a row stride in elements (0 = contiguous).  cu_seqlens,
+ * num_seqs, state_indices, pool_size and status are those of
+ * gdn_prefill_params; output_state may be the same memory as initial_state,
+ * and state_indices must be unique where a final state is written.  No other
+ * two tensors of a call may overlap (GDN_ERR_STATE where output or dx meets x
+ * or doutput); in a decode step output may be x itself.  Tensors start on a
+ * boundary of their element size.  Rows of output outside every sequence are
+ * untouched, those of dx are zero.  A sequence whose state index is out of range
+ * starts from zero and writes no final state.  A call takes at most 2^30
+ * sequences and (ceil(T / 16) + N) * ceil(C / 64) < 2^26 (a decode step
+ * C * N < 2^32); GDN_ERR_SHAPE otherwise.
+ */
+typedef struct gdn_convolution_params {
+  int64_t total_tokens;    /* T >= 0 */
+  int32_t num_seqs;        /* N >= 0; with cu_seqlens NULL, N must be 1 */
+  int32_t channels;        /* C >= 1 */
+  int32_t width;           /* W: 2, 3 or 4 */
+  int32_t x_dtype;         /* gdn_dtype: F32, BF16, F16 */
+  int32_t weight_dtype;    /* F32 or x_dtype */
+  int32_t silu;            /* 0: no activation, 1: SiLU */
+  const void *x;
+  int64_t x_stride;
+  const void *weight, *bias;
+  const void *cu_seqlens;  /* [N+1], NULL = one sequence [0, T] */
+  int32_t cu_seqlens_type;
+  void *output;
+  const void *initial_state;
+  int32_t initial_state_dtype;
+  int64_t initial_state_stride;
+  int32_t output_final_state;
+  void *output_state;
+  int32_t output_state_dtype;
+  int64_t output_state_stride;
+  const void *state_indices; /* [N] or NULL */
+  int32_t state_indices_type;
+  int64_t pool_size;
+  /* gradients, gdn_convolution_backward() only */
+  const void *doutput;       /* [T, C] x_dtype */
+  int64_t doutput_stride;
+  const float *dfinal_state; /* [N, W - 1, C] or NULL (zero) */
+  void *dx;
+  float *dweight;            /* [C, W] */
+  float *dbias;              /* [C] or NULL (not formed) */
+  float *dinitial_state;     /* [N, W - 1, C] or NULL (not formed) */
+  void *workspace;
+  size_t workspace_bytes;
+  int32_t *status;           /* optional device word */
+} gdn_convolution_params;
+
+/* Bytes of workspace gdn_convolution() (backward == 0; more than 63 sequences
+ * only) or gdn_convolution_backward() (backward != 0) needs.  Only the shape
+ * fields are read.  Host only; 0 can be a valid answer. */
+size_t gdn_convolution_workspace_size(const gdn_convolution_params *p, int32_t backward);
+
+/* The host-side checks of gdn_convolution() (mode 0), its backward pass (1) and
+ * its decode step (2); no GPU needed. */
+int gdn_validate_convolution_host(const gdn_convolution_params *p, int32_t mode);
+
+int gdn_convolution(const gdn_convolution_params *p, void *stream);
+
+/* The backward pass.  state_indices must be NULL; output and output_state are
+ * ignored.  Sums over tokens are formed in fp32 in a fixed order. */
+int gdn_convolution_backward(const gdn_convolution_params *p, void *stream);
+
+/* One decode step: token i of x, output [N, C] is the new token of sequence i
+ * (total_tokens == num_seqs, cu_seqlens NULL).  No workspace. */
+int gdn_convolution_decode(const gdn_convolution_params *p, void *stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Selective state space scan of packed sequences.  With the step size
+ * d_t = delta_t + delta_bias, or log(1 + e^ of it) with delta_softplus, for
+ * every channel and each of its N states n, in fp32,
+ *
+ *     h_t = exp(d_t A) h_{t-1} + d_t B_t x_t
+ *     y_t = sum_n C_t h_t + D x_t,     output_t = y_t, or y_t silu(z_t)
+ *
+ * from the given initial state (or zero).  A channel belongs to group
+ * c / (channels / groups) of B and C.
+ *
+ * Shapes: x, delta, z (or NULL), output and their gradients [T, channels], B, C
+ * and theirs [T, groups, N], all in x_dtype (F32, BF16 or F16); A [channels, N],
+ * D, delta_bias [channels] (or NULL) fp32.  1 <= N <= 64.  x, delta, z, B, C and
+ * doutput have token strides in elements (0 = contiguous); every other tensor is
+ * contiguous.  States are [rows, channels, N] in any state dtype with a row
+ * stride in elements (0 = contiguous).  cu_seqlens, num_seqs, state_indices,
+ * pool_size and status are those of gdn_prefill_params; output_state may be the
+ * same memory as initial_state, and state_indices must be unique where a final
+ * state is written.  No other two tensors of a call may overlap (GDN_ERR_STATE
+ * where output or a gradient meets an input).  Tensors start on a boundary of
+ * their element size, the workspace on a 256-byte boundary.  Calls that overlap
+ * in time need workspaces of their own.  Rows of output outside every sequence
+ * are untouched, those of gradients are zero.  An empty sequence's final state
+ * is its initial state.  A sequence whose state index is out of range starts
+ * from zero and writes no final state.  The products exp(A sum d) over 256
+ * consecutive tokens must stay finite (they do for A <= 0 and d >= 0).
+ * channels <= 2^24, and T and the channels are limited by a grid's size
+ * (GDN_ERR_SHAPE).
+ */
+typedef struct gdn_scan_params {
+  int64_t total_tokens;    /* T >= 0 */
+  int32_t num_seqs;        /* sequences; with cu_seqlens NULL, 1 */
+  int32_t channels;
+  int32_t num_states;      /* N */
+  int32_t groups;          /* divides channels */
+  int32_t x_dtype;         /* gdn_dtype: F32, BF16, F16 */
+  int32_t delta_softplus;  /* 0 or 1 */
+  const void *x, *delta, *z;
+  int64_t x_stride, delta_stride, z_stride;
+  const float *A;
+  const void *B, *C;
+  int64_t b_stride, c_stride;
+  const float *D, *delta_bias;
+  const void *cu_seqlens;  /* [num_seqs + 1], NULL = one sequence [0, T] */
+  int32_t cu_seqlens_type;
+  void *output;
+  const void *initial_state;
+  int32_t initial_state_dtype;
+  int64_t initial_state_stride;
+  int32_t output_final_state;
+  void *output_state;
+  int32_t output_state_dtype;
+  int64_t output_state_stride;
+  const void *state_indices; /* [num_seqs] or NULL */
+  int32_t state_indices_type;
+  int64_t pool_size;
+  /* fp32 [ceil(T / gdn_scan_chunk()), N, channels] or NULL.  gdn_scan() writes
+   * the states before every gdn_scan_chunk() tokens; gdn_scan_backward() reads
+   * them, or forms them in its workspace with one more pass when NULL. */
+  float *chunk_states;
+  /* gradients, gdn_scan_backward() only */
+  const void *doutput;       /* [T, channels] x_dtype */
+  int64_t doutput_stride;
+  const float *dfinal_state; /* [num_seqs, channels, N] or NULL (zero) */
+  void *dx, *ddelta, *dz;    /* dz: required with z */
+  void *dB, *dC;
+  float *dA;                 /* [channels, N] */
+  float *dD, *ddelta_bias;   /* [channels] or NULL (not formed) */
+  float *dinitial_state;     /* [num_seqs, channels, N] or NULL (not formed) */
+  void *workspace;
+  size_t workspace_bytes;
+  int32_t *status;           /* optional device word */
+} gdn_scan_params;
+
+/* Tokens per row of chunk_states for these sizes (0: an invalid shape). */
+int64_t gdn_scan_chunk(const gdn_scan_params *p);
+
+/* Bytes of workspace gdn_scan() (backward == 0) or gdn_scan_backward() needs;
+ * only the shape fields and whether chunk_states is given are read. */
+size_t gdn_scan_workspace_size(const gdn_scan_params *p, int32_t backward);
+
+/* The host-side checks of gdn_scan() (mode 0), its backward pass (1) and its
+ * decode step (2); no GPU needed. */
+int gdn_validate_scan_host(const gdn_scan_params *p, int32_t mode);
+
+int gdn_scan(const gdn_scan_params *p, void *stream);
+
+/* The backward pass.  state_indices must be NULL, initial_state fp32; output and
+ * output_state are ignored.  The states are formed again in fp32.  Results do
+ * not depend on the order in which workgroups run. */
+int gdn_scan_backward(const gdn_scan_params *p, void *stream);
+
+/* One decode step: token i of x, delta, z, B, C, output is the new token of
+ * sequence i (total_tokens == num_seqs, cu_seqlens and chunk_states NULL).  No
+ * workspace. */
+int gdn_scan_decode(const gdn_scan_params *p, void *stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Beam search: the best continuations of a group's beams.  Continuation v of
+ * beam k scores scores_k + logits_kv - log sum_u exp(logits_ku); the
+ * num_candidates best of a group's K V continuations are returned in descending
+ * order, ties to the lowest beam, then the lowest token.  Sums over the
+ * vocabulary are formed in fp32 (their parts joined in fp64), scores compared in
+ * fp64 and returned in fp32.  A logit that is NaN or -inf, and every one of a
+ * beam whose score is -inf or NaN (a beam that has ended), scores -inf; such
+ * continuations come last, by beam and token.  Logits of +inf share the beam's
+ * whole probability.
+ */
+#define GDN_BEAM_MAX 64 /* beams of a group, candidates of a group */
+
+typedef struct gdn_beam_params {
+  int32_t num_groups;      /* B >= 0 */
+  int32_t num_beams;       /* K: 1 .. GDN_BEAM_MAX */
+  int32_t vocab;           /* V: 1 .. 2^28 */
+  int32_t num_candidates;  /* 1 .. GDN_BEAM_MAX, at most K V */
+  int32_t logits_dtype;    /* F32, BF16 or F16 */
+  const void *logits;      /* [B, K, V] */
+  int64_t logits_stride;   /* elements from a beam to the next (0 = contiguous) */
+  const float *scores;     /* [B, K] */
+  float *out_scores;       /* [B, num_candidates] */
+  int32_t *out_parents;    /* beams */
+  int32_t *out_tokens;
+  void *workspace;
+  size_t workspace_bytes;
+} gdn_beam_params;
+
+size_t gdn_beam_workspace_size(const gdn_beam_params *p);
+int gdn_validate_beam_host(const gdn_beam_params *p);
+int gdn_beam_select(const gdn_beam_params *p, void *stream);
+
+/* Brings the rows of state pools in the order of the selected parents.  Beam k
+ * of group b holds row state_indices[b K + k] of every pool, rows all distinct;
+ * child j of the group continues beam parents[b K + j].  The first child of a
+ * parent keeps its row; the other children, in order, take the rows of the
+ * beams without a child, in order, which are overwritten with their parents'
+ * rows; no other row changes.  new_indices [B K] receives the children's rows.
+ * An entry of parents outside [0, K) is no parent: its child takes a row that
+ * is left over, as it is.  Rows outside the pool are handed on and neither read
+ * nor written.  Both set GDN_STATUS_POOL_ROW (-1 does not: padding); a row that
+ * is named twice sets GDN_STATUS_POOL_DUPLICATE, and what it holds afterwards is
+ * unspecified.  Lists are int32 or int64, at most GDN_POOL_MAX_ROWS entries;
+ * new_indices may not overlap them. */
+typedef struct gdn_reorder_pool {
+  void *pool;
+  int32_t dtype;
+  int64_t extent[3];   /* d1, d2, d3 >= 1, as in gdn_pool_params */
+  int64_t strides[4];
+} gdn_reorder_pool;
+
+typedef struct gdn_reorder_params {
+  int32_t num_groups;      /* B >= 0 */
+  int32_t num_beams;       /* K: 1 .. GDN_BEAM_MAX */
+  int32_t num_pools;       /* >= 1; they may share no elements */
+  int64_t pool_rows;       /* rows of every pool */
+  const gdn_reorder_pool *pools; /* host */
+  const void *state_indices;
+  const void *parents;
+  void *new_indices;
+  int32_t index_type;      /* gdn_itype of the three lists */
+  int32_t *status;         /* optional device word */
+} gdn_reorder_params;
+
+int gdn_validate_reorder_host(const gdn_reorder_params *p);
+int gdn_pool_reorder(const gdn_reorder_params *p, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
