@@ -66,8 +66,13 @@ template <typename P> int check_batch(const P *p, int mode, int64_t row) {
   return GDN_OK;
 }
 
+// `part`: elements of a state's rows of channels.
 template <typename P> void fill_batch(const P *p, Batch &b, StateRows &init, StateRows &fin,
-                                      int64_t row) {
+                                      int64_t row, int64_t part) {
+  auto vec = [&](const StateRows &s) {
+    const int64_t es = size_of(s.dtype);
+    return aligned(s.p, 16) && s.stride * es % 16 == 0 && part * es % 16 == 0;
+  };
   b.T = p->total_tokens;
   b.N = p->num_seqs;
   b.cu = p->cu_seqlens;
@@ -79,10 +84,12 @@ template <typename P> void fill_batch(const P *p, Batch &b, StateRows &init, Sta
   init.p = const_cast<void *>(p->initial_state);
   init.dtype = p->initial_state_dtype;
   init.stride = p->initial_state_stride ? p->initial_state_stride : row;
+  init.vec = vec(init);
   if (p->output_final_state) {
     fin.p = p->output_state;
     fin.dtype = p->output_state_dtype;
     fin.stride = p->output_state_stride ? p->output_state_stride : row;
+    fin.vec = vec(fin);
   }
 }
 
@@ -144,8 +151,10 @@ bool rows16(const void *p, int64_t stride, int64_t es) {
 ConvPlan conv_plan(const gdn_convolution_params *p, int mode) {
   ConvPlan L{};
   const int64_t C = p->channels, es = size_of(p->x_dtype), T = p->total_tokens;
-  const int64_t V = 16 / es;
-  L.vec = C % V == 0 && rows16(p->x, p->x_stride, es);
+  const int64_t V = conv_lane(mode, (int)es);
+  // rows of whole 16-byte groups, and a lane's weights too
+  L.vec = C * es % 16 == 0 && rows16(p->x, p->x_stride, es) && aligned(p->weight, 16) &&
+          aligned(p->bias, 16);
   if (mode == kBackward)
     L.vec = L.vec && rows16(p->doutput, p->doutput_stride, es) && aligned(p->dx, 16);
   else
@@ -170,6 +179,7 @@ ConvPlan conv_plan(const gdn_convolution_params *p, int mode) {
 size_t conv_bytes(const gdn_convolution_params *p, int mode) {
   gdn_convolution_params q = *p;
   q.x = q.doutput = q.output = q.dx = nullptr;
+  q.weight = q.bias = nullptr;
   const size_t vec = conv_plan(&q, mode).total;
   q.x = (const void *)1;
   return std::max(vec, conv_plan(&q, mode).total);
@@ -216,7 +226,7 @@ int conv_run(const gdn_convolution_params *p, int mode, hipStream_t s) {
   ConvArgs a;
   std::memset(&a, 0, sizeof(a));
   const int64_t C = p->channels;
-  fill_batch(p, a.b, a.init, a.fin, (p->width - 1) * C);
+  fill_batch(p, a.b, a.init, a.fin, (p->width - 1) * C, C);
   a.C = p->channels;
   a.W = p->width;
   a.x_dtype = p->x_dtype;
@@ -239,6 +249,7 @@ int conv_run(const gdn_convolution_params *p, int mode, hipStream_t s) {
   a.ncb = L.ncb;
   a.vec = L.vec;
   a.num_cus = num_cus;
+  a.fvec = C % 4 == 0 && aligned(p->dfinal_state, 16) && aligned(p->dinitial_state, 16);
   if (mode == kBackward) a.part = (float *)(ws + L.part);
   hipError_t e = hipSuccess;
   if (mode == kDecode) {
@@ -392,7 +403,7 @@ int scan_run(const gdn_scan_params *p, int mode, hipStream_t s) {
   ScanArgs a;
   std::memset(&a, 0, sizeof(a));
   const int64_t C = p->channels, bn = (int64_t)p->groups * p->num_states;
-  fill_batch(p, a.b, a.init, a.fin, C * p->num_states);
+  fill_batch(p, a.b, a.init, a.fin, C * p->num_states, C * p->num_states);
   a.C = p->channels;
   a.N = p->num_states;
   a.G = p->groups;
@@ -418,6 +429,9 @@ int scan_run(const gdn_scan_params *p, int mode, hipStream_t s) {
   hipError_t e = hipSuccess;
   auto result = [&]() { return e == hipSuccess ? GDN_OK : GDN_ERR_LAUNCH; };
   if (mode == kDecode) {
+    const int64_t es = size_of(p->x_dtype);
+    a.vec = p->num_states % 4 == 0 && aligned(p->A, 16) && aligned(p->B, 4 * es) &&
+            aligned(p->C, 4 * es) && a.b_stride % 4 == 0 && a.c_stride % 4 == 0;
     if (a.b.N > 0 || a.b.status) e = launch_scan_decode(a, s);
     return result();
   }

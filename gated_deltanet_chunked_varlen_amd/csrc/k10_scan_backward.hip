@@ -31,14 +31,17 @@ constexpr int kBlock = 16;
 constexpr int kPart = 4;  // tokens whose raw values are held at once
 
 // Gradients of the empty sequences' initial states: those of their final states.
-__device__ __forceinline__ void empty_sequences(const ScanArgs &a, int part) {
+// A row of workgroups (`slice` of `slices`) takes every a.empties-th sequence.
+__device__ __forceinline__ void empty_sequences(const ScanArgs &a, int part, int slice,
+                                                int slices) {
   const int lane = threadIdx.x & 63;
-  const int64_t row = (int64_t)a.C * a.N;
+  const int64_t row = (int64_t)a.C * a.N, step = (int64_t)slices * kThreads;
   for (int i = part; i < a.b.N; i += a.empties) {
     int bos, len;
     sequence_of(a.b, i, lane, bos, len);
     if (len != 0) continue;
-    for (int64_t e = threadIdx.x; e < row; e += kThreads)
+#pragma unroll 4
+    for (int64_t e = slice * kThreads + threadIdx.x; e < row; e += step)
       a.dinit[i * row + e] = a.dfin ? a.dfin[i * row + e] : 0.f;
   }
 }
@@ -176,7 +179,8 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs a) 
   const int tile = blockIdx.x / ncw, t0 = tile * a.L;
   if (blockIdx.x == 0 && wave == 0 && a.b.status && !a.b.bos) batch_status(a.b, lane);
   if (tile >= a.ntiles) {
-    if (blockIdx.x % ncw == 0 && tile - a.ntiles < a.empties) empty_sequences(a, tile - a.ntiles);
+    if (tile - a.ntiles < a.empties)
+      empty_sequences(a, tile - a.ntiles, blockIdx.x % ncw, ncw);
     return;
   }
   tile_geometry(a, t0, G);
@@ -185,9 +189,10 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs a) 
   const Channel ch(a, cb, lane);
   const unsigned c4 = (unsigned)ch.c * 4;
   const int c = ch.c, end = (int)a.b.T - 1, blocks = a.L / kBlock;
-  // this wave's LDS: states before blocks 1 .., gradient and dA of each state
-  float *const st = lds + (int64_t)wave * (blocks + 1) * NS * 64 + lane;
-  float *const gs = st + (int64_t)(blocks - 1) * NS * 64, *const as = gs + NS * 64;
+  // this wave's LDS: the states before blocks 1 .. (once used, the gradients behind
+  // the block before), and dA of each state
+  float *const st = lds + (int64_t)wave * blocks * NS * 64 + lane;
+  float *const as = st + (int64_t)(blocks - 1) * NS * 64;
   const float bias = a.dbias ? a.dbias[c] : 0.f, D = a.D ? a.D[c] : 0.f;
   const int64_t row = (int64_t)tile * a.N * a.C;
   const bool chained = a.ntiles > 1;
@@ -271,8 +276,11 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs a) 
         const f32x16 bb = uniform_load<f32x16>(a.bct + at);
         const f32x16 cc = uniform_load<f32x16>(a.bct + at + (int64_t)NS * a.Tp);
         float h = blk > 0 ? st[((blk - 1) * NS + n) * 64]
-                          : chained ? *lane_of<float>(a.chunk, row + (int64_t)n * a.C, c4) : 0.f;
-        float g = !newest ? gs[n * 64] : chained ? *lane_of<float>(a.gchunk, row + (int64_t)n * a.C, c4) : 0.f;
+                  : chained ? *lane_of<float>(a.chunk, row + (int64_t)n * a.C, c4)
+                            : 0.f;
+        float g = !newest ? st[(blk * NS + n) * 64]
+                  : chained ? *lane_of<float>(a.gchunk, row + (int64_t)n * a.C, c4)
+                            : 0.f;
         float e[kBlock], before[kBlock], v[2 * kBlock];
 #pragma unroll
         for (int i = 0; i < kBlock; ++i) {
@@ -306,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs a) 
           if (!PLAIN && a.dinit && ch.ok && (m.first >> i & 1))
             a.dinit[((int64_t)m.seq_at(i) * a.C + c) * a.N + n] = g;
         }
-        gs[n * 64] = g;
+        if (blk > 0) st[((blk - 1) * NS + n) * 64] = g;
         as[n * 64] = newest ? dA : as[n * 64] + dA;
         if (!ch.ok) {
 #pragma unroll
@@ -417,8 +425,8 @@ template <typename Tx, int NS> struct Backward {
       if (e != hipSuccess) return e;
     }
     static std::atomic<uint64_t> done{0};
-    const int lds = kWaves * (a.L / kBlock + 1) * NS * 64 * (int)sizeof(float);
-    e = set_dynamic_lds((const void *)scan_backward_kernel<Tx, NS>, 148 << 10, done);
+    const int lds = kWaves * (a.L / kBlock) * NS * 64 * (int)sizeof(float);
+    e = set_dynamic_lds((const void *)scan_backward_kernel<Tx, NS>, 96 << 10, done);
     if (e != hipSuccess) return e;
     scan_backward_kernel<Tx, NS><<<dim3(tile_grid(a, a.empties)), dim3(kThreads), lds, s>>>(a);
     e = hipGetLastError();

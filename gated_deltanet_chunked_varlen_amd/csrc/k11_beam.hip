@@ -7,11 +7,14 @@
 // (beam, token).  Within a beam the order is that of the logits, so the first
 // kernel reads every row once, cut into parts: a workgroup keeps its part in
 // registers, sums the exponentials relative to the part's largest logit, and
-// finds the part's M largest (logit, token) keys: the M-th largest of the
-// threads' largest keys bounds them from below, at most M threads hold a key at
-// or above it, and these few are ranked by counting.  The second kernel, a
-// workgroup per group, combines the sums (in fp64: scores of different beams
-// are compared) and takes the M best of the parts' candidates in the same way.
+// finds the part's M largest (logit, token) keys.  The smallest of the largest
+// logits of 16 (or 64) groups of threads is a bound that at least 16 (64) logits
+// reach, usually some 50 of 8192, which are ranked by counting; where more than
+// kPass reach it (ties, masked rows) the bound is taken from whole keys, which
+// are all different: at most M threads hold one at or above the M-th largest of
+// the threads' largest.  The second kernel, a workgroup per group, joins the sums
+// (in fp64: scores of different beams are compared) and takes the M best of the
+// parts' candidates in the same way.
 // Bounded by HBM for a batch (the logits), by latency for one request.
 //
 // Reordering.  Within a group the first child of a parent keeps its row; the
@@ -93,16 +96,42 @@ template <typename Key, int E, int M> struct Largest {
   }
 };
 
-__device__ __forceinline__ float wave_max(float x) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor(x, o));
-  return x;
-}
 __device__ __forceinline__ double wave_sum(double x) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o);
   return x;
 }
+
+// Candidates that pass a bound, ranked by counting; more of them are left to
+// Largest.
+constexpr int kPass = 512;
+
+// Lanes of one of the groups whose largest keys' smallest one is the bound: at
+// least M groups of the workgroup's 256 threads, so that at least M keys reach it.
+constexpr int group_lanes(int M) { return M <= 16 ? 16 : 4; }
+
+template <typename T> __device__ __forceinline__ T group_max(T x, int lanes) {
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    if (o >= lanes) break;
+    const T y = __shfl_xor(x, o);
+    x = y > x ? y : x;
+  }
+  return x;
+}
+template <typename T> __device__ __forceinline__ T wave_min(T x) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    const T y = __shfl_xor(x, o);
+    x = y < x ? y : x;
+  }
+  return x;
+}
+
+template <typename Key> struct Pass {
+  Key key[kPass];
+  unsigned count;
+};
 
 // A part of one row, E logits per thread.  VEC: rows are whole aligned groups of
 // 16 bytes.
@@ -110,62 +139,110 @@ template <typename T, int E, int M, bool VEC>
 __global__ void __launch_bounds__(kThreads) beam_rows_kernel(BeamArgs a) {
   constexpr int V = VEC ? 16 / (int)sizeof(T) : 1;
   constexpr int S = E / V;  // vectors per thread
-  __shared__ Largest<u64, E, M> L;
-  __shared__ float s_max[kThreads / 64];
-  __shared__ double s_sum[kThreads / 64];
+  constexpr int kWaves = kThreads / 64;
+  __shared__ union {
+    Largest<u64, E, M> all;
+    Pass<u64> pass;
+  } L;
+  __shared__ float s_top[kWaves], s_low[kWaves];
+  __shared__ double s_sum[kWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int row = blockIdx.x / a.parts, part = blockIdx.x % a.parts;
   const int from = part * a.part_len, to = min(from + a.part_len, a.V);
+  const int64_t o = (int64_t)blockIdx.x;
+  if (!(a.scores[row] > -kInf)) {
+    // a beam that has ended: its continuations are all alike
+    if (tid < a.M) {
+      a.best[o * a.M + tid] = -kInf;
+      a.where[o * a.M + tid] = from + tid < to ? from + tid : -1;
+    }
+    if (tid == 0) {
+      a.stat[2 * o] = -kInf;
+      a.stat[2 * o + 1] = 0.f;
+    }
+    return;
+  }
   const T *p = (const T *)a.logits + (int64_t)row * a.stride;
-  const bool live = a.scores[row] > -kInf;
   float x[E];
 #pragma unroll
   for (int s = 0; s < S; ++s) {
     const int at = from + (s * kThreads + tid) * V;
-    float o[V];
+    float v[V];
     if (at < to) {
-      widen(load_vec<T, V>(p + at), o);
+      widen(load_vec<T, V>(p + at), v);
     } else {
 #pragma unroll
-      for (int e = 0; e < V; ++e) o[e] = -kInf;
+      for (int e = 0; e < V; ++e) v[e] = -kInf;
     }
 #pragma unroll
-    for (int e = 0; e < V; ++e) x[s * V + e] = o[e] == o[e] ? o[e] : -kInf;  // NaN: never taken
+    for (int e = 0; e < V; ++e) x[s * V + e] = fmaxf(v[e], -kInf);  // NaN: never taken
   }
-  float top = -kInf;
+  if (tid == 0) L.pass.count = 0;
+  float mine = -kInf;
 #pragma unroll
-  for (int e = 0; e < E; ++e) top = fmaxf(top, x[e]);
-  top = wave_max(top);
-  if (lane == 0) s_max[wave] = top;
+  for (int e = 0; e < E; ++e) mine = fmaxf(mine, x[e]);
+  const float of_group = group_max(mine, group_lanes(M));
+  const float of_wave = group_max(of_group, 64), low = wave_min(of_group);
+  if (lane == 0) {
+    s_top[wave] = of_wave;
+    s_low[wave] = low;
+  }
   __syncthreads();
-  top = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
-  // relative to the largest one, which counts 1 also where it is infinite
+  const float top = fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3]));
+  const float bound = fminf(fminf(s_low[0], s_low[1]), fminf(s_low[2], s_low[3]));
+  // sum of exponentials relative to the largest logit (of infinite ones each
+  // counts 1, and nothing else does)
   float sum = 0.f;
+  if (fabsf(top) < kInf) {
 #pragma unroll
-  for (int e = 0; e < E; ++e)
-    sum += x[e] == top ? 1.f : __builtin_amdgcn_exp2f(kLog2E * (x[e] - top));
-  const double all = wave_sum(top == -kInf ? 0.0 : (double)sum);
-  if (lane == 0) s_sum[wave] = all;
-  u64 k[E];
+    for (int e = 0; e < E; ++e) sum += __builtin_amdgcn_exp2f(kLog2E * (x[e] - top));
+  } else if (top > 0.f) {
 #pragma unroll
-  for (int s = 0; s < S; ++s)
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const int at = from + (s * kThreads + tid) * V + e;
-      // the continuations of a beam that has ended are all alike
-      k[s * V + e] = at < to ? key_of(live ? x[s * V + e] : -kInf, (unsigned)at) : 0;
-    }
-  L.find(k, a.M);
-  const int64_t o = (int64_t)blockIdx.x;
-  if (tid < a.M) {
-    const u64 b = L.best[tid];
-    a.best[o * a.M + tid] = b ? key_value(b) : -kInf;
-    a.where[o * a.M + tid] = b ? (int)key_place(b) : -1;
+    for (int e = 0; e < E; ++e) sum += x[e] == top ? 1.f : 0.f;
   }
+  const double all = wave_sum((double)sum);
+  if (lane == 0) s_sum[wave] = all;
+  auto place = [&](int k) { return from + (k / V * kThreads + tid) * V + k % V; };
+  if (mine >= bound) {
+    unsigned n = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) n += x[e] >= bound && place(e) < to;
+    if (n > 0) {
+      unsigned at = atomicAdd(&L.pass.count, n);
+      if (at + n <= kPass) {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (x[e] >= bound && place(e) < to) L.pass.key[at++] = key_of(x[e], (unsigned)place(e));
+      }
+    }
+  }
+  __syncthreads();
+  const int n = (int)L.pass.count;
   if (tid == 0) {
     a.stat[2 * o] = top;
     a.stat[2 * o + 1] = (float)((s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3]));
   }
+  auto put = [&](int r, u64 b) {
+    a.best[o * a.M + r] = b ? key_value(b) : -kInf;
+    a.where[o * a.M + r] = b ? (int)key_place(b) : -1;
+  };
+  if (n <= kPass) {
+    for (int i = tid; i < n; i += kThreads) {
+      const u64 k = L.pass.key[i];
+      int r = 0;
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) r += L.pass.key[j] > k;
+      if (r < a.M) put(r, k);
+    }
+    if (tid >= n && tid < a.M) put(tid, 0);  // fewer tokens than places
+    return;
+  }
+  __syncthreads();
+  u64 k[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) k[e] = place(e) < to ? key_of(x[e], (unsigned)place(e)) : 0;
+  L.all.find(k, a.M);
+  if (tid < a.M) put(tid, L.all.best[tid]);
 }
 
 // A score in fp64, in the order of whole numbers, and (beam, token) descending.
@@ -185,61 +262,129 @@ __device__ __forceinline__ double value_of(u64 o) {
 
 constexpr int kTake = 8;  // candidates per thread and round
 
+// One group.  Candidates come in rounds of kTake a thread; those of a round that
+// reach its bound, with the best so far, are ranked by counting.
 template <int M> __global__ void __launch_bounds__(kThreads) beam_group_kernel(BeamArgs a) {
-  __shared__ Largest<Score, kTake + 1, M> L;
+  constexpr int kWaves = kThreads / 64;
+  __shared__ union {
+    Largest<Score, kTake + 1, M> all;
+    Pass<Score> pass;
+  } L;
+  __shared__ Score s_best[M];
   __shared__ double s_log[kMaxM];
-  __shared__ float s_top[kMaxM];
+  __shared__ u64 s_low[kWaves];
+  __shared__ float s_top[kMaxM], s_score[kMaxM];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, b = blockIdx.x;
-  const int per = a.parts * a.M;
-  const int64_t first = (int64_t)b * a.K * a.parts, n = (int64_t)a.K * per;
-  for (int k = wave; k < a.K; k += kThreads / 64) {
+  const int per = a.parts * a.M, n = a.K * per;
+  const int64_t first = (int64_t)b * a.K * a.parts;
+  // the first round's candidates are on their way while the sums are joined
+  int at[kTake];
+  float logit[kTake];
+  auto fetch = [&](int base) {
+#pragma unroll
+    for (int e = 0; e < kTake; ++e) {
+      const int i = base + e * kThreads + tid;
+      at[e] = i < n ? a.where[first * a.M + i] : -1;
+      logit[e] = i < n ? a.best[first * a.M + i] : 0.f;
+    }
+  };
+  fetch(0);
+  for (int k = wave; k < a.K; k += kWaves) {
     const float *st = a.stat + 2 * (first + (int64_t)k * a.parts);
-    float top = -kInf;
+    const float score = a.scores[(int64_t)b * a.K + k];
+    float top = -kInf, own = lane < a.parts ? st[2 * lane] : -kInf;
+    const float part = lane < a.parts ? st[2 * lane + 1] : 0.f;
     for (int i = lane; i < a.parts; i += 64) top = fmaxf(top, st[2 * i]);
-    top = wave_max(top);
-    double sum = 0.0;
-    for (int i = lane; i < a.parts; i += 64) {
-      const double own = st[2 * i + 1];
-      sum += st[2 * i] == top ? own : own * exp((double)st[2 * i] - (double)top);
+    top = group_max(top, 64);
+    double sum = own == top ? (double)part : (double)part * exp((double)own - (double)top);
+    for (int i = lane + 64; i < a.parts; i += 64) {
+      own = st[2 * i];
+      sum += own == top ? (double)st[2 * i + 1]
+                        : (double)st[2 * i + 1] * exp((double)own - (double)top);
     }
     sum = wave_sum(sum);
     if (lane == 0) {
       s_top[k] = top;
+      s_score[k] = score;
       s_log[k] = log(sum);
     }
   }
+  if (tid < M) s_best[tid] = Score{};
   __syncthreads();
-  Score mine{};
-  for (int64_t base = 0; base < n; base += kTake * kThreads) {
+  for (int base = 0; base < n; base += kTake * kThreads) {
     Score c[kTake + 1];
-    bool any = false;
+    if (base > 0) fetch(base);
+    c[kTake] = tid < a.M ? s_best[tid] : Score{};  // the best so far, one a thread
+    const Score last = s_best[a.M - 1];
+    bool any = base == 0;
+    u64 mine = c[kTake].value;
 #pragma unroll
     for (int e = 0; e < kTake; ++e) {
-      const int64_t i = base + e * kThreads + tid;
+      const int i = base + e * kThreads + tid;
       c[e] = Score{};
-      if (i >= n) continue;
-      const int k = (int)(i / per), at = a.where[first * a.M + i];
-      if (at < 0) continue;
-      const float logit = a.best[first * a.M + i], score = a.scores[(int64_t)b * a.K + k];
+      if (at[e] < 0) continue;
+      const int k = i / per;
+      const float score = s_score[k], top = s_top[k];
       double v = -(double)kInf;
       // (of an infinite largest logit the others have no share)
-      if (logit > -kInf && score > -kInf) {
-        const double own = logit == s_top[k] ? 0.0 : (double)logit - (double)s_top[k];
+      if (logit[e] > -kInf && score > -kInf) {
+        const double own = logit[e] == top ? 0.0 : (double)logit[e] - (double)top;
         if (own > -(double)kInf) v = (double)score + (own - s_log[k]);
       }
-      c[e] = Score{order_of(v), ~((u64)k * (u64)a.V + (u64)at)};
-      any |= c[e] > L.best[a.M - 1] || base == 0;
+      c[e] = Score{order_of(v), ~((u64)k * (u64)a.V + (u64)at[e])};
+      any |= c[e] > last;
+      mine = c[e].value > mine ? c[e].value : mine;
     }
     // nothing better than what there is: on to the next ones
     if (!__syncthreads_or(any)) continue;
-    c[kTake] = mine;  // the best so far, one a thread
-    L.find(c, a.M);
-    mine = tid < a.M ? L.best[tid] : Score{};
+    const u64 low = wave_min(group_max(mine, group_lanes(M)));
+    if (lane == 0) s_low[wave] = low;
+    if (tid == 0) L.pass.count = 0;
+    __syncthreads();
+    u64 bound = ~0ull;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const u64 x = s_low[w];
+      bound = x < bound ? x : bound;
+    }
+    bound = bound > 0 ? bound : 1;
+    if (mine >= bound) {
+#pragma unroll
+      for (int e = 0; e <= kTake; ++e)
+        if (c[e].value >= bound) {
+          const unsigned slot = atomicAdd(&L.pass.count, 1u);
+          if (slot < kPass) L.pass.key[slot] = c[e];
+        }
+    }
+    __syncthreads();
+    const int m = (int)L.pass.count;
+    if (m <= kPass) {
+      Score keep[2];
+      int rank[2] = {M, M};
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int i = tid + q * kThreads;
+        if (i >= m) continue;
+        keep[q] = L.pass.key[i];
+        int r = 0;
+        for (int j = 0; j < m; ++j) r += L.pass.key[j] > keep[q];
+        rank[q] = r;
+      }
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        if (rank[q] < a.M) s_best[rank[q]] = keep[q];
+    } else {
+      __syncthreads();
+      L.all.find(c, a.M);
+      if (tid < a.M) s_best[tid] = L.all.best[tid];
+    }
+    __syncthreads();
   }
   if (tid >= a.M) return;
-  const u64 flat = ~mine.place;
+  const Score best = s_best[tid];
+  const u64 flat = ~best.place;
   const int64_t o = (int64_t)b * a.M + tid;
-  a.out_scores[o] = (float)value_of(mine.value);
+  a.out_scores[o] = (float)value_of(best.value);
   a.parents[o] = (int)(flat / (u64)a.V);
   a.tokens[o] = (int)(flat % (u64)a.V);
 }

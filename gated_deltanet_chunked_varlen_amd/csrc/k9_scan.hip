@@ -148,20 +148,30 @@ __device__ __forceinline__ void final_state(const ScanArgs &a, int i, int c, flo
 }
 
 // Final states of the empty sequences, by workgroups behind the tiles': their
-// initial states.
-__device__ __forceinline__ void empty_sequences(const ScanArgs &a, int part) {
+// initial states.  A row of workgroups (`slice` of `slices`) takes every
+// a.empties-th sequence.
+__device__ __forceinline__ void empty_sequences(const ScanArgs &a, int part, int slice,
+                                                int slices) {
+  constexpr int U = 4;
   const int lane = threadIdx.x & 63;
-  const int64_t row = (int64_t)a.C * a.N;
+  const int64_t row = (int64_t)a.C * a.N, step = (int64_t)slices * kThreads;
   for (int i = part; i < a.b.N; i += a.empties) {
     int bos, len;
     sequence_of(a.b, i, lane, bos, len);
-    if (len != 0) continue;
     const int64_t r = state_row(a.b, i);
-    if (r < 0) continue;
-    for (int64_t e = threadIdx.x; e < row; e += kThreads) {
-      float one[1] = {0.f};
-      if (a.init.p) state_read<1>(a.init, r * a.init.stride + e, one);
-      state_write<1>(a.fin, r * a.fin.stride + e, one);
+    if (len != 0 || r < 0) continue;
+    for (int64_t e = slice * kThreads + threadIdx.x; e < row; e += U * step) {
+      int64_t from[U], to[U];
+      float v[U][1];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t at = min(e + u * step, row - 1);
+        from[u] = r * a.init.stride + at;
+        to[u] = r * a.fin.stride + at;
+        v[u][0] = 0.f;
+      }
+      if (a.init.p) state_read<U, 1>(a.init, from, v);
+      state_write<U, 1>(a.fin, to, v);
     }
   }
 }
@@ -180,8 +190,8 @@ __global__ void __launch_bounds__(kThreads, scan_waves(NS)) scan_tile_kernel(Sca
   if (blockIdx.x == 0 && wave == 0 && a.b.status && !a.b.bos && (!OUT || a.ntiles <= 1))
     batch_status(a.b, lane);
   if (tile >= a.ntiles) {
-    if (OUT && blockIdx.x % ncw == 0 && tile - a.ntiles < a.empties)
-      empty_sequences(a, tile - a.ntiles);
+    if (OUT && tile - a.ntiles < a.empties)
+      empty_sequences(a, tile - a.ntiles, blockIdx.x % ncw, ncw);
     return;
   }
   const int t0 = tile * a.L;
@@ -328,56 +338,83 @@ __global__ void __launch_bounds__(kThreads) scan_chain_kernel(ScanArgs a, float 
 
 // --------------------------------------------------------------------- decode
 
-// Q lanes per channel with four states each (N = 4 Q): the state row is read,
-// updated and written once, 16 bytes a lane for fp32 states, and the output is
-// summed over the lanes.  Bounded by memory for a full batch.  Q = 0: one lane
-// per channel, any N.
-template <typename Tx, int Q>
-__global__ void __launch_bounds__(kThreads) scan_decode_kernel(ScanArgs a) {
-  constexpr int S = Q ? Q : 1;
+// Q lanes per channel with four states each (N = 4 Q), U such quarters a thread, a
+// workgroup apart: the state row is read, updated and written once, 16 bytes a
+// lane for fp32 states, and the output is summed over the lanes.  Bounded by
+// memory for a full batch.
+template <typename Tx, int Q, int U>
+__global__ void __launch_bounds__(kThreads) scan_decode_kernel(ScanArgs a, int blocks) {
   if (blockIdx.x == 0 && a.b.status) decode_status(a.b);
-  const int64_t per = (int64_t)a.C * S;
-  const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  const bool on = id < per * a.b.N;
-  const int i = on ? (int)(id / per) : 0;
-  const int64_t at = on ? id % per : 0;
-  const int c = (int)(at / S), q = (int)(at % S);
-  const int64_t r = on ? state_row(a.b, i) : -1;
-  float x = 0.f, dt = 0.f, y = 0.f;
-  if (on) {
-    x = to_f32(((const Tx *)a.x)[i * a.x_stride + c]);
-    dt = step_size(a, to_f32(((const Tx *)a.delta)[i * a.delta_stride + c]) +
-                          (a.dbias ? a.dbias[c] : 0.f));
-    const float u = dt * x;
-    const int64_t bn = (int64_t)(c / a.P) * a.N;
-    const Tx *B = (const Tx *)a.B + i * a.b_stride + bn, *C = (const Tx *)a.C_ + i * a.c_stride + bn;
-    const float *A = a.A + (int64_t)c * a.N;
-    const int64_t off = (int64_t)c * a.N;
-    if constexpr (Q > 0) {
-      float h[4] = {0.f, 0.f, 0.f, 0.f}, Av[4], Bv[4], Cv[4];
-      if (a.init.p && r >= 0) state_read<4>(a.init, r * a.init.stride + off + 4 * q, h);
-      row_load<float, 4>(A, 4 * q, Av);
-      row_load<Tx, 4>(B, 4 * q, Bv);
-      row_load<Tx, 4>(C, 4 * q, Cv);
+  if (a.b.N == 0) return;
+  const int i = blockIdx.x / blocks;
+  const int per = a.C * Q, first = (int)(blockIdx.x % blocks) * (U * kThreads) + threadIdx.x;
+  const int64_t r = state_row(a.b, i);
+  float h[U][4], Av[U][4], Bv[U][4], Cv[U][4], x[U], d[U], z[U], D[U];
+  int64_t on_a[U], on_b[U], on_h[U];
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        h[n] = fmaf(__builtin_amdgcn_exp2f(dt * (kLog2E * Av[n])), h[n], u * Bv[n]);
-        y = fmaf(Cv[n], h[n], y);
-      }
-      if (a.fin.p && r >= 0) state_write<4>(a.fin, r * a.fin.stride + off + 4 * q, h);
-    } else {
-      for (int n = 0; n < a.N; ++n) {
-        float h[1] = {0.f};
-        if (a.init.p && r >= 0) state_read<1>(a.init, r * a.init.stride + off + n, h);
-        h[0] = fmaf(__builtin_amdgcn_exp2f(dt * (kLog2E * A[n])), h[0], u * to_f32(B[n]));
-        y = fmaf(to_f32(C[n]), h[0], y);
-        if (a.fin.p && r >= 0) state_write<1>(a.fin, r * a.fin.stride + off + n, h);
-      }
-    }
+  for (int k = 0; k < U; ++k) {
+    const int at = min(first + k * kThreads, per - 1), c = at / Q, q = at % Q;
+    on_a[k] = 4 * at;
+    on_b[k] = (int64_t)(c / a.P) * a.N + 4 * q;
+    on_h[k] = r * a.init.stride + 4 * at;
+#pragma unroll
+    for (int n = 0; n < 4; ++n) h[k][n] = 0.f;
+    x[k] = to_f32(((const Tx *)a.x)[i * a.x_stride + c]);
+    d[k] = to_f32(((const Tx *)a.delta)[i * a.delta_stride + c]) + (a.dbias ? a.dbias[c] : 0.f);
+    z[k] = a.z ? to_f32(((const Tx *)a.z)[i * a.z_stride + c]) : 0.f;
+    D[k] = a.D ? a.D[c] : 0.f;
   }
+  rows_load<float, U, 4>(a.A, a.vec, on_a, Av);
+  rows_load<Tx, U, 4>((const Tx *)a.B + i * a.b_stride, a.vec, on_b, Bv);
+  rows_load<Tx, U, 4>((const Tx *)a.C_ + i * a.c_stride, a.vec, on_b, Cv);
+  if (a.init.p && r >= 0) state_read<U, 4>(a.init, on_h, h);
 #pragma unroll
-  for (int o = 1; o < S; o <<= 1) y += __shfl_xor(y, o);
-  if (!on || q != 0) return;
+  for (int k = 0; k < U; ++k) {
+    const int at = first + k * kThreads;
+    const bool on = at < per;
+    const float dt = step_size(a, d[k]), u = dt * x[k];
+    float y = 0.f;
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      h[k][n] = fmaf(__builtin_amdgcn_exp2f(dt * (kLog2E * Av[k][n])), h[k][n], u * Bv[k][n]);
+      y = fmaf(Cv[k][n], h[k][n], y);
+    }
+    if (a.fin.p && r >= 0 && on) {
+      const int64_t to[1] = {r * a.fin.stride + 4 * at};
+      const float(&row)[1][4] = reinterpret_cast<const float(&)[1][4]>(h[k]);
+      state_write<1, 4>(a.fin, to, row);
+    }
+#pragma unroll
+    for (int o = 1; o < Q; o <<= 1) y += __shfl_xor(y, o);
+    if (!on || at % Q != 0) continue;
+    y = fmaf(D[k], x[k], y);
+    if (a.z) y *= z[k] * sigmoid(z[k]);
+    ((Tx *)a.out)[(int64_t)i * a.C + at / Q] = from_f32<Tx>(y);
+  }
+}
+
+// Any N: one lane per channel.
+template <typename Tx>
+__global__ void __launch_bounds__(kThreads) scan_decode_any_kernel(ScanArgs a, int blocks) {
+  if (blockIdx.x == 0 && a.b.status) decode_status(a.b);
+  if (a.b.N == 0) return;
+  const int i = blockIdx.x / blocks, c = (int)(blockIdx.x % blocks) * kThreads + threadIdx.x;
+  if (c >= a.C) return;
+  const int64_t r = state_row(a.b, i), off = (int64_t)c * a.N, bn = (int64_t)(c / a.P) * a.N;
+  const float x = to_f32(((const Tx *)a.x)[i * a.x_stride + c]);
+  const float dt = step_size(a, to_f32(((const Tx *)a.delta)[i * a.delta_stride + c]) +
+                                    (a.dbias ? a.dbias[c] : 0.f));
+  const float u = dt * x;
+  const Tx *B = (const Tx *)a.B + i * a.b_stride + bn, *C = (const Tx *)a.C_ + i * a.c_stride + bn;
+  float y = 0.f;
+  for (int n = 0; n < a.N; ++n) {
+    float h[1][1] = {{0.f}};
+    const int64_t from[1] = {r * a.init.stride + off + n}, to[1] = {r * a.fin.stride + off + n};
+    if (a.init.p && r >= 0) state_read<1, 1>(a.init, from, h);
+    h[0][0] = fmaf(__builtin_amdgcn_exp2f(dt * (kLog2E * a.A[off + n])), h[0][0], u * to_f32(B[n]));
+    y = fmaf(to_f32(C[n]), h[0][0], y);
+    if (a.fin.p && r >= 0) state_write<1, 1>(a.fin, to, h);
+  }
   y = fmaf(a.D ? a.D[c] : 0.f, x, y);
   if (a.z) {
     const float z = to_f32(((const Tx *)a.z)[i * a.z_stride + c]);
@@ -409,16 +446,33 @@ template <typename Tx> hipError_t prepare(const ScanArgs &a, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <typename Tx, int Q> hipError_t decode_by(const ScanArgs &a, hipStream_t s) {
+  // four quarters a thread where that leaves two workgroups per CU
+  constexpr int U = 4;
+  const int64_t per = (int64_t)a.C * Q, n = std::max<int64_t>(a.b.N, 1);
+  const int64_t long_ = (per + U * kThreads - 1) / (U * kThreads);
+  if (long_ * n >= 2 * (int64_t)a.num_cus) {
+    scan_decode_kernel<Tx, Q, U>
+        <<<dim3((unsigned)(long_ * n)), dim3(kThreads), 0, s>>>(a, (int)long_);
+  } else {
+    const int64_t blocks = (per + kThreads - 1) / kThreads;
+    scan_decode_kernel<Tx, Q, 1>
+        <<<dim3((unsigned)(blocks * n)), dim3(kThreads), 0, s>>>(a, (int)blocks);
+  }
+  return hipGetLastError();
+}
 template <typename Tx> hipError_t decode(const ScanArgs &a, hipStream_t s) {
-  const int q = a.N == 4 ? 1 : a.N == 8 ? 2 : a.N == 16 ? 4 : a.N == 32 ? 8 : a.N == 64 ? 16 : 0;
-  const int64_t n = (int64_t)a.b.N * a.C * (q ? q : 1);
-  const dim3 grid((unsigned)(n > 0 ? (n + kThreads - 1) / kThreads : 1)), block(kThreads);
-  if (q == 1) scan_decode_kernel<Tx, 1><<<grid, block, 0, s>>>(a);
-  else if (q == 2) scan_decode_kernel<Tx, 2><<<grid, block, 0, s>>>(a);
-  else if (q == 4) scan_decode_kernel<Tx, 4><<<grid, block, 0, s>>>(a);
-  else if (q == 8) scan_decode_kernel<Tx, 8><<<grid, block, 0, s>>>(a);
-  else if (q == 16) scan_decode_kernel<Tx, 16><<<grid, block, 0, s>>>(a);
-  else scan_decode_kernel<Tx, 0><<<grid, block, 0, s>>>(a);
+  switch (a.N) {
+    case 4: return decode_by<Tx, 1>(a, s);
+    case 8: return decode_by<Tx, 2>(a, s);
+    case 16: return decode_by<Tx, 4>(a, s);
+    case 32: return decode_by<Tx, 8>(a, s);
+    case 64: return decode_by<Tx, 16>(a, s);
+    default: break;
+  }
+  const int64_t blocks = (a.C + kThreads - 1) / kThreads, n = std::max<int64_t>(a.b.N, 1);
+  scan_decode_any_kernel<Tx>
+      <<<dim3((unsigned)(blocks * n)), dim3(kThreads), 0, s>>>(a, (int)blocks);
   return hipGetLastError();
 }
 
