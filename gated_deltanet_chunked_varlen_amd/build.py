@@ -21,7 +21,7 @@ SOURCES = ["gdn_host.hip", "k0_chunk_index.hip", "k1_intra.hip",
            "k2_state.hip", "k3_output.hip", "k4_decode.hip", "k5_cp.hip",
            "gdn_recurrence_host.hip", "k6_recurrence.hip", "k7_pool.hip",
            "gdn_layers_host.hip", "k8_convolution.hip", "k9_scan.hip", "k10_scan_backward.hip",
-           "k11_beam.hip"]
+           "k11_beam.hip", "k12_scan_walk.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

@@ -80,6 +80,8 @@ struct ScanArgs {
   StateRows init, fin;
   // tiles of L tokens and what a pass leaves for the next one
   int32_t L, ntiles, empties;
+  int32_t near;   // walk: a run's tokens lie within 2^30 bytes of its first one
+  int32_t nseg;   // segments of the tokens that workgroups walk along (k12_scan_walk.hip)
   float *bc;      // [T][G][2][NS] B and C in fp32, padded with zeros
   float *chunk;   // [ntiles][N][C] first each tile's own state, then the state before it
   float *span;    // [ntiles][C] sum of the step sizes over which a state crosses the tile
@@ -99,7 +101,7 @@ struct ScanArgs {
   int64_t Tp;
   float *psum;    // [ntiles][N + 2][C] sums of dA, dD and ddelta_bias over a tile
   float *pbc;     // [ncb][2][NS][Tp] sums of dB and dC over a block of channels
-  int32_t vec;    // decode: four states of A, B and C are aligned vectors
+  int32_t vec;    // decode: four states of A, B and C are aligned vectors; walk: eight of B and C
   int32_t num_cus;
 };
 
@@ -110,6 +112,7 @@ hipError_t launch_scan_prepare(const ScanArgs &a, hipStream_t s);
 hipError_t launch_scan_states(const ScanArgs &a, hipStream_t s);
 hipError_t launch_scan_chain(const ScanArgs &a, bool backward, hipStream_t s);
 hipError_t launch_scan_forward(const ScanArgs &a, hipStream_t s);
+hipError_t launch_scan_walk(const ScanArgs &a, hipStream_t s);
 hipError_t launch_scan_backward(const ScanArgs &a, hipStream_t s);
 hipError_t launch_scan_decode(const ScanArgs &a, hipStream_t s);
 
@@ -189,10 +192,14 @@ __device__ __forceinline__ void widen(const Vec<T, V> &v, float (&o)[V]) {
 }
 template <typename T, int V>
 __device__ __forceinline__ void store_vec(T *p, const float (&o)[V]) {
-  Vec<T, V> v;
+  constexpr int Q = sizeof(T) * V <= 16 ? V : 16 / (int)sizeof(T);
 #pragma unroll
-  for (int e = 0; e < V; ++e) v.e[e] = from_f32<T>(o[e]);
-  *reinterpret_cast<Vec<T, V> *>(p) = v;
+  for (int q = 0; q < V; q += Q) {
+    Vec<T, Q> v;
+#pragma unroll
+    for (int e = 0; e < Q; ++e) v.e[e] = from_f32<T>(o[q + e]);
+    *reinterpret_cast<Vec<T, Q> *>(p + q) = v;
+  }
 }
 
 // V elements at each of R offsets, all loads on their way before the first is
@@ -291,10 +298,12 @@ struct Block64 {
 };
 
 // Sequence i of the batch: first token and length, inside [0, T] whatever the
-// workspace holds.  For the whole wave.
-__device__ __forceinline__ void sequence_of(const Batch &b, int i, int lane, int &bos, int &len) {
+// workspace holds.  For the whole wave; `pre`: the lanes' sequences of a small
+// batch, where the caller holds them.
+__device__ __forceinline__ void sequence_of(const Batch &b, int i, int lane, int &bos, int &len,
+                                            const SeqLane *pre = nullptr) {
   if (!b.bos) {
-    const SeqLane s = seq_lane(b.cu, b.cu_type, b.N, b.T, lane);
+    const SeqLane s = pre ? *pre : seq_lane(b.cu, b.cu_type, b.N, b.T, lane);
     bos = __builtin_amdgcn_readlane(s.bos, i);
     len = __builtin_amdgcn_readlane(s.len, i);
     return;
@@ -335,15 +344,16 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// `mark`: 64 words of LDS of this wave's own.  Every lane calls it.
-__device__ __forceinline__ Block64 block_geometry(const Batch &b, int t0, int lane, int *mark) {
+// `mark`: 64 words of LDS of this wave's own.  Every lane calls it; `pre` as above.
+__device__ __forceinline__ Block64 block_geometry(const Batch &b, int t0, int lane, int *mark,
+                                                  const SeqLane *pre = nullptr) {
   Block64 g;
   mark[lane] = -1;
   wave_sync();
   int covering;  // the sequence of token t0, if an earlier token starts it
   SeqLane s;
   if (!b.bos) {
-    s = seq_lane(b.cu, b.cu_type, b.N, b.T, lane);
+    s = pre ? *pre : seq_lane(b.cu, b.cu_type, b.N, b.T, lane);
     const bool some = lane < b.N && s.len > 0;
     const unsigned long long m = __ballot(some && s.bos < t0 && s.bos + s.len > t0);
     covering = m ? 63 - __builtin_clzll(m) : -1;

@@ -276,9 +276,38 @@ int64_t scan_tile(const gdn_scan_params *p, bool backward) {
   const int64_t waves = p->total_tokens * scan_blocks(p);
   int64_t most = 256;
   if (backward) most = p->num_states <= 16 ? 64 : p->num_states <= 32 ? 32 : 16;
+  // (whole runs of the walk, k12_scan_walk.hip, which leaves chunk_states too)
   int64_t L = 16;
   while (L < most && waves / (2 * L) >= 4096) L *= 2;
   return L;
+}
+
+// The forward pass that walks along the tokens, 16 channels a workgroup, and how
+// many segments of them: a walk takes 9 us per 256 tokens of 16 states however many
+// workgroups there are (up to one per CU), the passes over tiles some 35 us and 12
+// per 256 tokens of 4096 channels.
+int64_t walk_blocks(const gdn_scan_params *p) {
+  return (int64_t)p->groups * ((p->channels / p->groups + 15) / 16);
+}
+// (It takes 8, 16, 32 or 64 states, in aligned fp32 rows, and aligned B and C.)
+int scan_walks(const gdn_scan_params *p) {
+  const int64_t xs = size_of(p->x_dtype);
+  auto states_ok = [&](const void *q, int dtype, int64_t stride) {
+    return !q || (dtype == GDN_F32 && aligned(q, 16) && stride % 4 == 0);
+  };
+  if (p->num_states != scan_states(p->num_states) || !rows16(p->B, p->b_stride, xs) ||
+      !rows16(p->C, p->c_stride, xs) || !aligned(p->A, 4) || p->channels > (1 << 23) ||
+      !states_ok(p->initial_state, p->initial_state_dtype, p->initial_state_stride) ||
+      (p->output_final_state &&
+       !states_ok(p->output_state, p->output_state_dtype, p->output_state_stride)))
+    return 0;
+  const int64_t steps = (p->total_tokens + 255) / 256, n = scan_states(p->num_states);
+  // us, times 16 states and 4096 channels
+  const int64_t walk = 9 * steps * n * 4096;
+  const int64_t tiles = 35 * 16 * 4096 + 12 * steps * n * 64 * scan_blocks(p);
+  if (p->total_tokens == 0 || walk > tiles) return 0;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(256 / walk_blocks(p),
+                                                     std::min<int64_t>(p->num_seqs, steps)));
 }
 
 int scan_shape(const gdn_scan_params *p, int mode) {
@@ -295,6 +324,7 @@ int scan_shape(const gdn_scan_params *p, int mode) {
     if (C * p->num_states * (int64_t)p->num_seqs > kMaxGrid * 256) return GDN_ERR_SHAPE;
     return GDN_OK;
   }
+  if (T > 0 && (walk_blocks(p) + 8) * (16 + 64) > kMaxGrid / 4) return GDN_ERR_SHAPE;
   if (T > 0 && ((T + 15) / 16 + 64) * ((scan_blocks(p) + 3) / 4) > kMaxGrid) return GDN_ERR_SHAPE;
   const int64_t rows = (int64_t)p->groups * 2 * scan_states(p->num_states);
   if (((T + 255) / 256 * 256) * rows > kMaxGrid * 256) return GDN_ERR_SHAPE;
@@ -305,6 +335,7 @@ struct ScanPlan {
   int64_t L, ntiles, Tp;
   size_t bos, bc, a2, chunk, span, flag, start, bct, gchunk, gspan, gflag, psum, pbc, total;
   bool own_chunk;
+  int walk;  // segments of the walk, 0: passes over tiles
 };
 
 ScanPlan scan_plan(const gdn_scan_params *p, int mode) {
@@ -315,6 +346,7 @@ ScanPlan scan_plan(const gdn_scan_params *p, int mode) {
   S.ntiles = (T + S.L - 1) / S.L;
   S.Tp = S.ntiles * S.L;
   S.own_chunk = S.ntiles > 1 && !p->chunk_states;
+  S.walk = back ? 0 : scan_walks(p);
   Taker take;
   if (p->num_seqs > kDirectSeqs) S.bos = take(4 * ((size_t)p->num_seqs + 1));
   S.bc = take(4 * (size_t)T * p->groups * 2 * ns);
@@ -470,6 +502,15 @@ int scan_run(const gdn_scan_params *p, int mode, hipStream_t s) {
     a.gflag = (int32_t *)(ws + S.gflag);
     a.psum = (float *)(ws + S.psum);
     a.pbc = (float *)(ws + S.pbc);
+  }
+  if (S.walk) {
+    const int64_t es = size_of(p->x_dtype);
+    a.ncb = (int32_t)walk_blocks(p);
+    a.nseg = S.walk;
+    a.near = std::max(std::max(a.x_stride, a.delta_stride), std::max(a.z_stride, C)) * 64 * es <
+             (1 << 30);
+    if (e == hipSuccess) e = launch_scan_walk(a, s);
+    return result();
   }
   if (e == hipSuccess) e = launch_scan_prepare(a, s);
   if (e == hipSuccess && a.ntiles > 1 && (!back || S.own_chunk)) e = launch_scan_states(a, s);

@@ -117,24 +117,40 @@ __device__ __forceinline__ void token_step(const float *bc, float dt, float u,
   if (OUT) y = s[0] + s[1];
 }
 
+// An address that is the same for all lanes, in scalar registers: 64-bit products
+// are formed in vector registers even where their factors are the same for the
+// whole wave, and a load then takes a vector address (six vector operations each).
+template <typename T> __device__ __forceinline__ T *uniform(T *p) {
+  const uint64_t v = (uint64_t)(uintptr_t)p;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  return (T *)(uintptr_t)((uint64_t)hi << 32 | lo);
+}
+
 // Element of a lane in a row that starts `at` elements behind p: an address that
 // is the same for all lanes and `bytes` of this one (so that a load takes one
 // register for its address).
 template <typename T> __device__ __forceinline__ const T *lane_of(const void *p, int64_t at,
                                                                   unsigned bytes) {
-  return (const T *)((const char *)p + at * (int64_t)sizeof(T) + bytes);
+  return (const T *)(uniform((const char *)p + at * (int64_t)sizeof(T)) + bytes);
 }
 template <typename T> __device__ __forceinline__ T *lane_of(void *p, int64_t at, unsigned bytes) {
-  return (T *)((char *)p + at * (int64_t)sizeof(T) + bytes);
+  return (T *)(uniform((char *)p + at * (int64_t)sizeof(T)) + bytes);
 }
 
 // Raw values of U tokens of one channel.
 template <typename Tx, int U> struct Rows {
   Tx v[U];
+  // Tokens t .. of rows `stride` elements apart, the last one in place of those
+  // behind it.
   __device__ __forceinline__ void load(const void *p, int64_t stride, int t, int end, int c) {
+    const int64_t step = stride * (int64_t)sizeof(Tx);
+    const char *row = uniform((const char *)p + min(t, end) * step);
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      v[u] = *lane_of<Tx>(p, (int64_t)min(t + u, end) * stride, (unsigned)c * sizeof(Tx));
+    for (int u = 0; u < U; ++u) {
+      v[u] = *(const Tx *)(row + (unsigned)c * (unsigned)sizeof(Tx));
+      row += t + u < end ? step : 0;
+    }
   }
 };
 

@@ -28,7 +28,7 @@ using namespace scan;
 namespace {
 
 constexpr int kBlock = 16;
-constexpr int kPart = 4;  // tokens whose raw values are held at once
+constexpr int kPart = 8;  // tokens whose raw values are held at once
 
 // Gradients of the empty sequences' initial states: those of their final states.
 // A row of workgroups (`slice` of `slices`) takes every a.empties-th sequence.
@@ -244,6 +244,15 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs a) 
       }
     }
   }
+  // the gradients behind the tile wait in dA's place, which is not used before them
+  if (chained) {
+#pragma unroll
+    for (int n = 0; n < NS; ++n)
+      if (n < a.N) as[n * 64] = *lane_of<float>(a.gchunk, row + (int64_t)n * a.C, c4);
+  } else {
+#pragma unroll
+    for (int n = 0; n < NS; ++n) as[n * 64] = 0.f;
+  }
   float dD = 0.f, dbias = 0.f;
   for (int blk = used - 1; blk >= 0; --blk) {
     const int tb = t0 + blk * kBlock;
@@ -269,19 +278,29 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs a) 
     }
     auto states = [&](auto plain) {
       constexpr bool PLAIN = decltype(plain)::value;
+      // what state n starts from, read while the state before it is worked on
+      struct Start {
+        float A2, h, g;
+        f32x16 bb;
+      };
+      const int64_t at0 = (int64_t)ch.g * 2 * NS * a.Tp + tb;
+      auto start_of = [&](int n) {
+        Start o;
+        o.A2 = *lane_of<float>(a.a2, (int64_t)n * a.C, c4);
+        o.bb = uniform_load<f32x16>(a.bct + at0 + (int64_t)n * a.Tp);
+        o.h = blk > 0  ? st[((blk - 1) * NS + n) * 64]
+              : chained ? *lane_of<float>(a.chunk, row + (int64_t)n * a.C, c4)
+                        : 0.f;
+        o.g = newest ? as[n * 64] : st[(blk * NS + n) * 64];
+        return o;
+      };
+      Start now = start_of(0);
 #pragma unroll 1
       for (int n = 0; n < a.N; ++n) {
-        const float A2 = *lane_of<float>(a.a2, (int64_t)n * a.C, c4);
-        const int64_t at = ((int64_t)ch.g * 2 * NS + n) * a.Tp + tb;
-        const f32x16 bb = uniform_load<f32x16>(a.bct + at);
-        const f32x16 cc = uniform_load<f32x16>(a.bct + at + (int64_t)NS * a.Tp);
-        float h = blk > 0 ? st[((blk - 1) * NS + n) * 64]
-                  : chained ? *lane_of<float>(a.chunk, row + (int64_t)n * a.C, c4)
-                            : 0.f;
-        float g = !newest ? st[(blk * NS + n) * 64]
-                  : chained ? *lane_of<float>(a.gchunk, row + (int64_t)n * a.C, c4)
-                            : 0.f;
-        float e[kBlock], before[kBlock], v[2 * kBlock];
+        const float A2 = now.A2;
+        const f32x16 cc = uniform_load<f32x16>(a.bct + at0 + (int64_t)(NS + n) * a.Tp);
+        float h = now.h, g = now.g;
+        float e[kBlock], before[kBlock + 1], v[2 * kBlock];
 #pragma unroll
         for (int i = 0; i < kBlock; ++i) {
           v[i] = v[kBlock + i] = 0.f;
@@ -292,10 +311,12 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs a) 
           }
           before[i] = h;
           e[i] = __builtin_amdgcn_exp2f(dt[i] * A2);
-          h = fmaf(e[i], h, u[i] * bb[i]);
+          h = fmaf(e[i], h, u[i] * now.bb[i]);
           v[kBlock + i] = y[i] * h;
-          yy[i] = fmaf(cc[i], h, yy[i]);
+          if (!PLAIN) yy[i] = fmaf(cc[i], h, yy[i]);
         }
+        before[kBlock] = h;
+        const Start next = start_of(min(n + 1, a.N - 1));
         float dA = 0.f;
 #pragma unroll
         for (int i = kBlock - 1; i >= 0; --i) {
@@ -304,9 +325,10 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs a) 
             if (m.last >> i & 1)
               g = a.dfin ? a.dfin[((int64_t)m.seq_at(i) * a.C + c) * a.N + n] : 0.f;
           }
+          if (PLAIN) yy[i] = fmaf(cc[i], before[i + 1], yy[i]);
           g = fmaf(cc[i], y[i], g);
           v[i] = g * u[i];
-          du[i] = fmaf(g, bb[i], du[i]);
+          du[i] = fmaf(g, now.bb[i], du[i]);
           g *= e[i];
           const float r = g * before[i];
           dd[i] = fmaf(r, A2, dd[i]);
@@ -316,6 +338,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs a) 
         }
         if (blk > 0) st[((blk - 1) * NS + n) * 64] = g;
         as[n * 64] = newest ? dA : as[n * 64] + dA;
+        now = next;
         if (!ch.ok) {
 #pragma unroll
           for (int i = 0; i < 2 * kBlock; ++i) v[i] = 0.f;
@@ -332,6 +355,10 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs a) 
     // keeps all of them in registers (and others in memory)
     const void *xs = a.x, *ds = a.delta, *ys = a.dy, *zs = a.z;
     asm volatile("" : "+s"(xs), "+s"(ds), "+s"(ys), "+s"(zs));
+    const int64_t first_row = (int64_t)tb * a.C * (int)sizeof(Tx);
+    char *const orow[3] = {uniform((char *)a.dx + first_row), uniform((char *)a.ddelta + first_row),
+                           uniform((char *)a.dz + first_row)};
+    const unsigned cx = (unsigned)c * (unsigned)sizeof(Tx);
 #pragma unroll
     for (int k = 0; k < kBlock; k += kPart) {
       Rows<Tx, kPart> rx, rd, ry, rz;
@@ -346,17 +373,16 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs a) 
         const int i = k + j;
         if (tb + i > end || !ch.ok) continue;
         const bool in = m.valid >> i & 1;
-        const int64_t at = (int64_t)(tb + i) * a.C;
-        const unsigned cx = (unsigned)c * sizeof(Tx);
+        const int64_t at = (int64_t)i * a.C * (int)sizeof(Tx);
         const float x = to_f32(rx.v[j]);
         float ddt = fmaf(du[i], x, kLn2 * dd[i]);
         if (a.softplus) ddt *= sigmoid(to_f32(rd.v[j]) + bias);
-        *lane_of<Tx>(a.dx, at, cx) = from_f32<Tx>(in ? fmaf(du[i], dt[i], D * y[i]) : 0.f);
-        *lane_of<Tx>(a.ddelta, at, cx) = from_f32<Tx>(in ? ddt : 0.f);
+        *(Tx *)(orow[0] + at + cx) = from_f32<Tx>(in ? fmaf(du[i], dt[i], D * y[i]) : 0.f);
+        *(Tx *)(orow[1] + at + cx) = from_f32<Tx>(in ? ddt : 0.f);
         if (a.z) {
           const float z = to_f32(rz.v[j]), sg = sigmoid(z);
           const float dz = to_f32(ry.v[j]) * fmaf(D, x, yy[i]) * (sg * fmaf(z, 1.f - sg, 1.f));
-          *lane_of<Tx>(a.dz, at, cx) = from_f32<Tx>(in ? dz : 0.f);
+          *(Tx *)(orow[2] + at + cx) = from_f32<Tx>(in ? dz : 0.f);
         }
         if (in) {
           dD = fmaf(y[i], x, dD);

@@ -96,12 +96,6 @@ template <typename Key, int E, int M> struct Largest {
   }
 };
 
-__device__ __forceinline__ double wave_sum(double x) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o);
-  return x;
-}
-
 // Candidates that pass a bound, ranked by counting; more of them are left to
 // Largest.
 constexpr int kPass = 512;
@@ -110,21 +104,55 @@ constexpr int kPass = 512;
 // least M groups of the workgroup's 256 threads, so that at least M keys reach it.
 constexpr int group_lanes(int M) { return M <= 16 ? 16 : 4; }
 
-template <typename T> __device__ __forceinline__ T group_max(T x, int lanes) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    if (o >= lanes) break;
-    const T y = __shfl_xor(x, o);
-    x = y > x ? y : x;
-  }
-  return x;
+// Reductions by lane moves within rows of 16 lanes (all of them receive the
+// result), then over the wave's four rows: through LDS each step took as long as
+// reading a part of a row does.
+template <int CTRL> __device__ __forceinline__ unsigned moved(unsigned x) {
+  return (unsigned)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xF, 0xF, true);
 }
-template <typename T> __device__ __forceinline__ T wave_min(T x) {
+template <int CTRL> __device__ __forceinline__ float moved(float x) {
+  return __uint_as_float(moved<CTRL>(__float_as_uint(x)));
+}
+__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ unsigned larger(unsigned a, unsigned b) { return max(a, b); }
+__device__ __forceinline__ float smaller(float a, float b) { return fminf(a, b); }
+__device__ __forceinline__ unsigned smaller(unsigned a, unsigned b) { return min(a, b); }
+__device__ __forceinline__ float of_lane(float x, int l) {
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), l));
+}
+__device__ __forceinline__ unsigned of_lane(unsigned x, int l) {
+  return (unsigned)__builtin_amdgcn_readlane((int)x, l);
+}
+
+// The largest value of the wave and the smallest one of its groups' largest.
+template <int M, typename T>
+__device__ __forceinline__ void top_and_low(T x, T &top, T &low) {
+  T g = larger(x, moved<0xB1>(x));  // quads
+  g = larger(g, moved<0x4E>(g));
+  T hi = larger(g, moved<0x124>(g)), lo = smaller(g, moved<0x124>(g));
+  hi = larger(hi, moved<0x128>(hi));
+  lo = group_lanes(M) == 16 ? hi : smaller(lo, moved<0x128>(lo));
+  top = larger(larger(of_lane(hi, 0), of_lane(hi, 16)), larger(of_lane(hi, 32), of_lane(hi, 48)));
+  low = smaller(smaller(of_lane(lo, 0), of_lane(lo, 16)),
+                smaller(of_lane(lo, 32), of_lane(lo, 48)));
+}
+__device__ __forceinline__ float wave_max(float x) {
+  float top, low;
+  top_and_low<16>(x, top, low);
+  return top;
+}
+// A sum over the wave: rows in fp32, their sums in fp64.
+__device__ __forceinline__ double wave_sum(float x) {
+  x += moved<0xB1>(x);
+  x += moved<0x4E>(x);
+  x += moved<0x124>(x);
+  x += moved<0x128>(x);
+  return ((double)of_lane(x, 0) + (double)of_lane(x, 16)) +
+         ((double)of_lane(x, 32) + (double)of_lane(x, 48));
+}
+__device__ __forceinline__ double wave_sum(double x) {
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    const T y = __shfl_xor(x, o);
-    x = y < x ? y : x;
-  }
+  for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o);
   return x;
 }
 
@@ -181,8 +209,8 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(BeamArgs a) {
   float mine = -kInf;
 #pragma unroll
   for (int e = 0; e < E; ++e) mine = fmaxf(mine, x[e]);
-  const float of_group = group_max(mine, group_lanes(M));
-  const float of_wave = group_max(of_group, 64), low = wave_min(of_group);
+  float of_wave, low;
+  top_and_low<M>(mine, of_wave, low);
   if (lane == 0) {
     s_top[wave] = of_wave;
     s_low[wave] = low;
@@ -200,21 +228,22 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(BeamArgs a) {
 #pragma unroll
     for (int e = 0; e < E; ++e) sum += x[e] == top ? 1.f : 0.f;
   }
-  const double all = wave_sum((double)sum);
+  const double all = wave_sum(sum);
   if (lane == 0) s_sum[wave] = all;
   auto place = [&](int k) { return from + (k / V * kThreads + tid) * V + k % V; };
-  if (mine >= bound) {
-    unsigned n = 0;
+  auto pass = [&](int e) {
+    const unsigned at = atomicAdd(&L.pass.count, 1u);
+    if (at < kPass) L.pass.key[at] = key_of(x[e], (unsigned)place(e));
+  };
+  if (bound > -kInf) {
+    // few of them, so that most registers are passed over by the whole wave
 #pragma unroll
-    for (int e = 0; e < E; ++e) n += x[e] >= bound && place(e) < to;
-    if (n > 0) {
-      unsigned at = atomicAdd(&L.pass.count, n);
-      if (at + n <= kPass) {
+    for (int e = 0; e < E; ++e)
+      if (__ballot(x[e] >= bound) != 0 && x[e] >= bound) pass(e);
+  } else {
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-          if (x[e] >= bound && place(e) < to) L.pass.key[at++] = key_of(x[e], (unsigned)place(e));
-      }
-    }
+    for (int e = 0; e < E; ++e)
+      if (place(e) < to) pass(e);
   }
   __syncthreads();
   const int n = (int)L.pass.count;
@@ -230,7 +259,7 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(BeamArgs a) {
     for (int i = tid; i < n; i += kThreads) {
       const u64 k = L.pass.key[i];
       int r = 0;
-#pragma unroll 4
+#pragma unroll 8
       for (int j = 0; j < n; ++j) r += L.pass.key[j] > k;
       if (r < a.M) put(r, k);
     }
@@ -272,7 +301,7 @@ template <int M> __global__ void __launch_bounds__(kThreads) beam_group_kernel(B
   } L;
   __shared__ Score s_best[M];
   __shared__ double s_log[kMaxM];
-  __shared__ u64 s_low[kWaves];
+  __shared__ unsigned s_low[kWaves];
   __shared__ float s_top[kMaxM], s_score[kMaxM];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, b = blockIdx.x;
   const int per = a.parts * a.M, n = a.K * per;
@@ -295,7 +324,7 @@ template <int M> __global__ void __launch_bounds__(kThreads) beam_group_kernel(B
     float top = -kInf, own = lane < a.parts ? st[2 * lane] : -kInf;
     const float part = lane < a.parts ? st[2 * lane + 1] : 0.f;
     for (int i = lane; i < a.parts; i += 64) top = fmaxf(top, st[2 * i]);
-    top = group_max(top, 64);
+    top = wave_max(top);
     double sum = own == top ? (double)part : (double)part * exp((double)own - (double)top);
     for (int i = lane + 64; i < a.parts; i += 64) {
       own = st[2 * i];
@@ -337,17 +366,16 @@ template <int M> __global__ void __launch_bounds__(kThreads) beam_group_kernel(B
     }
     // nothing better than what there is: on to the next ones
     if (!__syncthreads_or(any)) continue;
-    const u64 low = wave_min(group_max(mine, group_lanes(M)));
+    // (the bound: the upper half of a score's order)
+    unsigned top, low;
+    top_and_low<M>((unsigned)(mine >> 32), top, low);
     if (lane == 0) s_low[wave] = low;
     if (tid == 0) L.pass.count = 0;
     __syncthreads();
-    u64 bound = ~0ull;
+    unsigned low32 = s_low[0];
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      const u64 x = s_low[w];
-      bound = x < bound ? x : bound;
-    }
-    bound = bound > 0 ? bound : 1;
+    for (int w = 1; w < kWaves; ++w) low32 = min(low32, s_low[w]);
+    const u64 bound = low32 > 0 ? (u64)low32 << 32 : 1;
     if (mine >= bound) {
 #pragma unroll
       for (int e = 0; e <= kTake; ++e)
@@ -367,6 +395,7 @@ template <int M> __global__ void __launch_bounds__(kThreads) beam_group_kernel(B
         if (i >= m) continue;
         keep[q] = L.pass.key[i];
         int r = 0;
+#pragma unroll 4
         for (int j = 0; j < m; ++j) r += L.pass.key[j] > keep[q];
         rank[q] = r;
       }

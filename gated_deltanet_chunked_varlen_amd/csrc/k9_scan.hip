@@ -233,12 +233,15 @@ __global__ void __launch_bounds__(kThreads, scan_waves(NS)) scan_tile_kernel(Sca
       rd.load(a.delta, a.delta_stride, t + kRun, end, c);
       if (OUT && a.z) rz.load(a.z, a.z_stride, t + kRun, end, c);
     }
+    char *const orow = uniform((char *)a.out + (int64_t)t * a.C * (int)sizeof(Tx));
     auto token = [&](int u, float x, float dt, float z) {
       float y = D * x;
       token_step<NS, OUT>(bc + (t + u) * bcs, dt, dt * x, A2, h, y);
       if (OUT) {
         if (a.z) y *= z * sigmoid(z);
-        if (ch.ok) *lane_of<Tx>(a.out, (int64_t)(t + u) * a.C, (unsigned)c * sizeof(Tx)) = from_f32<Tx>(y);
+        if (ch.ok)
+          *(Tx *)(orow + (int64_t)u * a.C * (int)sizeof(Tx) + (unsigned)c * (unsigned)sizeof(Tx)) =
+              from_f32<Tx>(y);
       } else {
         span += dt;
       }
