@@ -101,7 +101,7 @@ struct ScanArgs {
   int64_t Tp;
   float *psum;    // [ntiles][N + 2][C] sums of dA, dD and ddelta_bias over a tile
   float *pbc;     // [ncb][2][NS][Tp] sums of dB and dC over a block of channels
-  int32_t vec;    // decode: four states of A, B and C are aligned vectors; walk: eight of B and C
+  int32_t vec;    // decode: four states of A, B and C are aligned vectors
   int32_t num_cus;
 };
 

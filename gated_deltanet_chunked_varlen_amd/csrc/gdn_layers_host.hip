@@ -130,11 +130,12 @@ int conv_shape(const gdn_convolution_params *p, int mode) {
   const int64_t C = p->channels;
   const int rc = check_batch(p, mode, (p->width - 1) * C);
   if (rc != GDN_OK) return rc;
-  // a wave per 64 channels of a run of 16 tokens or of a sequence, at the least
-  const int64_t ncb = (C + 63) / 64, T = p->total_tokens, N = p->num_seqs;
-  if (mode == kDecode ? C * N > kMaxGrid * 256 : ((T + 15) / 16 + N) * ncb > kMaxGrid * 4)
-    return GDN_ERR_SHAPE;
   if (C > INT32_MAX / 8) return GDN_ERR_SHAPE;
+  // a wave per 64 channels of a run of 16 tokens or of a sequence, at the least; in a
+  // decode step a workgroup per 256 channels of a sequence
+  const int64_t ncb = (C + 63) / 64, T = p->total_tokens, N = p->num_seqs;
+  if (mode == kDecode ? (C + 255) / 256 * N > kMaxGrid : ((T + 15) / 16 + N) * ncb > kMaxGrid * 4)
+    return GDN_ERR_SHAPE;
   return GDN_OK;
 }
 
@@ -276,7 +277,7 @@ int64_t scan_tile(const gdn_scan_params *p, bool backward) {
   const int64_t waves = p->total_tokens * scan_blocks(p);
   int64_t most = 256;
   if (backward) most = p->num_states <= 16 ? 64 : p->num_states <= 32 ? 32 : 16;
-  // (whole runs of the walk, k12_scan_walk.hip, which leaves chunk_states too)
+  // (All are whole runs of the walk, k12_scan_walk.hip, which leaves chunk_states too.)
   int64_t L = 16;
   while (L < most && waves / (2 * L) >= 4096) L *= 2;
   return L;
@@ -321,8 +322,9 @@ int scan_shape(const gdn_scan_params *p, int mode) {
   const int rc = check_batch(p, mode, C * p->num_states);
   if (rc != GDN_OK) return rc;
   if (mode == kDecode) {
-    if (C * p->num_states * (int64_t)p->num_seqs > kMaxGrid * 256) return GDN_ERR_SHAPE;
-    return GDN_OK;
+    // a workgroup per 256 lanes of four states (or of a channel) of a sequence
+    const int64_t lanes = C * ((p->num_states + 3) / 4);
+    return (lanes + 255) / 256 * p->num_seqs > kMaxGrid ? GDN_ERR_SHAPE : GDN_OK;
   }
   if (T > 0 && (walk_blocks(p) + 8) * (16 + 64) > kMaxGrid / 4) return GDN_ERR_SHAPE;
   if (T > 0 && ((T + 15) / 16 + 64) * ((scan_blocks(p) + 3) / 4) > kMaxGrid) return GDN_ERR_SHAPE;

@@ -15,6 +15,7 @@ constexpr int kWaves = kThreads / 64;
 constexpr int kRun = 8;  // tokens of which raw values are under way
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kTiny = 0x1p-149f;
+constexpr float kLargest = 0x1.fffffep127f;
 
 // Waves per SIMD that the register budget is made for.
 constexpr int scan_waves(int ns) { return ns == 8 ? 4 : ns == 16 ? 3 : ns == 32 ? 2 : 1; }
@@ -154,7 +155,6 @@ template <typename Tx, int U> struct Rows {
   }
 };
 
-
 inline unsigned tile_grid(const ScanArgs &a, int empties) {
   const int rows = a.ntiles + empties;  // (without any, one for the status word)
   return (unsigned)((rows > 0 ? rows : 1) * ((a.ncb + kWaves - 1) / kWaves));
@@ -174,7 +174,6 @@ hipError_t dispatch(const ScanArgs &a, hipStream_t s) {
   if (a.x_dtype == GDN_F32) return by_states<L, float>(a, s);
   return a.x_dtype == GDN_BF16 ? by_states<L, bf16>(a, s) : by_states<L, f16>(a, s);
 }
-
 
 }  // namespace scan
 }  // namespace gdn

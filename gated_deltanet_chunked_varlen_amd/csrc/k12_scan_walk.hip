@@ -329,7 +329,8 @@ __global__ void __launch_bounds__(64 * run_waves(S), S <= 8 ? 2 : 1)
 #pragma unroll
       for (int s = 0; s < S; ++s) {
         hs.e[s] = h[s];
-        es.e[s] = fmaxf(__builtin_amdgcn_exp2f(span * A2[s]), kTiny);
+        // (neither 0 nor infinite: 0 times infinity is no number)
+        es.e[s] = __builtin_amdgcn_fmed3f(__builtin_amdgcn_exp2f(span * A2[s]), kTiny, kLargest);
       }
       s_state[turn][wave][lane] = hs;
       s_decay[turn][wave][lane] = es;

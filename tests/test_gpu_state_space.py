@@ -115,9 +115,14 @@ def test_steps_as_given(lens, C, N, G, dtype):
 @pytest.mark.parametrize("T,C,N,dtype", [(3000, 192, 4, F32), (9000, 70, 2, BF16)])
 def test_long_tiles(T, C, N, dtype):
     """Enough work for tiles of more than 16 tokens, in both passes."""
-    lens = [T // 2 + 5, 0, T // 2 - 6, 1]
-    reps = 40  # channels alike in pairs of groups: the reference forms one group
-    d = L.scan_make(21, lens, C, N, 1, dtype, True)
+    d = L.scan_make(21, [T // 2 + 5, 0, T // 2 - 6, 1], C, N, 1, dtype, True)
+    tiles = _check_wide(d, [T // 2 + 5, 0, T // 2 - 6, 1], C, 40, dtype)
+    assert tiles < (T + 15) // 16
+
+
+def _check_wide(d, lens, C, reps, dtype):
+    """Both passes of a layer whose channels are `reps` times those of `d`, a group
+    each time: the reference forms one group."""
     wide = {k: (d[k].repeat(1, reps) if k in ("x", "z", "delta", "dy") else
                 d[k].repeat(reps, 1) if k == "A" else d[k].repeat(reps) if k in ("D", "dbias") else
                 d[k].repeat(1, reps, 1) if k in ("h0", "dfinal", "B", "C") else d[k]) for k in d}
@@ -126,7 +131,6 @@ def test_long_tiles(T, C, N, dtype):
                                       return_chunk_states=True)
     plain = selective_scan(*_args(wide), **_layer(wide, True), initial_state=wide["h0"],
                            cu_seqlens=d["cu"])
-    assert kept.shape[0] < (T + 15) // 16
     got = selective_scan_backward(wide["dy"], *_args(wide), **_layer(wide, True),
                                   initial_state=wide["h0"], dfinal_state=wide["dfinal"],
                                   cu_seqlens=d["cu"], chunk_states=kept, output_dinitial_state=True)
@@ -143,6 +147,46 @@ def test_long_tiles(T, C, N, dtype):
                "dz": got[6][:, part], "dbias": got[7][part], "dh0": got[8][:, part]}
         for name, g in cut.items():
             L.check(name, g, back[name], F32 if name in FP32_GRADS else dtype)
+    return kept.shape[0]
+
+
+@pytest.mark.parametrize("lens,C,reps,N,dtype", [
+    ([1000, 0, 1037, 63], 16, 520, 16, BF16), ([257, 0, 300, 1], 64, 50, 32, F32),
+    ([130, 17, 253], 64, 52, 64, BF16), ([90, 500, 33], 64, 70, 8, F16)])
+def test_wide_layers(lens, C, reps, N, dtype):
+    """Layers whose forward pass walks along the tokens, with what it leaves for the
+    backward pass."""
+    d = L.scan_make(C + N + 2, lens, C, N, 1, dtype, True)
+    _check_wide(d, lens, C, reps, dtype)
+
+
+@pytest.mark.parametrize("lens,C,N,G,dtype", [
+    ([250, 0, 300, 90, 60, 1, 16, 17], 24, 16, 1, BF16), ([13] * 50 + [0] * 5 + [7] * 10, 20, 16, 2, F32),
+    ([700, 33, 800, 130], 9, 8, 1, F16), ([128, 128, 0, 256, 2], 40, 16, 1, F32), ([30, 2], 8, 64, 1, F32)])
+def test_walks_of_segments(lens, C, N, G, dtype):
+    """Batches that several workgroups walk along, and the same ones by tiles: B and C
+    at odd addresses."""
+    T, n = sum(lens), len(lens)
+    d = L.scan_make(C + N + 4, lens, C, N, G, dtype, True)
+    want = _want(d, lens, True)
+    both = torch.empty((T, 2 * G * N + 3), device="cuda", dtype=dtype)
+    odd = dict(d, B=both[:, 1:1 + G * N].view(T, G, N), C=both[:, 2 + G * N:2 + 2 * G * N].view(T, G, N))
+    odd["B"].copy_(d["B"])
+    odd["C"].copy_(d["C"])
+    for k in (d, odd):
+        idx = torch.randperm(n + 3, generator=torch.Generator().manual_seed(4))[:n].cuda()
+        pool = torch.zeros((n + 3, C, N), device="cuda")
+        pool[idx] = d["h0"]
+        status = torch.full((1,), 5, dtype=torch.int32, device="cuda")
+        out, final = selective_scan(*_args(k), **_layer(k, True), initial_state=d["h0"],
+                                    output_final_state=True, cu_seqlens=d["cu"])
+        again = selective_scan(*_args(k), **_layer(k, True), initial_state=pool, output_state=pool,
+                               output_final_state=True, cu_seqlens=d["cu"], state_indices=idx,
+                               status=status)[0]
+        L.check("out", out, want.out, dtype)
+        for i in range(n):
+            L.check("final %d" % i, final[i], want.final[i], F32)
+        assert L.same(out, again) and L.same(pool[idx], final) and status.item() == 0
 
 
 @pytest.mark.parametrize("N", [3, 70])

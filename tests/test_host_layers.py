@@ -85,6 +85,8 @@ def test_convolution_accepted(mode):
     (0, dict(total_tokens=-1), "SHAPE"), (0, dict(cu_seqlens=None), "SHAPE"), (0, dict(silu=2), "SHAPE"),
     (0, dict(num_seqs=2 ** 30 + 1), "SHAPE"), (0, dict(total_tokens=2 ** 31 - 1), "SHAPE"),
     (0, dict(total_tokens=2 ** 30, channels=2 ** 20), "SHAPE"), (2, dict(total_tokens=4), "SHAPE"),
+    (2, dict(total_tokens=2 ** 24, num_seqs=2 ** 24, channels=1), "SHAPE"),
+    (2, dict(total_tokens=2 ** 23, num_seqs=2 ** 23, channels=257), "SHAPE"),
     (2, dict(cu_seqlens=FAKE), "SHAPE"), (0, dict(x_dtype=3), "DTYPE"),
     (0, dict(weight_dtype=nat.GDN_F16), "DTYPE"), (0, dict(cu_seqlens_type=5), "DTYPE"),
     (0, dict(x=None), "NULL"), (0, dict(weight=None), "NULL"), (0, dict(output=None), "NULL"),
@@ -157,6 +159,8 @@ def test_scan_accepted(mode):
     (0, dict(total_tokens=2 ** 30, channels=2 ** 20), "SHAPE"), (0, dict(cu_seqlens=None), "SHAPE"),
     (0, dict(delta_softplus=2), "SHAPE"), (2, dict(total_tokens=4), "SHAPE"),
     (2, dict(total_tokens=2 ** 29, num_seqs=2 ** 29), "SHAPE"), (0, dict(x_dtype=4), "DTYPE"),
+    (2, dict(total_tokens=2 ** 24, num_seqs=2 ** 24, channels=1, groups=1), "SHAPE"),
+    (2, dict(total_tokens=2 ** 22, num_seqs=2 ** 22, channels=65, groups=1, num_states=64), "SHAPE"),
     (0, dict(A=None), "NULL"), (0, dict(delta=None), "NULL"), (0, dict(B=None), "NULL"),
     (1, dict(dA=None), "NULL"), (1, dict(dC=None), "NULL"), (1, dict(z=far(20)), "NULL"),
     (0, dict(delta_stride=95), "STRIDES"), (0, dict(c_stride=31), "STRIDES"),
