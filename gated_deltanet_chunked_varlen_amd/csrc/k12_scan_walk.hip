@@ -38,6 +38,7 @@ constexpr int kChannels = 16;  // of a workgroup
 // once would take the registers that the decays are in.
 constexpr int kTogether = 4;
 constexpr int kCompose = 4;  // waves' states read from LDS together
+constexpr int kLoadsDone = 0x0F70;  // s_waitcnt vmcnt(0), nothing else
 
 // Tokens of a run and waves of a workgroup by the states of a lane: S TW decays
 // are held in registers, and the waves' states in LDS.
@@ -161,20 +162,27 @@ __global__ void __launch_bounds__(64 * run_waves(S), S <= 8 ? 2 : 1)
   };
 
   // raw values of the next run: lane q of a channel holds tokens q TQ .. of it
+  // (without z, x in its place: a load less under a condition)
   Tx rx[TQ], rd[TQ], rz[TQ];
   Vec<Tx, 8> rbc[NV];
-  const unsigned xs = (unsigned)(q * TQ * a.x_stride + c) * (unsigned)sizeof(Tx);
-  const unsigned ds = (unsigned)(q * TQ * a.delta_stride + c) * (unsigned)sizeof(Tx);
-  const unsigned zs = (unsigned)(q * TQ * a.z_stride + c) * (unsigned)sizeof(Tx);
-  const unsigned os = (unsigned)(q * TQ * a.C + c) * (unsigned)sizeof(Tx);
+  const Tx *const zsrc = (const Tx *)(a.z ? a.z : a.x);
+  const int64_t zstep = a.z ? a.z_stride : a.x_stride;
+  constexpr int kStep = WAVES * TW;
+  const int base0 = from / kStep * kStep;
+  // this lane's first token of the run that is fetched next, and of the one written
+  const int64_t t00 = base0 + wave * TW + q * TQ;
+  const Tx *xp = (const Tx *)a.x + t00 * a.x_stride + c;
+  const Tx *dp = (const Tx *)a.delta + t00 * a.delta_stride + c;
+  const Tx *zp = zsrc + t00 * zstep + c;
+  Tx *op = (Tx *)a.out + (t00 - kStep) * a.C + c;  // (of the run before)
   auto fetch = [&](int t0) {
-    if (t0 + TW <= T && a.near) {
+    if (t0 + TW <= T) {
+      const Tx *x = xp, *d = dp, *z = zp;
 #pragma unroll
-      for (int k = 0; k < TQ; ++k) {
-        const int64_t t = t0 + k;
-        rx[k] = *shared_row<Tx>(a.x, t * a.x_stride, xs);
-        rd[k] = *shared_row<Tx>(a.delta, t * a.delta_stride, ds);
-        if (a.z) rz[k] = *shared_row<Tx>(a.z, t * a.z_stride, zs);
+      for (int k = 0; k < TQ; ++k, x += a.x_stride, d += a.delta_stride, z += zstep) {
+        rx[k] = *x;
+        rd[k] = *d;
+        rz[k] = *z;
       }
     } else {
 #pragma unroll
@@ -182,9 +190,12 @@ __global__ void __launch_bounds__(64 * run_waves(S), S <= 8 ? 2 : 1)
         const int64_t t = min(t0 + q * TQ + k, end);
         rx[k] = ((const Tx *)a.x)[t * a.x_stride + c];
         rd[k] = ((const Tx *)a.delta)[t * a.delta_stride + c];
-        if (a.z) rz[k] = ((const Tx *)a.z)[t * a.z_stride + c];
+        rz[k] = zsrc[t * zstep + c];
       }
     }
+    xp += kStep * a.x_stride;
+    dp += kStep * a.delta_stride;
+    zp += kStep * zstep;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int id = v * 64 + lane, n0 = id % (NS / 8) * 8, which = id / (NS / 8) % 2;
@@ -195,9 +206,19 @@ __global__ void __launch_bounds__(64 * run_waves(S), S <= 8 ? 2 : 1)
     }
   };
 
-  constexpr int kStep = WAVES * TW;
+  // The outputs of a run are stored behind the waits of the next one, before its
+  // fetch: stores and loads end in order, and the values that were fetched would
+  // else be waited for until the stores behind them are done.
+  Tx out[TQ];
+  unsigned outs = 0;
+  auto put = [&]() {
+#pragma unroll
+    for (int k = 0; k < TQ; ++k)
+      if (outs >> k & 1) op[k * (int64_t)a.C] = out[k];
+    op += (int64_t)kStep * a.C;
+  };
   int turn = 0, within = 0, until = 0;
-  int base = from / kStep * kStep;
+  int base = base0;
   fetch(base + wave * TW);
   if (wave == 0) {
 #pragma unroll
@@ -256,6 +277,7 @@ __global__ void __launch_bounds__(64 * run_waves(S), S <= 8 ? 2 : 1)
       }
     }
     wave_sync();
+    put();
     if (base + kStep < to) fetch(t0 + kStep);
     auto coeff = [&](int t, int which, float(&o)[S]) {
 #pragma unroll
@@ -319,6 +341,9 @@ __global__ void __launch_bounds__(64 * run_waves(S), S <= 8 ? 2 : 1)
         }
         sweep1(lo, hi, std::false_type{});
       });
+      // the states read here are there; else the other branch would wait for them
+      // too, and with them for the next run's values
+      __builtin_amdgcn_s_waitcnt(kLoadsDone);
     }
     float span = 0.f;
 #pragma unroll
@@ -407,6 +432,7 @@ __global__ void __launch_bounds__(64 * run_waves(S), S <= 8 ? 2 : 1)
         sweep2(lo, hi, std::false_type{});
         if (a.fin.p && (last >> (hi - 1) & 1)) final(seq_at(hi - 1), h);
       });
+      __builtin_amdgcn_s_waitcnt(kLoadsDone);
     }
     if (wave == WAVES - 1) {
 #pragma unroll
@@ -419,10 +445,11 @@ __global__ void __launch_bounds__(64 * run_waves(S), S <= 8 ? 2 : 1)
         const float zz = to_f32(z[k]);
         o *= zz * sigmoid(zz);
       }
-      if (ok && (valid >> (q * TQ + k) & 1))
-        *shared_row<Tx>(a.out, (int64_t)(t0 + k) * a.C, os) = from_f32<Tx>(o);
+      out[k] = from_f32<Tx>(o);
     }
+    outs = ok ? valid >> q * TQ : 0u;
   }
+  put();
 }
 
 template <typename Tx, int NS> struct Walk {
