@@ -80,7 +80,6 @@ struct ScanArgs {
   StateRows init, fin;
   // tiles of L tokens and what a pass leaves for the next one
   int32_t L, ntiles, empties;
-  int32_t near;   // walk: a run's tokens lie within 2^30 bytes of its first one
   int32_t nseg;   // segments of the tokens that workgroups walk along (k12_scan_walk.hip)
   float *bc;      // [T][G][2][NS] B and C in fp32, padded with zeros
   float *chunk;   // [ntiles][N][C] first each tile's own state, then the state before it

@@ -506,11 +506,8 @@ int scan_run(const gdn_scan_params *p, int mode, hipStream_t s) {
     a.pbc = (float *)(ws + S.pbc);
   }
   if (S.walk) {
-    const int64_t es = size_of(p->x_dtype);
     a.ncb = (int32_t)walk_blocks(p);
     a.nseg = S.walk;
-    a.near = std::max(std::max(a.x_stride, a.delta_stride), std::max(a.z_stride, C)) * 64 * es <
-             (1 << 30);
     if (e == hipSuccess) e = launch_scan_walk(a, s);
     return result();
   }

@@ -10,8 +10,14 @@
 //      where the last step ended
 //   3. every wave: the true states, from the decays it kept, and the outputs
 // so that a token takes one exponential per state, and no second kernel.  A lane
-// holds S states of a channel, four lanes a channel: 57 cycles of a SIMD for 64
-// states against 85 for two passes over tiles.
+// holds S states of a channel, four lanes a channel.  One prompt of 16384 tokens of
+// 4096 channels with 16 states takes 547 us, the passes over tiles 783; 4096 such
+// tokens of a training step 145 and 230.
+//
+// Bounded by the vector ALU and by what two waves per SIMD leave idle: some 45 cycles
+// of a SIMD per 64 states (the exponential 8, its argument, the input's product twice,
+// three fused products; the rest is the outputs' sums over four lanes and what a token
+// takes for all of its states), which are 57% of the time.
 //
 // The tokens can be cut into segments that workgroups of their own walk along:
 // a segment begins with the first sequence that starts at or behind its place.
@@ -34,15 +40,18 @@ namespace {
 
 constexpr int kLanes = 4;      // of a channel
 constexpr int kChannels = 16;  // of a workgroup
-// Tokens of a sweep that the compiler may mix: all of a run's coefficients read at
-// once would take the registers that the decays are in.
-constexpr int kTogether = 4;
+// Tokens of which the coefficients are read together, those of the next ones while
+// these are worked on: 547 us for 16384 x 4096 in bf16, 572 if the compiler orders
+// the reads of four tokens.  All of a run's at once would take the registers that the
+// decays are in.
+constexpr int kStates = 4, kOutputs = 2;  // of the first sweep, of the second
 constexpr int kCompose = 4;  // waves' states read from LDS together
 constexpr int kLoadsDone = 0x0F70;  // s_waitcnt vmcnt(0), nothing else
 
 // Tokens of a run and waves of a workgroup by the states of a lane: S TW decays
-// are held in registers, and the waves' states in LDS.
-constexpr int run_tokens(int s) { return s <= 8 ? 16 : 8; }
+// are held in registers (16 tokens of 8 states do not fit: 273 us for 4096 tokens of
+// 4096 channels with 32 states, 245 with 8 tokens), and the waves' states in LDS.
+constexpr int run_tokens(int s) { return s <= 4 ? 16 : 8; }
 constexpr int run_waves(int s) { return s <= 8 ? 8 : 4; }
 
 template <int CTRL> __device__ __forceinline__ float quad(float x) {
@@ -310,20 +319,40 @@ __global__ void __launch_bounds__(64 * run_waves(S), S <= 8 ? 2 : 1)
     float e[TW][S], h[S], h0[S];
 #pragma unroll
     for (int s = 0; s < S; ++s) h[s] = h0[s] = 0.f;
+    auto step1 = [&](int t, const float(&b)[S]) {
+      const float d = quad_lane(dt[t % TQ], t / TQ), v = quad_lane(u[t % TQ], t / TQ);
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        e[t][s] = __builtin_amdgcn_exp2f(d * A2[s]);
+        h[s] = fmaf(e[t][s], h[s], v * b[s]);
+      }
+    };
     auto sweep1 = [&](int lo, int hi, auto all) {
       constexpr bool ALL = decltype(all)::value;
+      if constexpr (ALL) {
+        constexpr int K = kStates;
+        float b[2][K][S];
 #pragma unroll
-      for (int t = 0; t < TW; ++t) {
-        if (!ALL && (t < lo || t >= hi)) continue;
-        const float d = quad_lane(dt[t % TQ], t / TQ), v = quad_lane(u[t % TQ], t / TQ);
-        float b[S];
-        coeff(t, 0, b);
+        for (int k = 0; k < K; ++k) coeff(k, 0, b[0][k]);
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-          e[t][s] = __builtin_amdgcn_exp2f(d * A2[s]);
-          h[s] = fmaf(e[t][s], h[s], v * b[s]);
+        for (int t = 0; t < TW; t += K) {
+          if (t + K < TW) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) coeff(t + K + k, 0, b[(t / K + 1) & 1][k]);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int k = 0; k < K; ++k) step1(t + k, b[(t / K) & 1][k]);
+          __builtin_amdgcn_sched_barrier(0);
         }
-        if (ALL && t % kTogether == kTogether - 1) __builtin_amdgcn_sched_barrier(0);
+      } else {
+#pragma unroll
+        for (int t = 0; t < TW; ++t) {
+          if (t < lo || t >= hi) continue;
+          float b[S];
+          coeff(t, 0, b);
+          step1(t, b);
+        }
       }
     };
     if (plain) {
@@ -398,23 +427,50 @@ __global__ void __launch_bounds__(64 * run_waves(S), S <= 8 ? 2 : 1)
     for (int k = 0; k < TQ; ++k) y[k] = 0.f;
 #pragma unroll
     for (int s = 0; s < S; ++s) h[s] = cr[s];
+    auto step2 = [&](int t, const float(&b)[S], const float(&cc)[S]) {
+      const float v = quad_lane(u[t % TQ], t / TQ);
+      float o = 0.f;
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        h[s] = fmaf(e[t][s], h[s], v * b[s]);
+        o = fmaf(cc[s], h[s], o);
+      }
+      o = quad_sum(o);
+      y[t % TQ] = q == t / TQ ? o : y[t % TQ];
+    };
     auto sweep2 = [&](int lo, int hi, auto all) {
       constexpr bool ALL = decltype(all)::value;
+      if constexpr (ALL) {
+        constexpr int K = kOutputs;
+        float b[2][K][S], cc[2][K][S];
 #pragma unroll
-      for (int t = 0; t < TW; ++t) {
-        if (!ALL && (t < lo || t >= hi)) continue;
-        const float v = quad_lane(u[t % TQ], t / TQ);
-        float b[S], cc[S], o = 0.f;
-        coeff(t, 0, b);
-        coeff(t, 1, cc);
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-          h[s] = fmaf(e[t][s], h[s], v * b[s]);
-          o = fmaf(cc[s], h[s], o);
+        for (int k = 0; k < K; ++k) {
+          coeff(k, 0, b[0][k]);
+          coeff(k, 1, cc[0][k]);
         }
-        o = quad_sum(o);
-        y[t % TQ] = q == t / TQ ? o : y[t % TQ];
-        if (ALL && t % kTogether == kTogether - 1) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int t = 0; t < TW; t += K) {
+          if (t + K < TW) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+              coeff(t + K + k, 0, b[(t / K + 1) & 1][k]);
+              coeff(t + K + k, 1, cc[(t / K + 1) & 1][k]);
+            }
+          }
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int k = 0; k < K; ++k) step2(t + k, b[(t / K) & 1][k], cc[(t / K) & 1][k]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      } else {
+#pragma unroll
+        for (int t = 0; t < TW; ++t) {
+          if (t < lo || t >= hi) continue;
+          float b[S], cc[S];
+          coeff(t, 0, b);
+          coeff(t, 1, cc);
+          step2(t, b, cc);
+        }
       }
     };
     if (plain) {
