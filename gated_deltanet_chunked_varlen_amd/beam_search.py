@@ -21,7 +21,8 @@ def beam_select(logits, scores, num_candidates=None, workspace=None):
     many as beams; at most 64, as the beams) of a group are returned best first,
     ties to the lowest beam, then the lowest token.  A beam that has ended is
     given the score -inf; its continuations, and tokens of logit -inf or NaN,
-    come behind all others with the score -inf.
+    come behind all others with the score -inf.  Scores are compared in 64 bits:
+    those that are equal there are ties, whatever the logits.
 
     ``workspace`` (optional uint8 device tensor) is used, if it is large
     enough, instead of the one that is kept for the current stream.

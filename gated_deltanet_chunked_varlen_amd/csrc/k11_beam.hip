@@ -278,7 +278,8 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(BeamArgs a) {
   if (tid < a.M) put(tid, L.all.best[tid]);
 }
 
-// A score in fp64, in the order of whole numbers, and (beam, token) descending.
+// A score in fp64, in the order of whole numbers, and (beam, token) descending; the
+// lowest bit of place is 0 where unequal logits may have this score.
 struct Score {
   u64 value, place;
   __device__ __forceinline__ bool operator>(const Score &o) const {
@@ -294,9 +295,24 @@ __device__ __forceinline__ double value_of(u64 o) {
 }
 
 constexpr int kTake = 8;  // candidates per thread and round
+constexpr int kScan = 16;  // logits per thread and round of a look at whole rows
+
+__device__ __forceinline__ float logit_of(const BeamArgs &a, int64_t at) {
+  const float v = a.dtype == GDN_F32    ? ((const float *)a.logits)[at]
+                  : a.dtype == GDN_BF16 ? to_f32(((const bf16 *)a.logits)[at])
+                                        : to_f32(((const f16 *)a.logits)[at]);
+  return fmaxf(v, -kInf);
+}
 
 // One group.  Candidates come in rounds of kTake a thread; those of a round that
 // reach its bound, with the best so far, are ranked by counting.
+//
+// A beam's candidates are its largest logits, and their scores are in the same
+// order, but not strictly: where |score|, |largest logit| or |log| is so large that
+// 64 bits do not tell unequal logits' scores apart, or infinite, a token that is no
+// candidate can have the last place's score and stand before it.  Such scores carry
+// a mark, and if the last place's has it, the places of its score are filled again
+// from whole rows.
 template <int M> __global__ void __launch_bounds__(kThreads) beam_group_kernel(BeamArgs a) {
   constexpr int kWaves = kThreads / 64;
   __shared__ union {
@@ -307,6 +323,7 @@ template <int M> __global__ void __launch_bounds__(kThreads) beam_group_kernel(B
   __shared__ double s_log[kMaxM];
   __shared__ unsigned s_low[kWaves];
   __shared__ float s_top[kMaxM], s_score[kMaxM];
+  __shared__ int s_count[kWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, b = blockIdx.x;
   const int per = a.parts * a.M, n = a.K * per;
   const int64_t first = (int64_t)b * a.K * a.parts;
@@ -344,6 +361,23 @@ template <int M> __global__ void __launch_bounds__(kThreads) beam_group_kernel(B
   }
   if (tid < M) s_best[tid] = Score{};
   __syncthreads();
+  // (of an infinite largest logit the others have no share)
+  auto score_at = [&](int k, float logit) {
+    const float score = s_score[k], top = s_top[k];
+    if (!(logit > -kInf && score > -kInf)) return -(double)kInf;
+    const double own = logit == top ? 0.0 : (double)logit - (double)top;
+    return own > -(double)kInf ? (double)score + (own - s_log[k]) : -(double)kInf;
+  };
+  // Whether another logit of beam k may have the same score: the next one is 2^-24
+  // of |logit| away at least, and the three sums' roundings, of at most `most`, come
+  // to less than 2^-50 of it for both.
+  auto may_tie = [&](int k, float logit) {
+    const float score = s_score[k], top = s_top[k];
+    if (!(score > -kInf)) return false;  // all of its tokens are alike
+    if (!(logit > -kInf)) return top == kInf;
+    const float most = fabsf(score) + fabsf(top) + fabsf(logit) + fabsf((float)s_log[k]);
+    return !(fabsf(logit) > most * 0x1p-26f);
+  };
   for (int base = 0; base < n; base += kTake * kThreads) {
     Score c[kTake + 1];
     if (base > 0) fetch(base);
@@ -357,14 +391,8 @@ template <int M> __global__ void __launch_bounds__(kThreads) beam_group_kernel(B
       c[e] = Score{};
       if (at[e] < 0) continue;
       const int k = i / per;
-      const float score = s_score[k], top = s_top[k];
-      double v = -(double)kInf;
-      // (of an infinite largest logit the others have no share)
-      if (logit[e] > -kInf && score > -kInf) {
-        const double own = logit[e] == top ? 0.0 : (double)logit[e] - (double)top;
-        if (own > -(double)kInf) v = (double)score + (own - s_log[k]);
-      }
-      c[e] = Score{order_of(v), ~((u64)k * (u64)a.V + (u64)at[e])};
+      const u64 flat = (u64)k * (u64)a.V + (u64)at[e];
+      c[e] = Score{order_of(score_at(k, logit[e])), ~(flat << 1 | (may_tie(k, logit[e]) ? 1u : 0u))};
       any |= c[e] > last;
       mine = c[e].value > mine ? c[e].value : mine;
     }
@@ -413,9 +441,40 @@ template <int M> __global__ void __launch_bounds__(kThreads) beam_group_kernel(B
     }
     __syncthreads();
   }
+  const Score last = s_best[a.M - 1];
+  if (!(last.place & 1)) {
+    int have = 0;  // places that are filled: better scores, then the tokens found
+    for (int i = 0; i < a.M; ++i) have += s_best[i].value > last.value;
+    __syncthreads();
+    for (int k = 0; k < a.K && have < a.M; ++k) {
+      if (order_of(score_at(k, s_top[k])) < last.value) continue;
+      const int64_t row = ((int64_t)b * a.K + k) * a.stride;
+      for (int from = 0; from < a.V && have < a.M; from += kScan * kThreads) {
+        unsigned found = 0;
+#pragma unroll 4
+        for (int e = 0; e < kScan; ++e) {
+          const int t = from + tid * kScan + e;
+          if (t < a.V && order_of(score_at(k, logit_of(a, row + t))) == last.value) found |= 1u << e;
+        }
+        const int own = __builtin_popcount(found), sum = wave_prefix_sum_i(own);
+        if (lane == 63) s_count[wave] = sum;
+        __syncthreads();
+        int at0 = have + sum - own;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+          if (w < wave) at0 += s_count[w];
+          have += s_count[w];
+        }
+        for (; found != 0 && at0 < a.M; found &= found - 1, ++at0)
+          s_best[at0] = Score{last.value, ~(((u64)k * (u64)a.V +
+                                             (u64)(from + tid * kScan + __builtin_ctz(found))) << 1)};
+        __syncthreads();
+      }
+    }
+  }
   if (tid >= a.M) return;
   const Score best = s_best[tid];
-  const u64 flat = ~best.place;
+  const u64 flat = ~best.place >> 1;
   const int64_t o = (int64_t)b * a.M + tid;
   a.out_scores[o] = (float)value_of(best.value);
   a.parents[o] = (int)(flat / (u64)a.V);

@@ -651,7 +651,8 @@ int gdn_scan_decode(const gdn_scan_params *p, void *stream);
  * fp64 and returned in fp32.  A logit that is NaN or -inf, and every one of a
  * beam whose score is -inf or NaN (a beam that has ended), scores -inf; such
  * continuations come last, by beam and token.  Logits of +inf share the beam's
- * whole probability.
+ * whole probability, and its other continuations score -inf.  Scores that are equal
+ * in fp64 or infinite are ties, also those of unequal logits.
  */
 #define GDN_BEAM_MAX 64 /* beams of a group, candidates of a group */
 

@@ -130,6 +130,31 @@ def test_large_logits_and_scores():
     assert np.allclose(got[0].cpu().numpy(), want[0], rtol=2.0 ** -23, atol=0)
 
 
+@pytest.mark.parametrize("V", [50, 3000, 20001])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_scores_that_are_equal_for_unequal_logits(V, dtype):
+    """Scores that 64 bits do not tell apart, or infinite ones, are ties: the lowest
+    token, whatever its logit."""
+    logits, scores = _make(V, 7, 3, V, dtype)
+    scores[0] = torch.finfo(F32).min                  # beams as good as dead
+    scores[1, 1:] = torch.finfo(F32).min
+    logits[1, 0, 2:] = -INF                           # two tokens are allowed
+    scores[2] = torch.tensor([-1e30, INF, -1e30])
+    logits[3, 1, V // 2] = INF                        # the others have no share
+    logits[3, 1, V - 1] = INF
+    scores[3, 0] = -INF
+    scores[3, 2] = float("nan")
+    logits[4, :, V - 3] = 1e30
+    logits[5, :, ::2] = -INF
+    scores[5] = -1e30
+    logits[6, 0] = INF
+    logits[6, 1, 7] = INF
+    scores[6, 2] = -INF
+    for m in (1, 5, 16, 40):
+        _check(logits, scores, m)
+        _check(logits[:, 1:2].contiguous(), scores[:, 1:2].contiguous(), m)
+
+
 def test_strides_and_odd_addresses():
     logits, scores = _make(9, 3, 4, 1001, BF16)
     wide = torch.zeros((3, 4, 1100), dtype=BF16, device="cuda")
