@@ -155,6 +155,11 @@ template <typename Tx, int U> struct Rows {
   }
 };
 
+// D x, nothing without D (0 times infinity is no number).
+__device__ __forceinline__ float skip_of(const ScanArgs &a, float D, float x) {
+  return a.D ? D * x : 0.f;
+}
+
 inline unsigned tile_grid(const ScanArgs &a, int empties) {
   const int rows = a.ntiles + empties;  // (without any, one for the status word)
   return (unsigned)((rows > 0 ? rows : 1) * ((a.ncb + kWaves - 1) / kWaves));

@@ -383,11 +383,12 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs a) 
         const float x = to_f32(rx.v[j]);
         float ddt = fmaf(du[i], x, kLn2 * dd[i]);
         if (a.softplus) ddt *= sigmoid(to_f32(rd.v[j]) + bias);
-        *(Tx *)(orow[0] + at + cx) = from_f32<Tx>(in ? fmaf(du[i], dt[i], D * y[i]) : 0.f);
+        *(Tx *)(orow[0] + at + cx) = from_f32<Tx>(in ? fmaf(du[i], dt[i], skip_of(a, D, y[i])) : 0.f);
         *(Tx *)(orow[1] + at + cx) = from_f32<Tx>(in ? ddt : 0.f);
         if (a.z) {
           const float z = to_f32(rz.v[j]), sg = sigmoid(z);
-          const float dz = to_f32(ry.v[j]) * fmaf(D, x, yy[i]) * (sg * fmaf(z, 1.f - sg, 1.f));
+          const float out = a.D ? fmaf(D, x, yy[i]) : yy[i];
+          const float dz = to_f32(ry.v[j]) * out * (sg * fmaf(z, 1.f - sg, 1.f));
           *(Tx *)(orow[2] + at + cx) = from_f32<Tx>(in ? dz : 0.f);
         }
         if (in) {

@@ -496,7 +496,7 @@ __global__ void __launch_bounds__(64 * run_waves(S), S <= 8 ? 2 : 1)
     }
 #pragma unroll
     for (int k = 0; k < TQ; ++k) {
-      float o = fmaf(D, to_f32(x[k]), y[k]);
+      float o = a.D ? fmaf(D, to_f32(x[k]), y[k]) : y[k];
       if (a.z) {
         const float zz = to_f32(z[k]);
         o *= zz * sigmoid(zz);

@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, scan_waves(NS)) scan_tile_kernel(Sca
     }
     char *const orow = uniform((char *)a.out + (int64_t)t * a.C * (int)sizeof(Tx));
     auto token = [&](int u, float x, float dt, float z) {
-      float y = D * x;
+      float y = OUT ? skip_of(a, D, x) : 0.f;
       token_step<NS, OUT>(bc + (t + u) * bcs, dt, dt * x, A2, h, y);
       if (OUT) {
         if (a.z) y *= z * sigmoid(z);
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kThreads) scan_decode_kernel(ScanArgs a, int b
 #pragma unroll
     for (int o = 1; o < Q; o <<= 1) y += __shfl_xor(y, o);
     if (!on || at % Q != 0) continue;
-    y = fmaf(D[k], x[k], y);
+    if (a.D) y = fmaf(D[k], x[k], y);
     if (a.z) y *= z[k] * sigmoid(z[k]);
     ((Tx *)a.out)[(int64_t)i * a.C + at / Q] = from_f32<Tx>(y);
   }
@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(kThreads) scan_decode_any_kernel(ScanArgs a, i
     y = fmaf(to_f32(C[n]), h[0][0], y);
     if (a.fin.p && r >= 0) state_write<1, 1>(a.fin, to, h);
   }
-  y = fmaf(a.D ? a.D[c] : 0.f, x, y);
+  if (a.D) y = fmaf(a.D[c], x, y);
   if (a.z) {
     const float z = to_f32(((const Tx *)a.z)[i * a.z_stride + c]);
     y *= z * sigmoid(z);

@@ -335,6 +335,50 @@ def test_steps_of_zero_and_strong_decay():
     assert torch.isfinite(out).all()
 
 
+def _infinite(N):
+    """An infinite token or step makes its channel's states infinite, and with
+    coefficients above 0 and no D the outputs: infinite, not NaN."""
+    lens, C = [70, 30], 6
+    d = _drop(L.scan_make(38, lens, C, N, 1, F32, False), "D", "z", "dbias")
+    for k in ("x", "B", "C"):
+        d[k] = d[k].abs() + 0.1
+    d["delta"].fill_(0.25)
+    d["x"][20, 1] = d["x"][93, 4] = float("inf")
+    d["delta"][40, 2] = float("inf")
+    want = torch.zeros((100, C), dtype=torch.bool, device="cuda")
+    want[20:70, 1] = want[93:, 4] = want[40:70, 2] = True
+    out, final = selective_scan(*_args(d), initial_state=d["h0"].abs(), output_final_state=True,
+                                cu_seqlens=d["cu"])
+    assert torch.equal(out == float("inf"), want) and not torch.isnan(out).any()
+    ends = torch.stack([want[69], want[99]])[:, :, None].expand(2, C, N)
+    assert torch.equal(final == float("inf"), ends) and not torch.isnan(final).any()
+    out, final = selective_scan_decode(*_args(d))
+    here = torch.zeros_like(want)
+    here[20, 1] = here[93, 4] = here[40, 2] = True
+    assert torch.equal(out == float("inf"), here) and not torch.isnan(out).any()
+    assert torch.equal(final == float("inf"), here[:, :, None].expand(100, C, N))
+
+
+@pytest.mark.parametrize("N", [8, 16, 64])
+def test_infinite_inputs_without_a_skip(N):
+    _infinite(N)
+
+
+@pytest.mark.parametrize("N", [4, 16])
+def test_infinite_gradients_without_a_skip(N):
+    """The gradient of an output of channel 1 is infinite: that of its inputs up to
+    there too, not NaN."""
+    lens = [40, 30]
+    d = L.scan_make(39, lens, 6, N, 1, F32, False)
+    for k in ("x", "B", "C"):
+        d[k] = d[k].abs() + 0.1
+    d["dy"][60, 1] = float("inf")
+    dx = selective_scan_backward(d["dy"], *_args(d), cu_seqlens=d["cu"])[0]
+    want = torch.zeros((70, 6), dtype=torch.bool, device="cuda")
+    want[40:61, 1] = True
+    assert torch.equal(dx == float("inf"), want) and not torch.isnan(dx).any()
+
+
 def test_softplus_over_its_range():
     """Large and very small arguments keep their relative precision."""
     d = L.scan_make(35, [64], 1, 1, 1, F32, True)
