@@ -181,8 +181,8 @@ __device__ __forceinline__ void empty_sequences(const ScanArgs &a, int part, int
 
 // OUT false: a tile's own last state, the sum of its step sizes, and the initial
 // state of a sequence that starts in it and goes on.  OUT true: outputs and
-// final states from the state before the tile.
-template <typename Tx, int NS, bool OUT>
+// final states from the state before the tile.  FULL: N = NS.
+template <typename Tx, int NS, bool OUT, bool FULL>
 __global__ void __launch_bounds__(kThreads, scan_waves(NS)) scan_tile_kernel(ScanArgs a) {
   __shared__ TileGeo G;
   __shared__ float s_states[kWaves][NS][64], s_run[kWaves][3 * kRun][64];
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, scan_waves(NS)) scan_tile_kernel(Sca
     char *const orow = uniform((char *)a.out + (int64_t)t * a.C * (int)sizeof(Tx));
     auto token = [&](int u, float x, float dt, float z) {
       float y = OUT ? skip_of(a, D, x) : 0.f;
-      token_step<NS, OUT>(bc + (t + u) * bcs, dt, dt * x, A2, h, y);
+      token_step<NS, OUT, FULL>(bc + (t + u) * bcs, dt, dt * x, A2, h, y, a.N);
       if (OUT) {
         if (a.z) y *= z * sigmoid(z);
         if (ch.ok)
@@ -434,14 +434,17 @@ __global__ void __launch_bounds__(kThreads) scan_decode_any_kernel(ScanArgs a, i
 
 template <typename Tx, int NS> struct States {
   static hipError_t go(const ScanArgs &a, hipStream_t s) {
-    scan_tile_kernel<Tx, NS, false><<<dim3(tile_grid(a, 0)), dim3(kThreads), 0, s>>>(a);
+    // (which leaves no more than N states, and no sums over them)
+    scan_tile_kernel<Tx, NS, false, true><<<dim3(tile_grid(a, 0)), dim3(kThreads), 0, s>>>(a);
     const hipError_t e = hipGetLastError();
     return e == hipSuccess ? launch_scan_chain(a, false, s) : e;
   }
 };
 template <typename Tx, int NS> struct Forward {
   static hipError_t go(const ScanArgs &a, hipStream_t s) {
-    scan_tile_kernel<Tx, NS, true><<<dim3(tile_grid(a, a.empties)), dim3(kThreads), 0, s>>>(a);
+    const dim3 grid(tile_grid(a, a.empties));
+    if (a.N == NS) scan_tile_kernel<Tx, NS, true, true><<<grid, dim3(kThreads), 0, s>>>(a);
+    else scan_tile_kernel<Tx, NS, true, false><<<grid, dim3(kThreads), 0, s>>>(a);
     return hipGetLastError();
   }
 };

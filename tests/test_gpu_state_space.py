@@ -364,6 +364,12 @@ def test_infinite_inputs_without_a_skip(N):
     _infinite(N)
 
 
+@pytest.mark.parametrize("N", [1, 3, 12, 33])
+def test_infinite_inputs_with_any_number_of_states(N):
+    """Numbers of states that kernels are not compiled for."""
+    _infinite(N)
+
+
 @pytest.mark.parametrize("N", [4, 16])
 def test_infinite_gradients_without_a_skip(N):
     """The gradient of an output of channel 1 is infinite: that of its inputs up to
