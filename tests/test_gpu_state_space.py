@@ -405,6 +405,122 @@ def test_sequence_bounds_that_are_wrong():
         assert status.item() == nat.STATUS_CU_SEQLENS and out.shape == (40, 32)
 
 
+# The walk (8, 16, 32 or 64 states in aligned rows, few enough tokens: 768 of 16 states
+# where there are few channels): the same as above, over segments and over sequences
+# that end where a run of 16 tokens or a step of eight runs does.
+
+@pytest.mark.parametrize("N", [8, 16])
+@pytest.mark.parametrize("lens", [[126, 200, 128, 90, 16, 0, 60], [7] * 70])
+def test_walks_leave_rows_outside_alone(lens, N):
+    d = L.scan_make(40, lens, 6, N, 1, F32, True, tail=77)
+    cu, T = (d["cu"] + 30).to(torch.int64), sum(lens)
+    out = torch.full_like(d["x"], 7.0)
+    kept = selective_scan(*_args(d), **_layer(d, True), cu_seqlens=cu, output=out,
+                          return_chunk_states=True)[1]
+    want = _want(_drop(d, "h0"), lens, True, 30)
+    span = slice(30, 30 + T)
+    L.check("out", out[span], want.out[span], F32)
+    assert (out[:30] == 7).all() and (out[30 + T:] == 7).all()
+    got = selective_scan_backward(d["dy"], *_args(d), **_layer(d, True), cu_seqlens=cu,
+                                  chunk_states=kept)
+    _check_backward(_drop(d, "h0", "dfinal"), lens, True, F32, got, 30)
+
+
+@pytest.mark.parametrize("N", [8, 16])
+def test_walks_keep_a_nan_in_its_sequence_and_channel(N):
+    lens = [128, 112, 16, 30, 40, 128, 250]
+    d = L.scan_make(41, lens, 5, N)
+    starts = [0] + np.cumsum(lens).tolist()
+    d["x"][starts[0] + 127, 1] = float("nan")     # a step's last token
+    d["delta"][starts[2] + 15, 2] = float("nan")  # a run's last token
+    d["x"][starts[3] + 5, 4] = float("nan")
+    d["h0"][5, 3, 1] = float("inf")
+    out, final, kept = selective_scan(*_args(d), **_layer(d, True), initial_state=d["h0"],
+                                      output_final_state=True, cu_seqlens=d["cu"],
+                                      return_chunk_states=True)
+    want = torch.zeros(out.shape, dtype=torch.bool, device="cuda")
+    want[127, 1] = want[starts[2] + 15, 2] = True
+    want[starts[3] + 5:starts[4], 4] = True
+    want[starts[5]:starts[6], 3] = True
+    assert torch.equal(~torch.isfinite(out), want)
+    bad = torch.zeros((7, 5), dtype=torch.bool, device="cuda")
+    bad[0, 1] = bad[2, 2] = bad[3, 4] = bad[5, 3] = True
+    assert torch.equal(~torch.isfinite(final).all(2), bad)
+    assert torch.isinf(final[5, 3, 1]) and torch.isnan(final[0, 1]).all()
+    got = selective_scan_backward(d["dy"], *_args(d), **_layer(d, True), initial_state=d["h0"],
+                                  cu_seqlens=d["cu"], chunk_states=kept, output_dinitial_state=True)
+    for i in (1, 4, 6):
+        assert torch.isfinite(got[0][starts[i]:starts[i + 1]]).all()
+        assert torch.isfinite(got[8][i]).all()
+
+
+@pytest.mark.parametrize("N", [4, 8, 16, 64])
+def test_an_infinite_state_under_a_decay_that_underflows(N):
+    """Every token's decay is above 0, that of a run or tile is not."""
+    lens = [300, 40]
+    d = L.scan_make(42, lens, 4, N, 1, F32, False)
+    d["delta"].fill_(2.0)
+    d["A"].fill_(-4.0)
+    d["h0"][0, 2] = float("inf")
+    d["h0"][1, 1] = -float("inf")
+    d["C"].abs_()
+    out, final = selective_scan(*_args(d), initial_state=d["h0"], output_final_state=True,
+                                cu_seqlens=d["cu"])
+    assert (out[:300, 2] == float("inf")).all() and (out[300:, 1] == -float("inf")).all()
+    assert (final[0, 2] == float("inf")).all() and (final[1, 1] == -float("inf")).all()
+    assert torch.isfinite(out[:, [0, 3]]).all() and torch.isfinite(final[:, [0, 3]]).all()
+
+
+@pytest.mark.parametrize("N", [8, 16, 64])
+def test_walks_of_steps_of_zero_and_strong_decay(N):
+    lens = [300, 300]
+    d = L.scan_make(43, lens, 4, N, 1, F32, False)
+    d["delta"][:300] = 0.0
+    d["delta"][300:] = 90.0
+    d["A"].fill_(-4.0)
+    out, final = selective_scan(*_args(d), initial_state=d["h0"], output_final_state=True,
+                                cu_seqlens=d["cu"])
+    assert torch.equal(final[0], d["h0"][0])
+    last = (90.0 * d["x"][599])[:, None] * d["B"][599, 0]
+    assert torch.allclose(final[1], last, rtol=3 * 2.0 ** -24, atol=0)
+    assert torch.isfinite(out).all()
+
+
+@pytest.mark.parametrize("N", [8, 16])
+def test_walks_over_sequence_bounds_that_are_wrong(N):
+    d = L.scan_make(44, [350, 350], 32, N)
+    for cu, used in (([0, 500, 300, 650], 650), ([0, 300, 20000], 700), ([-5, 300, 600], 600),
+                     ([0] + [500, 300] * 40, 500)):
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = torch.full_like(d["x"], 7.0)
+        selective_scan(*_args(d), delta_softplus=True, cu_seqlens=torch.tensor(cu).cuda(),
+                       status=status, output=out)
+        assert status.item() == nat.STATUS_CU_SEQLENS
+        assert (out[used:] == 7).all() and torch.isfinite(out).all()
+
+
+@pytest.mark.parametrize("N,G,lens", [(8, 2, [240, 0, 90, 270]), (16, 1, [240, 0, 90, 270]),
+                                      (64, 2, [100, 0, 60, 90])])
+def test_walks_over_strided_tokens(N, G, lens):
+    """Every input a slice of wider rows, B and C on boundaries of 16 bytes."""
+    T, C = sum(lens), 70
+    d = L.scan_make(45, lens, C, N, G, BF16, True)
+    s = dict(d)
+    for i, k in enumerate(("x", "delta", "z")):
+        s[k] = torch.randn((T, 2 * C + 3 + i), device="cuda").to(BF16)[:, 1:1 + C]
+        s[k].copy_(d[k])
+    both = torch.randn((T, 3, G, N), device="cuda").to(BF16)
+    s["B"], s["C"] = both[:, 0], both[:, 2]
+    s["B"].copy_(d["B"])
+    s["C"].copy_(d["C"])
+    out, final = selective_scan(*_args(s), **_layer(s, True), initial_state=d["h0"],
+                                output_final_state=True, cu_seqlens=d["cu"])
+    want = _want(d, lens, True)
+    L.check("out", out, want.out, BF16)
+    for i in range(len(lens)):
+        L.check("final %d" % i, final[i], want.final[i], F32)
+
+
 def test_no_tokens():
     d = L.scan_make(36, [0, 0], 8, 4)
     status = torch.full((1,), 9, dtype=torch.int32, device="cuda")
