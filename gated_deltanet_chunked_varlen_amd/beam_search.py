@@ -43,8 +43,8 @@ def state_pool_reorder(pools, state_indices, parents, output_indices=None, statu
     row, the others take the rows of beams without a child, which are
     overwritten with their parents' rows; no other row changes.  ``pools`` is one
     pool or a list of pools (any state dtypes and shapes, the same number of
-    rows; they share no elements), all reordered alike, or none if one of them
-    is refused.
+    rows; pools that share elements are refused), all reordered alike, or none if
+    one of them is refused.
 
     Returns the children's rows, like state_indices (in ``output_indices`` if
     given, which must not overlap the other lists).  A parent outside

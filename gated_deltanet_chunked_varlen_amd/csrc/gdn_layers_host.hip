@@ -5,9 +5,12 @@
 
 #include <algorithm>
 #include <cstring>
+#include <memory>
+#include <new>
 
 #include "../../include/gdn_prefill.h"
 #include "gdn_layers.h"
+#include "gdn_pool_views.h"
 #include "gdn_recurrence.h"
 
 using namespace gdn;
@@ -570,31 +573,6 @@ int beam_validate(const gdn_beam_params *p) {
   return GDN_OK;
 }
 
-// Strides of a pool in elements, positive and not overlapping.
-bool settle_strides(const int64_t in[4], int64_t rows, const int64_t ext[3], int64_t out[4]) {
-  if (in[0] == 0 && in[1] == 0 && in[2] == 0 && in[3] == 0) {
-    out[3] = 1;
-    out[2] = ext[2];
-    out[1] = ext[1] * ext[2];
-    out[0] = ext[0] * ext[1] * ext[2];
-    return true;
-  }
-  const int64_t n[4] = {rows, ext[0], ext[1], ext[2]};
-  int at[4] = {0, 1, 2, 3};
-  for (int i = 0; i < 4; ++i) {
-    out[i] = in[i];
-    if (in[i] <= 0 && n[i] > 1) return false;
-  }
-  std::sort(at, at + 4, [&](int x, int y) { return in[x] < in[y]; });
-  int64_t reach = 1;
-  for (int k : at) {
-    if (n[k] <= 1) continue;
-    if (in[k] < reach) return false;
-    reach += in[k] * (n[k] - 1);
-  }
-  return true;
-}
-
 int reorder_pool(const gdn_reorder_params *p, const gdn_reorder_pool &q, ReorderArgs::Pool &o) {
   int64_t row = 1;
   for (int i = 0; i < 3; ++i) {
@@ -607,15 +585,15 @@ int reorder_pool(const gdn_reorder_params *p, const gdn_reorder_pool &q, Reorder
   const int64_t es = size_of(q.dtype);
   if (!aligned(q.pool, es)) return GDN_ERR_ALIGN;
   int64_t s[4];
-  if (!settle_strides(q.strides, p->pool_rows, q.extent, s)) return GDN_ERR_STRIDES;
+  if (!pool_strides_ok(q.strides, p->pool_rows, q.extent)) return GDN_ERR_STRIDES;
+  pool_strides(q.strides, q.extent, s);
   o.p = (char *)q.pool;
   for (int i = 0; i < 4; ++i) o.str[i] = s[i] * es;
   o.d2 = q.extent[1];
   o.d3 = q.extent[2];
   o.row = row;
   o.es = (int32_t)es;
-  o.flat = (q.extent[2] == 1 || s[3] == 1) && (q.extent[1] == 1 || s[2] == q.extent[2]) &&
-           (q.extent[0] == 1 || s[1] == q.extent[1] * q.extent[2]);
+  o.flat = row_contiguous(s, q.extent);
   const int64_t step = p->pool_rows > 1 ? o.str[0] : 0;
   o.align = 16;
   while (o.align > 1 && ((uintptr_t)q.pool % o.align || step % o.align || (row * es) % o.align))
@@ -627,6 +605,74 @@ int reorder_pool(const gdn_reorder_params *p, const gdn_reorder_pool &q, Reorder
   o.unit = (int32_t)unit;
   o.units = (int32_t)((row + unit - 1) / unit);
   return GDN_OK;
+}
+
+// The bytes that a pool lies in, and those of one row.
+struct PoolSpan {
+  const gdn_reorder_pool *q;
+  uintptr_t lo, hi;
+  int64_t step, row;  // from row to row
+  PoolSpan() = default;
+  PoolSpan(const gdn_reorder_pool &pool, int64_t rows) : q(&pool), lo((uintptr_t)pool.pool) {
+    int64_t s[4];
+    pool_strides(pool.strides, pool.extent, s);
+    const int64_t es = size_of(pool.dtype);
+    step = s[0] * es;
+    row = row_span(s, pool.extent, es);
+    hi = lo + (uintptr_t)((rows - 1) * step + row);
+  }
+  bool apart(const PoolSpan &o, int64_t rows) const {
+    if (lo >= o.hi || o.lo >= hi) return true;
+    int64_t s[4], t[4];
+    pool_strides(q->strides, q->extent, s);
+    pool_strides(o.q->strides, o.q->extent, t);
+    return views_apart((int64_t)(lo - o.lo), s, rows, size_of(q->dtype), q->extent, t, rows,
+                       size_of(o.q->dtype), o.q->extent);
+  }
+};
+
+// The pools of a call share no bytes.  Where neighbours in memory overlap as
+// stretches, they are mostly interleaved row by row (the layers of one buffer):
+// then their rows are apart in one period of rows, sorted by their place in it.
+// What that does not settle is compared pair by pair.
+bool pools_apart(const gdn_reorder_params *p) {
+  const int32_t n = p->num_pools;
+  const int64_t rows = p->pool_rows;
+  if (n < 2 || rows < 1) return true;
+  const std::unique_ptr<PoolSpan[]> v(new (std::nothrow) PoolSpan[(size_t)n]);
+  auto each_pair = [&](int32_t from, int32_t to) {
+    for (int32_t i = from; i < to; ++i)
+      for (int32_t j = i + 1; j < to; ++j) {
+        const bool ok = v ? v[i].apart(v[j], rows)
+                          : PoolSpan(p->pools[i], rows).apart(PoolSpan(p->pools[j], rows), rows);
+        if (!ok) return false;
+      }
+    return true;
+  };
+  if (!v) return each_pair(0, n);
+  for (int32_t i = 0; i < n; ++i) v[i] = PoolSpan(p->pools[i], rows);
+  std::sort(&v[0], &v[0] + n, [](const PoolSpan &a, const PoolSpan &b) { return a.lo < b.lo; });
+  for (int32_t from = 0, to; from < n; from = to) {
+    uintptr_t end = v[from].hi;
+    for (to = from + 1; to < n && v[to].lo < end; ++to) end = std::max(end, v[to].hi);
+    if (to == from + 1) continue;
+    const uintptr_t base = v[from].lo, step = (uintptr_t)v[from].step;
+    bool one_step = rows > 1;
+    for (int32_t i = from; i < to; ++i)
+      one_step = one_step && (uintptr_t)v[i].step == step && (uintptr_t)v[i].row <= step;
+    if (one_step) {
+      auto place = [&](const PoolSpan &s) { return (s.lo - base) % step; };
+      std::sort(&v[0] + from, &v[0] + to,
+                [&](const PoolSpan &a, const PoolSpan &b) { return place(a) < place(b); });
+      for (int32_t i = from; i < to && one_step; ++i) {
+        const uintptr_t next = i + 1 < to ? place(v[i + 1]) : step + place(v[from]);
+        one_step = place(v[i]) + (uintptr_t)v[i].row <= next;
+      }
+      if (one_step) continue;
+    }
+    if (!each_pair(from, to)) return false;
+  }
+  return true;
 }
 
 int reorder_validate(const gdn_reorder_params *p) {
@@ -649,7 +695,7 @@ int reorder_validate(const gdn_reorder_params *p) {
     const int rc = reorder_pool(p, p->pools[i], one);
     if (rc != GDN_OK) return rc;
   }
-  return GDN_OK;
+  return pools_apart(p) ? GDN_OK : GDN_ERR_STATE;
 }
 
 }  // namespace

@@ -698,7 +698,7 @@ typedef struct gdn_reorder_pool {
 typedef struct gdn_reorder_params {
   int32_t num_groups;      /* B >= 0 */
   int32_t num_beams;       /* K: 1 .. GDN_BEAM_MAX */
-  int32_t num_pools;       /* >= 1; they may share no elements */
+  int32_t num_pools;       /* >= 1; GDN_ERR_STATE if two share elements */
   int64_t pool_rows;       /* rows of every pool */
   const gdn_reorder_pool *pools; /* host */
   const void *state_indices;

@@ -254,6 +254,59 @@ def test_reorder(pool, kw, err):
     assert _reorder(pool, **kw) == (code("GDN_ERR_" + err) if err else 0)
 
 
+BASE = 0x10000000
+
+
+def _view(at, extent, strides=(0, 0, 0, 0), dtype=nat.GDN_F32):
+    return (BASE + at, dtype, list(extent), list(strides))
+
+
+def _reorder_of(views, rows):
+    pools = (nat.ReorderPool * len(views))()
+    for q, (at, dtype, extent, strides) in zip(pools, views):
+        q.pool, q.dtype = ctypes.c_void_p(at), dtype
+        q.extent[:], q.strides[:] = extent, strides
+    p = nat.ReorderParams()
+    p.num_groups, p.num_beams, p.num_pools, p.pool_rows = 2, 4, len(views), rows
+    p.pools = ctypes.cast(pools, ctypes.c_void_p)
+    p.state_indices, p.parents, p.new_indices = far(1), far(2), far(3)
+    return nat.lib().gdn_validate_reorder_host(ctypes.byref(p))
+
+
+LAYERS = [_view(4 * 132 * i, (1, 4, 33), (9 * 132, 1, 33, 1)) for i in range(9)]
+
+
+@pytest.mark.parametrize("views", [
+    # one after the other; the layers of one [rows, layers, ...] buffer, in any order
+    [_view(0, (2, 3, 4)), _view(4 * 24 * 20, (2, 3, 4))], LAYERS, LAYERS[::-1], LAYERS + [_view(4 * 9 * 132 * 20, (5, 1, 1))],
+    # two kinds of states in one buffer of 100 elements a row
+    [_view(0, (1, 3, 20), (100, 1, 20, 1)), _view(240, (1, 4, 10), (100, 1, 10, 1))],
+    [_view(0, (1, 3, 20), (100, 1, 20, 1)), _view(240, (1, 4, 20), (200, 1, 20, 1), nat.GDN_BF16)],
+    # rows apart in one period, the second view's begin behind the first's end
+    [_view(4 * 100, (1, 1, 60), (100, 1, 1, 1)), _view(240, (1, 1, 40), (100, 1, 1, 1))],
+    # interleaved closer than row by row: alternate heads, layers in front of the rows
+    [_view(0, (4, 1, 10), (100, 20, 1, 1)), _view(40, (4, 1, 10), (100, 20, 1, 1))],
+    [_view(0, (3, 1, 6), (6, 240, 1, 1)), _view(4 * 120, (3, 1, 6), (6, 240, 1, 1))],
+])
+def test_reorder_of_pools_that_are_apart(views):
+    assert _reorder_of(views, 20) == 0
+
+
+@pytest.mark.parametrize("views", [
+    # the same one twice; a row or an element further on; a part of a row; as another type
+    [_view(0, (2, 3, 4)), _view(0, (2, 3, 4))], [_view(0, (2, 3, 4)), _view(96, (2, 3, 4))],
+    [_view(0, (2, 3, 4)), _view(4, (2, 3, 4))], [_view(0, (2, 3, 4)), _view(8, (1, 1, 4), (24, 1, 1, 1))],
+    [_view(0, (2, 3, 4)), _view(0, (2, 3, 4), dtype=nat.GDN_F16)],
+    [_view(0, (2, 3, 4)), _view(4 * 24 * 20 - 4, (1, 1, 1))],
+    # one among many that are apart; rows that meet only across the period's end
+    LAYERS + [_view(4 * (132 * 4 + 131), (1, 1, 2), (9 * 132, 1, 1, 1))], LAYERS[:5] + LAYERS[4:],
+    [_view(0, (1, 1, 60), (100, 1, 1, 1)), _view(4 * 70, (1, 1, 40), (100, 1, 1, 1))],
+    [_view(0, (4, 1, 10), (100, 20, 1, 1)), _view(36, (4, 1, 10), (100, 20, 1, 1))],
+])
+def test_reorder_of_pools_that_share_elements(views):
+    assert _reorder_of(views, 20) == code("GDN_ERR_STATE")
+
+
 def test_null_blocks():
     L = nat.lib()
     null = code("GDN_ERR_NULL")
