@@ -478,7 +478,7 @@ int gdn_pool_compact(const gdn_pool_params *p, void *new_rows, int32_t *num_live
  * gdn_prefill_params; output_state may be the same memory as initial_state,
  * and state_indices must be unique where a final state is written.  No other
  * two tensors of a call may overlap (GDN_ERR_STATE where output or dx meets x
- * or doutput); in a decode step output may be x itself.  Tensors start on a
+ * or doutput); in a decode step output may be x itself, the same rows.  Tensors start on a
  * boundary of their element size.  Rows of output outside every sequence are
  * untouched, those of dx are zero.  A sequence whose state index is out of range
  * starts from zero and writes no final state.  A call takes at most 2^30

@@ -103,6 +103,20 @@ def test_convolution_refused(mode, kw, err):
     assert _check_conv(_conv(mode, **kw), mode) == code("GDN_ERR_" + err)
 
 
+@pytest.mark.parametrize("kw,err", [
+    # the same rows: every thread reads what it overwrites
+    (dict(output=far(1)), None), (dict(output=far(1), x_stride=96), None),
+    (dict(output=far(1), x_stride=100, total_tokens=1, num_seqs=1), None),
+    # a row or a channel further on, or rows at another distance
+    (dict(output=ctypes.c_void_p(far(1).value + 2)), "STATE"),
+    (dict(output=ctypes.c_void_p(far(1).value + 192)), "STATE"),
+    (dict(output=far(1), x_stride=100), "STATE"),
+    (dict(output=ctypes.c_void_p(far(1).value + 3 * 192)), None),
+    (dict(output=ctypes.c_void_p(far(1).value + 2), total_tokens=1, num_seqs=1), "STATE")])
+def test_convolution_decode_in_place(kw, err):
+    assert _check_conv(_conv(2, **kw), 2) == (code("GDN_ERR_" + err) if err else 0)
+
+
 def test_convolution_workspace():
     L = nat.lib()
     assert L.gdn_convolution_workspace_size(ctypes.byref(_conv()), 0) == 0
