@@ -139,6 +139,8 @@ int conv_shape(const gdn_convolution_params *p, int mode) {
   const int64_t ncb = (C + 63) / 64, T = p->total_tokens, N = p->num_seqs;
   if (mode == kDecode ? (C + 255) / 256 * N > kMaxGrid : ((T + 15) / 16 + N) * ncb > kMaxGrid * 4)
     return GDN_ERR_SHAPE;
+  // the sums of dweight and dbias: a workgroup per 32 columns
+  if (mode == kBackward && ((p->width + 1) * C + 31) / 32 > kMaxGrid) return GDN_ERR_SHAPE;
   return GDN_OK;
 }
 
@@ -335,6 +337,9 @@ int scan_shape(const gdn_scan_params *p, int mode) {
   }
   if (T > 0 && (walk_blocks(p) + 8) * (16 + 64) > kMaxGrid / 4) return GDN_ERR_SHAPE;
   if (T > 0 && ((T + 15) / 16 + 64) * ((scan_blocks(p) + 3) / 4) > kMaxGrid) return GDN_ERR_SHAPE;
+  // the sums of dA, dD and ddelta_bias: a workgroup per 32 columns (of fewer channels
+  // where there are tokens)
+  if (mode == kBackward && ((p->num_states + 2) * C + 31) / 32 > kMaxGrid) return GDN_ERR_SHAPE;
   const int64_t rows = (int64_t)p->groups * 2 * scan_states(p->num_states);
   if (((T + 255) / 256 * 256) * rows > kMaxGrid * 256) return GDN_ERR_SHAPE;
   return GDN_OK;
@@ -603,7 +608,7 @@ int reorder_pool(const gdn_reorder_params *p, const gdn_reorder_pool &q, Reorder
     o.align /= 2;
   int64_t unit = std::min<int64_t>(kUnitBytes / es, row);
   const int64_t beams = std::max<int64_t>(1, (int64_t)p->num_groups * p->num_beams);
-  while ((row + unit - 1) / unit * beams > kMaxGrid) unit *= 2;
+  while ((row + unit - 1) / unit * beams >= kMaxGrid) unit *= 2;  // (and one for the status)
   if (unit > (1 << 30)) return GDN_ERR_SHAPE;
   o.unit = (int32_t)unit;
   o.units = (int32_t)((row + unit - 1) / unit);

@@ -483,7 +483,8 @@ int gdn_pool_compact(const gdn_pool_params *p, void *new_rows, int32_t *num_live
  * untouched, those of dx are zero.  A sequence whose state index is out of range
  * starts from zero and writes no final state.  A call takes at most 2^30
  * sequences and (ceil(T / 16) + N) * ceil(C / 64) < 2^26 (a decode step
- * ceil(C / 256) * N < 2^24); GDN_ERR_SHAPE otherwise.
+ * ceil(C / 256) * N < 2^24; a backward pass also ceil((W + 1) C / 32) < 2^24);
+ * GDN_ERR_SHAPE otherwise.
  */
 typedef struct gdn_convolution_params {
   int64_t total_tokens;    /* T >= 0 */
@@ -570,7 +571,8 @@ int gdn_convolution_decode(const gdn_convolution_params *p, void *stream);
  * from zero and writes no final state.  The products exp(A sum d) over 256
  * consecutive tokens must stay finite (they do for A <= 0 and d >= 0).
  * channels <= 2^24, and T and the channels are limited by a grid's size (in a
- * decode step ceil(channels * ceil(N / 4) / 256) * num_seqs < 2^24);
+ * decode step ceil(channels * ceil(N / 4) / 256) * num_seqs < 2^24, in a backward
+ * pass ceil((N + 2) channels / 32) < 2^24);
  * GDN_ERR_SHAPE otherwise.
  */
 typedef struct gdn_scan_params {

@@ -206,6 +206,23 @@ def test_scan_workspace_and_chunk():
     assert _check_scan(_scan(total_tokens=0, x=None, delta=None, B=None, C=None, output=None)) == 0
 
 
+@pytest.mark.parametrize("width,channels,ok", [
+    (4, 107374176, True), (4, 107374177, False), (2, 178956960, True), (2, 178956961, False)])
+def test_convolution_backward_grid(width, channels, ok):
+    """The sums over tokens: fewer than 2^24 workgroups of 32 columns."""
+    kw = dict(width=width, channels=channels, total_tokens=0, num_seqs=0, x=None, doutput=None, dx=None)
+    assert _check_conv(_conv(1, **kw), 1) == (0 if ok else code("GDN_ERR_SHAPE"))
+    assert _check_conv(_conv(0, **dict(kw, output=None)), 0) == 0
+
+
+@pytest.mark.parametrize("states,channels,ok", [
+    (64, 8134407, True), (64, 8134408, False), (30, 2 ** 24 - 1, True), (30, 2 ** 24, False)])
+def test_scan_backward_grid_without_tokens(states, channels, ok):
+    kw = dict(num_states=states, channels=channels, groups=1, total_tokens=0)
+    assert _check_scan(_scan(1, **kw), 1) == (0 if ok else code("GDN_ERR_SHAPE"))
+    assert _check_scan(_scan(0, **kw), 0) == 0
+
+
 # ----------------------------------------------------------------------- beam
 
 def _beam(**kw):
