@@ -403,9 +403,10 @@ int scan_validate(const gdn_scan_params *p, int mode) {
   auto span = [&](const void *q, int64_t stride, int64_t row) {
     return Span(q, T, stride ? stride : row, row, xs);
   };
-  const Span in[5] = {span(p->x, p->x_stride, C), span(p->delta, p->delta_stride, C),
+  const Span in[6] = {span(p->x, p->x_stride, C), span(p->delta, p->delta_stride, C),
                       span(p->z, p->z_stride, C), span(p->B, p->b_stride, bn),
-                      span(p->C, p->c_stride, bn)};
+                      span(p->C, p->c_stride, bn),
+                      span(mode == kBackward ? p->doutput : nullptr, p->doutput_stride, C)};
   auto overlaps = [&](const void *q, int64_t row) {
     const Span o = span(q, row, row);
     for (const Span &i : in)

@@ -187,6 +187,17 @@ def test_scan_refused(mode, kw, err):
     assert _check_scan(_scan(mode, **kw), mode) == code("GDN_ERR_" + err)
 
 
+@pytest.mark.parametrize("out", ["dx", "ddelta", "dz", "dB", "dC"])
+def test_scan_gradients_over_doutput(out):
+    """Tokens of the gradient of the output are read by several workgroups."""
+    kw = dict(z=far(20), dz=far(21))
+    last = far(6).value + 2 * (1000 * 96 - 1)
+    assert _check_scan(_scan(1, **dict(kw, **{out: far(6)})), 1) == code("GDN_ERR_STATE")
+    assert _check_scan(_scan(1, **dict(kw, **{out: ctypes.c_void_p(last)})), 1) == code("GDN_ERR_STATE")
+    assert _check_scan(_scan(1, **dict(kw, **{out: ctypes.c_void_p(last + 2)})), 1) == 0
+    assert _check_scan(_scan(0, doutput=far(5)), 0) == 0  # not looked at
+
+
 def test_scan_workspace_and_chunk():
     L = nat.lib()
     p = _scan()
