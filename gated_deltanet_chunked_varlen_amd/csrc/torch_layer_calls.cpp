@@ -239,6 +239,7 @@ PyObject *conv_backward(PyObject *const *a) {
   const Tensor dx = r.buffer("dx", a[9], r.x.sizes(), r.x.scalar_type());
   const Tensor dw = r.buffer("dweight", a[10], r.weight.sizes(), at::kFloat);
   Tensor db, di;
+  BAD_IF(!r.bias && a[11] != Py_None, "dbias needs a bias");
   if (r.bias) db = r.buffer("dbias", a[11], r.bias->sizes(), at::kFloat);
   if (with_init) di = r.buffer("dinitial_state", a[12], r.rows(r.N), at::kFloat);
   r.p.dx = dx.data_ptr();

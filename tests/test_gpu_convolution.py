@@ -278,3 +278,13 @@ def test_refusals_on_the_device():
     for call in bad:
         with pytest.raises(ValueError):
             call()
+
+
+def test_a_gradient_buffer_without_its_input():
+    """A buffer that no gradient would be written to is refused, not dropped."""
+    d = L.conv_make(19, [8], 16, 4, F32)
+    db = torch.full((16,), 3.0, device="cuda")
+    with pytest.raises(ValueError, match="dbias"):
+        short_convolution_backward(d["dy"], d["x"], d["w"], dbias=db)
+    assert (db == 3).all()
+    assert short_convolution_backward(d["dy"], d["x"], d["w"], d["bias"], dbias=db)[2] is db
