@@ -83,6 +83,7 @@ struct ScanArgs {
   int32_t nseg;   // segments of the tokens that workgroups walk along (k12_scan_walk.hip)
   float *bc;      // [T][G][2][NS] B and C in fp32, padded with zeros
   float *chunk;   // [ntiles][N][C] first each tile's own state, then the state before it
+                  // (the walk: that alone, where the caller wants it)
   float *span;    // [ntiles][C] sum of the step sizes over which a state crosses the tile
   float *start;   // [ntiles][N][C] initial state of the last sequence that starts in the tile
   int32_t *flag;  // [ntiles] a sequence starts in the tile

@@ -352,6 +352,8 @@ struct ScanPlan {
   int walk;  // segments of the walk, 0: passes over tiles
 };
 
+// The workspace is that of the passes over tiles, whichever form the addresses lead
+// to: its size does not depend on them.  The walk uses the sequence starts alone.
 ScanPlan scan_plan(const gdn_scan_params *p, int mode) {
   ScanPlan S{};
   const bool back = mode == kBackward;
@@ -519,6 +521,7 @@ int scan_run(const gdn_scan_params *p, int mode, hipStream_t s) {
     a.pbc = (float *)(ws + S.pbc);
   }
   if (S.walk) {
+    a.chunk = p->chunk_states;  // no states before tiles that nobody asked for
     a.ncb = (int32_t)walk_blocks(p);
     a.nseg = S.walk;
     if (e == hipSuccess) e = launch_scan_walk(a, s);

@@ -624,7 +624,9 @@ typedef struct gdn_scan_params {
 int64_t gdn_scan_chunk(const gdn_scan_params *p);
 
 /* Bytes of workspace gdn_scan() (backward == 0) or gdn_scan_backward() needs;
- * only the shape fields and whether chunk_states is given are read. */
+ * only the shape fields and whether chunk_states is given are read.  Which form a
+ * forward pass takes depends on addresses too: the size is that of the form that needs
+ * more, and a call may use little of it. */
 size_t gdn_scan_workspace_size(const gdn_scan_params *p, int32_t backward);
 
 /* The host-side checks of gdn_scan() (mode 0), its backward pass (1) and its

@@ -409,6 +409,26 @@ def test_sequence_bounds_that_are_wrong():
 # where there are few channels): the same as above, over segments and over sequences
 # that end where a run of 16 tokens or a step of eight runs does.
 
+@pytest.mark.parametrize("N,dtype", [(8, F32), (16, BF16)])
+def test_walks_leave_the_workspace_alone(N, dtype):
+    """States before tiles are written for a caller who wants them only."""
+    lens = [130, 20, 300, 0, 64, 1]
+    d = L.scan_make(46, lens, 40, N, 1, dtype, True)
+    ws = torch.full((1 << 24,), 7, dtype=torch.uint8, device="cuda")
+    out, kept = selective_scan(*_args(d), **_layer(d, True), cu_seqlens=d["cu"], workspace=ws,
+                               return_chunk_states=True)
+    again = selective_scan(*_args(d), **_layer(d, True), cu_seqlens=d["cu"], workspace=ws)
+    assert L.same(out, again) and (ws == 7).all()
+    want = _want(_drop(d, "h0"), lens, True)
+    L.check("out", out, want.out, dtype)
+    tile = (sum(lens) + kept.shape[0] - 1) // kept.shape[0]
+    tile = 1 << (tile - 1).bit_length()
+    for k in range(1, kept.shape[0]):  # in the middle of a sequence
+        i = int(np.searchsorted(np.cumsum(lens), tile * k, side="right"))
+        if tile * k > sum(lens[:i]):
+            L.check("tile %d" % k, kept[k].t(), want.h[tile * k - 1, i], F32)
+
+
 @pytest.mark.parametrize("N", [8, 16])
 @pytest.mark.parametrize("lens", [[126, 200, 128, 90, 16, 0, 60], [7] * 70])
 def test_walks_leave_rows_outside_alone(lens, N):
