@@ -415,7 +415,8 @@ __global__ void __launch_bounds__(64 * run_waves(S), S <= 8 ? 2 : 1)
           cr[s] = reset ? hj[j].e[s] : fmaf(ej[j].e[s], cr[s], hj[j].e[s]);
       }
     }
-    if (a.chunk && t0 % a.L == 0 && t0 > from && t0 < to && ok) {
+    // (0 where no earlier token of this segment is a sequence's)
+    if (a.chunk && t0 % a.L == 0 && t0 >= from && t0 < to && ok) {
       float *row = a.chunk + (int64_t)(t0 / a.L) * NS * a.C + c;
 #pragma unroll
       for (int s = 0; s < S; ++s) row[(int64_t)(q * S + s) * a.C] = cr[s];

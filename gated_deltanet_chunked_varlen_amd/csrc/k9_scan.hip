@@ -292,7 +292,12 @@ __global__ void __launch_bounds__(kThreads, scan_waves(NS)) scan_tile_kernel(Sca
       if (OUT && a.fin.p && ch.ok && (m.last >> u & 1)) final_state<NS>(a, m.seq_at(u), c, lds, h);
     }
   }
-  if (OUT || !ch.ok) return;
+  if (!ch.ok) return;
+  if (OUT) {  // of a single tile the state before it, which the caller may keep
+    if (a.ntiles == 1 && a.chunk)
+      for (int n = 0; n < a.N; ++n) *lane_of<float>(a.chunk, row + (int64_t)n * a.C, c4) = 0.f;
+    return;
+  }
 #pragma unroll
   for (int n = 0; n < NS; ++n)
     if (n < a.N) *lane_of<float>(a.chunk, row + (int64_t)n * a.C, c4) = h[n];

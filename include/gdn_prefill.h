@@ -603,7 +603,8 @@ typedef struct gdn_scan_params {
   int32_t state_indices_type;
   int64_t pool_size;
   /* fp32 [ceil(T / gdn_scan_chunk()), N, channels] or NULL.  gdn_scan() writes
-   * the states before every gdn_scan_chunk() tokens; gdn_scan_backward() reads
+   * the states before every gdn_scan_chunk() tokens (what a row holds whose first
+   * token no sequence reaches from before is not read); gdn_scan_backward() reads
    * them, or forms them in its workspace with one more pass when NULL. */
   float *chunk_states;
   /* gradients, gdn_scan_backward() only */

@@ -541,6 +541,25 @@ def test_walks_over_strided_tokens(N, G, lens):
         L.check("final %d" % i, final[i], want.final[i], F32)
 
 
+@pytest.mark.parametrize("lens,N,tail", [([300, 0, 200, 12], 8, 60), ([300, 0, 200, 12], 5, 60),
+                                          ([3, 9], 8, 2), ([3, 9], 5, 2), ([40] * 70, 16, 9)])
+def test_all_chunk_states_are_written(lens, N, tail):
+    """Also those of tiles that begin with a sequence or outside of any: zeros, not
+    what the memory held."""
+    d = L.scan_make(47, lens, 6, N, 1, F32, True, tail=tail)
+    cu = d["cu"] + tail // 2
+    rows = (sum(lens) + tail + 15) // 16
+    for fill in (float("nan"), 1.0):
+        old = torch.full((rows, N, 6), fill, device="cuda")
+        del old  # (the next tensor of this size takes its memory)
+        kept = selective_scan(*_args(d), **_layer(d, True), initial_state=d["h0"], cu_seqlens=cu,
+                              return_chunk_states=True)[1]
+        assert kept.shape[0] == rows and not kept[0].any()
+        if fill != fill:
+            first = kept
+    assert L.same(kept, first) and torch.isfinite(kept).all()
+
+
 def test_no_tokens():
     d = L.scan_make(36, [0, 0], 8, 4)
     status = torch.full((1,), 9, dtype=torch.int32, device="cuda")
