@@ -54,12 +54,10 @@ struct ConvArgs {
   const float *dfin;
   void *dx;
   float *dw, *db, *dinit;
-  float *part;  // [parts][C][W + 1] sums of one run of tokens
-  int32_t parts;
+  float *part;  // [runs][W + 1][C] sums of one run of tokens
   // cut: runs of `run` tokens by blocks of 64 lanes x vec channels
   int32_t run, runs, ncb, vec;
   int32_t fvec;  // fp32 rows of channels (dfin, dinit, part) are aligned groups of 16 bytes
-  int32_t num_cus;
 };
 
 hipError_t launch_conv_forward(const ConvArgs &a, hipStream_t s);

@@ -254,10 +254,9 @@ int conv_run(const gdn_convolution_params *p, int mode, hipStream_t s) {
   a.db = p->dbias;
   a.dinit = p->dinitial_state;
   a.run = L.run;
-  a.runs = a.parts = L.runs;
+  a.runs = L.runs;
   a.ncb = L.ncb;
   a.vec = L.vec;
-  a.num_cus = num_cus;
   a.fvec = C % 4 == 0 && aligned(p->dfinal_state, 16) && aligned(p->dinitial_state, 16);
   if (mode == kBackward) a.part = (float *)(ws + L.part);
   hipError_t e = hipSuccess;

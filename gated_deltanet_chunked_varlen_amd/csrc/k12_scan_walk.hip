@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(64 * run_waves(S), S <= 8 ? 2 : 1)
     scan_walk_kernel(ScanArgs a) {
   constexpr int TW = run_tokens(S), WAVES = run_waves(S), NS = kLanes * S, TQ = TW / kLanes;
   constexpr int NV = TW * 2 * NS / 8 / 64 > 0 ? TW * 2 * NS / 8 / 64 : 1;  // vectors of B and C
-  constexpr unsigned kAll = TW == 32 ? ~0u : (1u << (TW & 31)) - 1;
+  constexpr unsigned kAll = (1u << TW) - 1;
   __shared__ float s_bc[WAVES][TW][2][NS];
   __shared__ Vec<float, S> s_state[2][WAVES][64], s_decay[2][WAVES][64], s_carry[2][64];
   __shared__ int s_reset[2][WAVES];

@@ -474,7 +474,7 @@ template <int W> __global__ void __launch_bounds__(kThreads) conv_sums_kernel(Co
   float sum = 0.f;
   if (id < n) {
 #pragma unroll 4
-    for (int r = part; r < a.parts; r += kParts) sum += a.part[r * n + id];
+    for (int r = part; r < a.runs; r += kParts) sum += a.part[r * n + id];
   }
   sums[part][col] = sum;
   __syncthreads();

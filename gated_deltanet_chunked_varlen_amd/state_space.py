@@ -66,8 +66,9 @@ def selective_scan(x, delta, A, B, C, D=None, z=None, delta_bias=None, delta_sof
     state dtype, rows may be strided; with ``state_indices`` [N] sequence i
     starts from ``initial_state`` row state_indices[i] and leaves its final
     state in that row of ``output_state``, which may be ``initial_state`` itself;
-    rows must then be unique.  h is float32 throughout.  No other two tensors of
-    a call may overlap.
+    rows must then be unique.  h is float32 throughout.  The products exp(A sum d)
+    over 256 consecutive tokens must stay finite: they do for A <= 0 and d >= 0.
+    No other two tensors of a call may overlap.
 
     ``workspace`` (optional uint8 device tensor) is used, if it is large
     enough, instead of the one that is kept for the current stream.  A call
