@@ -98,12 +98,14 @@ struct Channel {
 
 // One token's step of all states of a lane's channel; with OUT the sum of
 // C h is added to y.  Not FULL: the states from N on, whose coefficients are 0, are
-// kept at 0 also under an infinite step or input, as they are part of that sum.
+// kept at 0 also under an infinite step or input, as they are part of that sum (4096
+// tokens of 4096 channels with 24 states: 353 us, 346 if they are not).
 template <int NS, bool OUT, bool FULL = true>
 __device__ __forceinline__ void token_step(const float *bc, float dt, float u,
                                            const float (&A2)[NS], float (&h)[NS], float &y,
                                            int N = NS) {
   constexpr int Q = NS < 16 ? NS : 16;
+  constexpr int kSure = FULL ? NS : NS > 8 ? NS / 2 : 1;  // states that there are
   typedef float row __attribute__((ext_vector_type(Q)));
   float s[2] = {y, 0.f};
 #pragma unroll
@@ -113,7 +115,7 @@ __device__ __forceinline__ void token_step(const float *bc, float dt, float u,
 #pragma unroll
     for (int n = 0; n < Q; ++n) {
       const float e = __builtin_amdgcn_exp2f(dt * A2[k + n]);
-      h[k + n] = FULL || k + n < N ? fmaf(e, h[k + n], u * b[n]) : 0.f;
+      h[k + n] = k + n < kSure || k + n < N ? fmaf(e, h[k + n], u * b[n]) : 0.f;
       if (OUT) s[n & 1] = fmaf(c[n], h[k + n], s[n & 1]);
     }
   }
