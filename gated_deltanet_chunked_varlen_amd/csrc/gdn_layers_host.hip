@@ -291,10 +291,15 @@ int64_t scan_tile(const gdn_scan_params *p, bool backward) {
 }
 
 // The forward pass that walks along the tokens, 16 channels a workgroup, and how
-// many segments of them: a walk takes 8 to 9.5 us per 256 tokens and 16 states however
-// many workgroups there are (up to one per CU; 7.6 with 32 states), the passes over
-// tiles some 35 us and 12 per 256 tokens of 4096 channels (16 384 tokens of 4096
-// channels: 547 us and 783; 515 of 2048: 23 and 47).
+// many segments of them: a walk takes 7.4 to 9 us per 256 tokens and 16 states however
+// many workgroups there are (up to one per CU; 7.2 with 32 states, 12 with 8), the passes
+// over tiles some 35 us and 12 per 256 tokens of 4096 channels.  Both measured, one
+// sequence in bf16, walk and tiles (us):
+//   16 states  16 384 x 4096: 487, 803    256 x 4096: 14, 43    2816 x 2048: 85, 114
+//              1024 x 1024: 35, 51        1024 x 256: 34, 48
+//   32 and 64 states  4096 x 4096: 233, 347 and 606, 1069    8 states  4096 x 2048: 100, 88
+// The rule counts a walk at its length without segments: how even these are is not
+// known here.
 int64_t walk_blocks(const gdn_scan_params *p) {
   return (int64_t)p->groups * ((p->channels / p->groups + 15) / 16);
 }

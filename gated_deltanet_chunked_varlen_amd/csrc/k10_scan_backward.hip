@@ -15,10 +15,13 @@
 // values at each step, stored, and added by a last kernel, in a fixed order.
 //
 // Bounded by the vector ALU (half of the time) and by the waits of two waves per
-// SIMD: 4096 tokens of 4096 channels with 16 states in bf16 take 467 us, of these
-// some 290 the loop over the states, 155 raw values and results, 45 the states before
-// the blocks; the gradients before the tiles 73 and the chain 14.  With the gradients
-// behind a block in LDS of their own, one workgroup less per CU, it was 700.
+// SIMD: 4096 tokens of 4096 channels with 16 states in bf16 take 457 us, in parts
+// that overlap some 290 the loop over the states, 155 raw values and results, 45 the
+// states before the blocks; the gradients before the tiles 71 and the chain 14.  With the gradients
+// behind a block in LDS of their own, one workgroup less per CU, it was 700.  With 64
+// states a tile has 16 tokens, so that the states and sums of tiles are most of the
+// traffic, and a few registers are spilled: the whole pass takes 1.93 ms there, 0.50
+// with 16 states.
 
 #include "gdn_scan.h"
 

@@ -16,16 +16,18 @@
 // (in fp64: scores of different beams are compared) and takes the M best of the
 // parts' candidates in the same way.
 // Bounded by the vector ALU and HBM for a batch (64 groups of 8 beams, 131 072 tokens
-// in bf16: rows 45 us, 3.0 TB/s, 102 when all keys were ranked; the groups 11, 25
-// before), by latency for one request (6 and 8.4 us).  4096 logits a workgroup take
-// 57 us and 16 384 63, where 8192 took 49.
+// in bf16: rows 49 us, 2.7 TB/s, 102 when all keys were ranked; the groups 11, 25
+// before), by latency for one request (6 and 8.9 us).  4096 logits a workgroup take
+// 57 us and 16 384 63, where 8192 took 49.  With 99.9 % of the tokens masked most parts
+// have no finite bound, and the batch takes 128 us instead of 57.
 //
 // Reordering.  Within a group the first child of a parent keeps its row; the
 // other children take the rows of beams without a child, in order, and only
 // those are copied.  A row is never both source and destination, so nothing has
 // to be set aside: one kernel, in which every workgroup works out its group's
 // plan from the parents (a wave, by ballots).  Bounded by HBM: 16 groups of 8 beams,
-// rows of 1 MB, 17 us for 92 MB.
+// rows of 1 MB, 20 us for 92 MB; 32 pools of two kinds in one call 4.7 TB/s.  Rows that
+// are no whole groups of 16 bytes move an element a lane: 1.1 TB/s in bf16.
 #include "gdn_layers.h"
 
 #include <algorithm>

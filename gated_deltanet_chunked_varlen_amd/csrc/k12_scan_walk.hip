@@ -11,13 +11,13 @@
 //   3. every wave: the true states, from the decays it kept, and the outputs
 // so that a token takes one exponential per state, and no second kernel.  A lane
 // holds S states of a channel, four lanes a channel.  One prompt of 16384 tokens of
-// 4096 channels with 16 states takes 547 us, the passes over tiles 783; 4096 such
-// tokens of a training step 145 and 230.
+// 4096 channels with 16 states takes 487 us, the passes over tiles 803; 4096 such
+// tokens 122 and 237.
 //
 // Bounded by the vector ALU and by what two waves per SIMD leave idle: some 45 cycles
 // of a SIMD per 64 states (the exponential 8, its argument, the input's product twice,
 // three fused products; the rest is the outputs' sums over four lanes and what a token
-// takes for all of its states), which are 57% of the time.
+// takes for all of its states); it is busy for 74% of the time.
 //
 // The tokens can be cut into segments that workgroups of their own walk along:
 // a segment begins with the first sequence that starts at or behind its place.
@@ -41,7 +41,7 @@ namespace {
 constexpr int kLanes = 4;      // of a channel
 constexpr int kChannels = 16;  // of a workgroup
 // Tokens of which the coefficients are read together, those of the next ones while
-// these are worked on: 547 us for 16384 x 4096 in bf16, 572 if the compiler orders
+// these are worked on: 16384 x 4096 in bf16 took 4 % longer where the compiler ordered
 // the reads of four tokens.  All of a run's at once would take the registers that the
 // decays are in.
 constexpr int kStates = 4, kOutputs = 2;  // of the first sweep, of the second
@@ -49,8 +49,8 @@ constexpr int kCompose = 4;  // waves' states read from LDS together
 constexpr int kLoadsDone = 0x0F70;  // s_waitcnt vmcnt(0), nothing else
 
 // Tokens of a run and waves of a workgroup by the states of a lane: S TW decays
-// are held in registers (16 tokens of 8 states do not fit: 273 us for 4096 tokens of
-// 4096 channels with 32 states, 245 with 8 tokens), and the waves' states in LDS.
+// are held in registers (16 tokens of 8 states do not fit: 4096 tokens of 4096 channels
+// with 32 states took 11 % longer than with 8, 233 us), and the waves' states in LDS.
 constexpr int run_tokens(int s) { return s <= 4 ? 16 : 8; }
 constexpr int run_waves(int s) { return s <= 8 ? 8 : 4; }
 

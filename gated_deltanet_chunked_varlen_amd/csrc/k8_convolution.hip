@@ -9,8 +9,10 @@
 // Bounded by HBM: 2 W + a few operations per element of x.  A wave takes a run of
 // tokens of 64 x V channels (V: 16 bytes of x) and slides the window along it in
 // registers, so that each row is read once but for the W - 1 rows before a run
-// (23 060 tokens of 8192 channels in bf16: 145 us, 5.2 TB/s, what a large copy
-// reaches; their gradients, 310 us, 3.7 TB/s; a decode step of 256 sequences 9 us).
+// (23 060 tokens of 8192 channels in bf16: 141 us, 5.4 TB/s, what a large copy
+// reaches; their gradients, 300 us, 3.8 TB/s, with fp32 weights at three waves a SIMD,
+// and a bound in most of its runs, as in 200 short sequences, 418 where 8 sequences
+// took 281; a decode step of 256 sequences 9 us).
 //
 // Forward: tokens whose window lies inside their sequence need no state, and a
 // run writes only those.  The first W - 1 tokens of a sequence and its final
