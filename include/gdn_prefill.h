@@ -570,6 +570,8 @@ int gdn_convolution_decode(const gdn_convolution_params *p, void *stream);
  * is its initial state.  A sequence whose state index is out of range starts
  * from zero and writes no final state.  The products exp(A sum d) over 256
  * consecutive tokens must stay finite (they do for A <= 0 and d >= 0).
+ * An infinite state whose decay underflows fp32 within one token (d A below -87) is NaN
+ * or infinite from there on.
  * channels <= 2^24, and T and the channels are limited by a grid's size (in a
  * decode step ceil(channels * ceil(N / 4) / 256) * num_seqs < 2^24, in a backward
  * pass ceil((N + 2) channels / 32) < 2^24);
