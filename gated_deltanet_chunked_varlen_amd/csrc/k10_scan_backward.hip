@@ -17,11 +17,11 @@
 // Bounded by the vector ALU (half of the time) and by the waits of two waves per
 // SIMD: 4096 tokens of 4096 channels with 16 states in bf16 take 457 us, in parts
 // that overlap some 290 the loop over the states, 155 raw values and results, 45 the
-// states before the blocks; the gradients before the tiles 71 and the chain 14.  With the gradients
-// behind a block in LDS of their own, one workgroup less per CU, it was 700.  With 64
-// states a tile has 16 tokens, so that the states and sums of tiles are most of the
-// traffic, and a few registers are spilled: the whole pass takes 1.93 ms there, 0.50
-// with 16 states.
+// states before the blocks; the gradients before the tiles 71 and the chain 14.  With
+// the gradients behind a block in LDS of their own, one workgroup less per CU, it was
+// 700.  With 64 states a tile has 16 tokens, so that the states and sums of tiles are
+// most of the traffic, and a few registers are spilled: the whole pass takes 1.93 ms
+// there, 0.50 with 16 states.
 
 #include "gdn_scan.h"
 
@@ -386,7 +386,8 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs a) 
         const float x = to_f32(rx.v[j]);
         float ddt = fmaf(du[i], x, kLn2 * dd[i]);
         if (a.softplus) ddt *= sigmoid(to_f32(rd.v[j]) + bias);
-        *(Tx *)(orow[0] + at + cx) = from_f32<Tx>(in ? fmaf(du[i], dt[i], skip_of(a, D, y[i])) : 0.f);
+        const float dx = fmaf(du[i], dt[i], skip_of(a, D, y[i]));
+        *(Tx *)(orow[0] + at + cx) = from_f32<Tx>(in ? dx : 0.f);
         *(Tx *)(orow[1] + at + cx) = from_f32<Tx>(in ? ddt : 0.f);
         if (a.z) {
           const float z = to_f32(rz.v[j]), sg = sigmoid(z);

@@ -297,13 +297,50 @@ __device__ __forceinline__ double value_of(u64 o) {
 }
 
 constexpr int kTake = 8;  // candidates per thread and round
-constexpr int kScan = 16;  // logits per thread and round of a look at whole rows
+constexpr int kScan = 8;  // vectors per thread and round of a look at whole rows
 
-__device__ __forceinline__ float logit_of(const BeamArgs &a, int64_t at) {
-  const float v = a.dtype == GDN_F32    ? ((const float *)a.logits)[at]
-                  : a.dtype == GDN_BF16 ? to_f32(((const bf16 *)a.logits)[at])
-                                        : to_f32(((const f16 *)a.logits)[at]);
-  return fmaxf(v, -kInf);
+// The first of 2^32 keys for which a condition holds that holds for all behind it too
+// (of those from lo on, n of them; lo + n: none), by the whole wave.
+template <typename F>
+__device__ __forceinline__ unsigned first_key(unsigned lo, unsigned n, F holds) {
+  const int lane = threadIdx.x & 63;
+  while (n > 0) {
+    const unsigned step = (n + 63) / 64;
+    const int p = __builtin_popcountll(
+        __ballot((u64)lane * step < n && !holds(lo + (unsigned)lane * step)));
+    if (p == 0) break;
+    const unsigned to = (unsigned)(p - 1) * step + 1;
+    lo += to;
+    n = min(step - 1, n - to);
+  }
+  return lo;
+}
+
+// Which logits of a round, from token `from` on, are in [low, high]: bit s V + e stands
+// for token from + (256 s + thread) V + e.
+template <typename T, int V>
+__device__ __forceinline__ u64 matches_of(const BeamArgs &a, int64_t row, int from, float low,
+                                          float high) {
+  const T *p = (const T *)a.logits + row;
+  const int first = from + (int)threadIdx.x * V;
+  Vec<T, V> raw[kScan];
+#pragma unroll
+  for (int s = 0; s < kScan; ++s) {
+    const int at = first + s * kThreads * V;
+    raw[s] = load_vec<T, V>(p + (at < a.V ? at : 0));
+  }
+  u64 found = 0;
+#pragma unroll
+  for (int s = 0; s < kScan; ++s) {
+    float x[V];
+    widen(raw[s], x);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const float v = fmaxf(x[e], -kInf);
+      if (first + s * kThreads * V < a.V && v >= low && v <= high) found |= 1ull << (s * V + e);
+    }
+  }
+  return found;
 }
 
 // One group.  Candidates come in rounds of kTake a thread; those of a round that
@@ -314,7 +351,8 @@ __device__ __forceinline__ float logit_of(const BeamArgs &a, int64_t at) {
 // 64 bits do not tell unequal logits' scores apart, or infinite, a token that is no
 // candidate can have the last place's score and stand before it.  Such scores carry
 // a mark, and if the last place's has it, the places of its score are filled again
-// from whole rows.
+// from whole rows (64 groups of 8 beams of 131 072 tokens, one candidate of logit 0: 75
+// us, 56 for another; 237 when every logit's score was formed).
 template <int M> __global__ void __launch_bounds__(kThreads) beam_group_kernel(BeamArgs a) {
   constexpr int kWaves = kThreads / 64;
   __shared__ union {
@@ -326,6 +364,8 @@ template <int M> __global__ void __launch_bounds__(kThreads) beam_group_kernel(B
   __shared__ unsigned s_low[kWaves];
   __shared__ float s_top[kMaxM], s_score[kMaxM];
   __shared__ int s_count[kWaves];
+  __shared__ unsigned s_any;
+  __shared__ u64 s_beams;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, b = blockIdx.x;
   const int per = a.parts * a.M, n = a.K * per;
   const int64_t first = (int64_t)b * a.K * a.parts;
@@ -394,7 +434,8 @@ template <int M> __global__ void __launch_bounds__(kThreads) beam_group_kernel(B
       if (at[e] < 0) continue;
       const int k = i / per;
       const u64 flat = (u64)k * (u64)a.V + (u64)at[e];
-      c[e] = Score{order_of(score_at(k, logit[e])), ~(flat << 1 | (may_tie(k, logit[e]) ? 1u : 0u))};
+      const u64 mark = may_tie(k, logit[e]) ? 1 : 0;
+      c[e] = Score{order_of(score_at(k, logit[e])), ~(flat << 1 | mark)};
       any |= c[e] > last;
       mine = c[e].value > mine ? c[e].value : mine;
     }
@@ -445,32 +486,70 @@ template <int M> __global__ void __launch_bounds__(kThreads) beam_group_kernel(B
   }
   const Score last = s_best[a.M - 1];
   if (!(last.place & 1)) {
+    // Of the beams that have a candidate in one of these places (a part that leaves out
+    // a token of this score leaves M candidates, the last of this score too), up to the
+    // last place's token.
+    const int V = !a.vec ? 1 : a.dtype == GDN_F32 ? 4 : 8;
+    const u64 behind = (~last.place >> 1) + 1;
+    if (tid == 0) {
+      s_beams = 0;
+      s_any = 0;
+    }
+    __syncthreads();
     int have = 0;  // places that are filled: better scores, then the tokens found
     for (int i = 0; i < a.M; ++i) have += s_best[i].value > last.value;
+    if (tid >= have && tid < a.M)
+      atomicOr(&s_beams, 1ull << (int)((~s_best[tid].place >> 1) / (u64)a.V));
     __syncthreads();
     for (int k = 0; k < a.K && have < a.M; ++k) {
-      if (order_of(score_at(k, s_top[k])) < last.value) continue;
+      if (!(s_beams >> k & 1)) continue;
       const int64_t row = ((int64_t)b * a.K + k) * a.stride;
-      for (int from = 0; from < a.V && have < a.M; from += kScan * kThreads) {
-        unsigned found = 0;
-#pragma unroll 4
-        for (int e = 0; e < kScan; ++e) {
-          const int t = from + tid * kScan + e;
-          if (t < a.V && order_of(score_at(k, logit_of(a, row + t))) == last.value) found |= 1u << e;
-        }
-        const int own = __builtin_popcount(found), sum = wave_prefix_sum_i(own);
-        if (lane == 63) s_count[wave] = sum;
+      const u64 flat = (u64)k * (u64)a.V;
+      const int end = (int)min((u64)a.V, behind - flat);
+      // a beam's scores rise with its logits: those of this score are a range
+      constexpr unsigned kLow = 0x007FFFFFu, kHigh = 0xFF800000u;  // keys of -inf and +inf
+      auto score_of = [&](unsigned key) { return order_of(score_at(k, key_value((u64)key << 32))); };
+      const unsigned low_key = first_key(kLow, kHigh - kLow + 1, [&](unsigned key) {
+        return score_of(key) >= last.value;
+      });
+      const unsigned next_key = first_key(low_key, kHigh - low_key + 1, [&](unsigned key) {
+        return score_of(key) > last.value;
+      });
+      if (next_key <= low_key) continue;
+      const float low = key_value((u64)low_key << 32), high = key_value((u64)(next_key - 1) << 32);
+      for (int from = 0; from < end && have < a.M; from += kScan * kThreads * V) {
+        const u64 found =
+            a.dtype == GDN_F32    ? a.vec ? matches_of<float, 4>(a, row, from, low, high)
+                                          : matches_of<float, 1>(a, row, from, low, high)
+            : a.dtype == GDN_BF16 ? a.vec ? matches_of<bf16, 8>(a, row, from, low, high)
+                                          : matches_of<bf16, 1>(a, row, from, low, high)
+                                  : a.vec ? matches_of<f16, 8>(a, row, from, low, high)
+                                          : matches_of<f16, 1>(a, row, from, low, high);
+        if (!__syncthreads_or(found != 0)) continue;
+        const u64 vector = (1ull << V) - 1;
+        unsigned mine = 0;
+        for (int s = 0; s < kScan; ++s) mine |= (found >> (s * V) & vector) != 0 ? 1u << s : 0u;
+        if (mine != 0) atomicOr(&s_any, mine);
         __syncthreads();
-        int at0 = have + sum - own;
+        for (unsigned any = s_any; any != 0 && have < a.M; any &= any - 1) {
+          const int s = __builtin_ctz(any);
+          u64 here = found >> (s * V) & vector;
+          const int own = __builtin_popcountll(here), sum = wave_prefix_sum_i(own);
+          if (lane == 63) s_count[wave] = sum;
+          __syncthreads();
+          int place = have + sum - own;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-          if (w < wave) at0 += s_count[w];
-          have += s_count[w];
+          for (int w = 0; w < kWaves; ++w) {
+            if (w < wave) place += s_count[w];
+            have += s_count[w];
+          }
+          for (; here != 0 && place < a.M; here &= here - 1, ++place) {
+            const int t = from + (s * kThreads + tid) * V + __builtin_ctzll(here);
+            s_best[place] = Score{last.value, ~((flat + (u64)t) << 1)};
+          }
+          __syncthreads();
         }
-        for (; found != 0 && at0 < a.M; found &= found - 1, ++at0)
-          s_best[at0] = Score{last.value, ~(((u64)k * (u64)a.V +
-                                             (u64)(from + tid * kScan + __builtin_ctz(found))) << 1)};
-        __syncthreads();
+        if (tid == 0) s_any = 0;  // (set again behind the next round's barrier)
       }
     }
   }

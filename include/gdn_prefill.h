@@ -563,8 +563,8 @@ int gdn_convolution_decode(const gdn_convolution_params *p, void *stream);
  * pool_size and status are those of gdn_prefill_params; output_state may be the
  * same memory as initial_state, and state_indices must be unique where a final
  * state is written.  No other two tensors of a call may overlap (GDN_ERR_STATE
- * where output or a token's gradient meets x, delta, z, B, C or doutput).  Tensors start on a boundary of
- * their element size, the workspace on a 256-byte boundary.  Calls that overlap
+ * where output or a token's gradient meets x, delta, z, B, C or doutput).  Tensors
+ * start on a boundary of their element size, the workspace on a 256-byte boundary.  Calls that overlap
  * in time need workspaces of their own.  Rows of output outside every sequence
  * are untouched, those of gradients are zero.  An empty sequence's final state
  * is its initial state.  A sequence whose state index is out of range starts

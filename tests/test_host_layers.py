@@ -320,7 +320,8 @@ LAYERS = [_view(4 * 132 * i, (1, 4, 33), (9 * 132, 1, 33, 1)) for i in range(9)]
 
 @pytest.mark.parametrize("views", [
     # one after the other; the layers of one [rows, layers, ...] buffer, in any order
-    [_view(0, (2, 3, 4)), _view(4 * 24 * 20, (2, 3, 4))], LAYERS, LAYERS[::-1], LAYERS + [_view(4 * 9 * 132 * 20, (5, 1, 1))],
+    [_view(0, (2, 3, 4)), _view(4 * 24 * 20, (2, 3, 4))], LAYERS, LAYERS[::-1],
+    LAYERS + [_view(4 * 9 * 132 * 20, (5, 1, 1))],
     # two kinds of states in one buffer of 100 elements a row
     [_view(0, (1, 3, 20), (100, 1, 20, 1)), _view(240, (1, 4, 10), (100, 1, 10, 1))],
     [_view(0, (1, 3, 20), (100, 1, 20, 1)), _view(240, (1, 4, 20), (200, 1, 20, 1), nat.GDN_BF16)],
@@ -337,7 +338,8 @@ def test_reorder_of_pools_that_are_apart(views):
 @pytest.mark.parametrize("views", [
     # the same one twice; a row or an element further on; a part of a row; as another type
     [_view(0, (2, 3, 4)), _view(0, (2, 3, 4))], [_view(0, (2, 3, 4)), _view(96, (2, 3, 4))],
-    [_view(0, (2, 3, 4)), _view(4, (2, 3, 4))], [_view(0, (2, 3, 4)), _view(8, (1, 1, 4), (24, 1, 1, 1))],
+    [_view(0, (2, 3, 4)), _view(4, (2, 3, 4))],
+    [_view(0, (2, 3, 4)), _view(8, (1, 1, 4), (24, 1, 1, 1))],
     [_view(0, (2, 3, 4)), _view(0, (2, 3, 4), dtype=nat.GDN_F16)],
     [_view(0, (2, 3, 4)), _view(4 * 24 * 20 - 4, (1, 1, 1))],
     # one among many that are apart; rows that meet only across the period's end
