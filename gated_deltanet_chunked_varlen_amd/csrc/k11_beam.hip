@@ -508,7 +508,9 @@ template <int M> __global__ void __launch_bounds__(kThreads) beam_group_kernel(B
       const int end = (int)min((u64)a.V, behind - flat);
       // a beam's scores rise with its logits: those of this score are a range
       constexpr unsigned kLow = 0x007FFFFFu, kHigh = 0xFF800000u;  // keys of -inf and +inf
-      auto score_of = [&](unsigned key) { return order_of(score_at(k, key_value((u64)key << 32))); };
+      auto score_of = [&](unsigned key) {
+        return order_of(score_at(k, key_value((u64)key << 32)));
+      };
       const unsigned low_key = first_key(kLow, kHigh - kLow + 1, [&](unsigned key) {
         return score_of(key) >= last.value;
       });
